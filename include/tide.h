@@ -467,6 +467,114 @@ tide_status tide_rs_two_phase_noalloc(const void *h_plan, const void *d_plan,
                                       int64_t tile_begin, int64_t tile_count,
                                       int32_t max_workgroups, tide_stream_t stream);
 
+/* Activations kept in 8 bits for the backward pass.
+ *
+ * A training step that gathers, uses and frees a layer's weights also keeps
+ * each product's input (and an activation function's) until the backward
+ * pass; in 8 bits they take half the memory.  A checkpoint of a [rows, cols]
+ * bf16 matrix is one piece of caller memory (16-byte aligned; e.g. part of a
+ * vacated gathered buffer, as with Slot-Reuse [Abstract; Design]):
+ *   rows * pitch e4m3 values, row-major, pitch = cols rounded up to 32 (the
+ *   padding columns are written as 0), then
+ *   rows * pitch / 32 scale bytes, one for 32 consecutive columns of a row.
+ * Scale byte b stands for 2^(b - 127); an element is its e4m3 value times its
+ * block's scale.  The scale is the smallest power of two, 2^-110 or more, of
+ * which 448 times is at least the block's largest finite magnitude; values
+ * are rounded to the nearest, ties to even: an element is off by at most 2^-4 of
+ * itself or 2^-10 of the scale.  Elements that are not finite become NaN.
+ * Reading back is exact in bf16 (values that round up to 2^128 read as
+ * infinity).
+ *
+ * tide_act8_bytes: the checkpoint's size.  x: bf16, element (t, c) at
+ * t * ldx + c, 2-byte aligned, ldx >= cols.  x and the checkpoint may not
+ * overlap.  rows < 2^31, cols and ldx <= 2^22 (TIDE_EUNSUPPORTED).
+ * Asynchronous on `stream`, which belongs to the current device
+ * (TIDE_EINVAL otherwise); allocates nothing. */
+tide_status tide_act8_bytes(int64_t rows, int64_t cols, size_t *bytes);
+tide_status tide_act8_pack(const void *x, int64_t ldx, int64_t rows, int64_t cols, void *kept,
+                           tide_stream_t stream);
+tide_status tide_act8_unpack(const void *kept, int64_t rows, int64_t cols, void *x, int64_t ldx,
+                             tide_stream_t stream);
+
+/* A layer's product on a placed weight, and its gradients.
+ *
+ * forward:  z = x W^T + bias, y = act(z) + residual, with T tokens, x [T, K],
+ *           W [N, K], bias [N], residual and y [T, N], all bf16; the sum, the
+ *           bias, act and the residual are in binary32 and y is rounded once.
+ *           W is contiguous: a full tensor that tide_ag_place writes.
+ *           z_kept, where given, receives the checkpoint of z (in 8 bits
+ *           straight from binary32) that the gradient of act needs.
+ * backward: dz = dy act'(z), dx = dz W, dW = dz^T x, dbias = the sum of dz over
+ *           the tokens, with z and x as their checkpoints stand for them.
+ *           dx, dW and dbias are bf16: dW [N, K] (contiguous) and dbias [N] are what
+ *           tide_rs_bf16_to_fp32 reads as a rank's gradients.  Each of the
+ *           three may be NULL (not computed), and so may what only it needs
+ *           (W for dx, x_kept for dW; z_kept with TIDE_ACT_NONE).  Where act
+ *           is not TIDE_ACT_NONE, dz is rounded to bf16 once before the
+ *           products (dbias sums it unrounded).  The residual's gradient is
+ *           dy itself.
+ *
+ * A z that is not finite was kept as NaN and makes its gradients NaN.  The
+ * gradient of relu at 0 is 0.
+ *
+ * Rows of x, residual, y, dy and dx lie ld* elements apart (>= the row's
+ * length; any 2-byte alignment; rows that start on 16 bytes with widths that
+ * are multiples of 8 save a copy of the operand into the workspace).  Outputs may
+ * overlap no input and no other output (TIDE_EOVERLAP), but y may be the
+ * residual itself (same address and ldy = ldr).  T < 2^31; N, K and every
+ * ld at most 2^22 (TIDE_EUNSUPPORTED).  T, N or K may be 0: an empty sum is 0,
+ * and outputs without elements are not touched.
+ *
+ * The workspace (16-byte aligned device memory of at least the bytes that
+ * the _workspace call gives for the same arguments, TIDE_ENOSPACE otherwise;
+ * NULL where that is 0) holds nothing between calls and needs no clearing.
+ * It may overlap nothing else.  Calls that may run at the same time, also two
+ * captured graphs, need a workspace each.  Asynchronous on `stream`, which
+ * belongs to the current device (TIDE_EINVAL otherwise); the library
+ * allocates nothing, no result depends on timing (no atomic adds). */
+#define TIDE_ACT_NONE 0
+#define TIDE_ACT_RELU 1
+#define TIDE_ACT_GELU 2      /* z Phi(z), Phi through erf */
+#define TIDE_ACT_GELU_TANH 3 /* its tanh approximation */
+#define TIDE_ACT_SILU 4      /* z / (1 + exp(-z)) */
+
+typedef struct tide_linear_forward_args {
+    int64_t tokens, out_features, in_features; /* T, N, K */
+    int32_t act;                               /* TIDE_ACT_* */
+    int32_t reserved;                          /* 0 */
+    const void *x;
+    int64_t ldx;
+    const void *weight;
+    const void *bias;     /* or NULL */
+    const void *residual; /* or NULL */
+    int64_t ldr;
+    void *y;
+    int64_t ldy;
+    void *z_kept; /* or NULL */
+} tide_linear_forward_args;
+
+typedef struct tide_linear_backward_args {
+    int64_t tokens, out_features, in_features; /* T, N, K */
+    int32_t act;                               /* TIDE_ACT_* */
+    int32_t reserved;                          /* 0 */
+    const void *dy;
+    int64_t lddy;
+    const void *weight;
+    const void *x_kept;
+    const void *z_kept;
+    void *dx; /* or NULL */
+    int64_t lddx;
+    void *dweight; /* or NULL */
+    void *dbias;   /* or NULL */
+} tide_linear_backward_args;
+
+tide_status tide_linear_forward_workspace(const tide_linear_forward_args *args, size_t *bytes);
+tide_status tide_linear_forward(const tide_linear_forward_args *args, void *workspace,
+                                size_t workspace_bytes, tide_stream_t stream);
+tide_status tide_linear_backward_workspace(const tide_linear_backward_args *args, size_t *bytes);
+tide_status tide_linear_backward(const tide_linear_backward_args *args, void *workspace,
+                                 size_t workspace_bytes, tide_stream_t stream);
+
 /* Static text for a status code. */
 const char *tide_status_str(int32_t status);
 

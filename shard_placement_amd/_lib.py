@@ -29,7 +29,9 @@ EXPORTS = ("tide_abi_version", "tide_status_str", "tide_desc_size", "tide_desc_g
            "tide_rs_stage_to_shards", "tide_rs_stage_to_shards_sdma", "tide_plan_rank_tiles",
            "tide_stream_create_cu_range", "tide_pipeline_create", "tide_pipeline_run",
            "tide_pipeline_destroy", "tide_rs_two_phase_noalloc", "tide_rs_bf16_to_fp32_trace",
-           "tide_rs_bf16_to_fp32_streams")
+           "tide_rs_bf16_to_fp32_streams", "tide_act8_bytes", "tide_act8_pack", "tide_act8_unpack",
+           "tide_linear_forward_workspace", "tide_linear_forward",
+           "tide_linear_backward_workspace", "tide_linear_backward")
 
 
 class TideShape(ctypes.Structure):
@@ -50,6 +52,24 @@ class TidePlanInfo(ctypes.Structure):
                 ("ag_tile_elems", ctypes.c_int32), ("blob_bytes", ctypes.c_int64),
                 ("rs_launch_tiles", ctypes.c_int64), ("ag_launch_tiles", ctypes.c_int64),
                 ("rs_lds_bytes", ctypes.c_int64)]
+
+
+class TideLinearForwardArgs(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("out_features", ctypes.c_int64),
+                ("in_features", ctypes.c_int64), ("act", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64), ("y", ctypes.c_void_p),
+                ("ldy", ctypes.c_int64), ("z_kept", ctypes.c_void_p)]
+
+
+class TideLinearBackwardArgs(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("out_features", ctypes.c_int64),
+                ("in_features", ctypes.c_int64), ("act", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("x_kept", ctypes.c_void_p),
+                ("z_kept", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64),
+                ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p)]
 
 
 class TideError(RuntimeError):
@@ -118,6 +138,15 @@ def lib():
     L.tide_rs_two_phase_noalloc.argtypes = [vp, vp, i64, i64, i32, vp]
     L.tide_rs_bf16_to_fp32_trace.argtypes = [vp, vp, i32, i32, vp, vp, i64, vp]
     L.tide_rs_bf16_to_fp32_streams.argtypes = [vp, vp, i32, i32, ctypes.POINTER(vp), i32]
+    sizep = ctypes.POINTER(ctypes.c_size_t)
+    fwd, bwd = ctypes.POINTER(TideLinearForwardArgs), ctypes.POINTER(TideLinearBackwardArgs)
+    L.tide_act8_bytes.argtypes = [i64, i64, sizep]
+    L.tide_act8_pack.argtypes = [vp, i64, i64, i64, vp, vp]
+    L.tide_act8_unpack.argtypes = [vp, i64, i64, vp, i64, vp]
+    L.tide_linear_forward_workspace.argtypes = [fwd, sizep]
+    L.tide_linear_forward.argtypes = [fwd, vp, ctypes.c_size_t, vp]
+    L.tide_linear_backward_workspace.argtypes = [bwd, sizep]
+    L.tide_linear_backward.argtypes = [bwd, vp, ctypes.c_size_t, vp]
     for name in ("tide_desc_size", "tide_desc_geometry", "tide_desc_build", "tide_plan_query",
                  "tide_rs_bf16_to_fp32", "tide_ag_place", "tide_ag_place_sdma",
                  "tide_stream_create_cu_limited", "tide_stream_destroy",
@@ -127,7 +156,10 @@ def lib():
                  "tide_rs_stage_to_shards", "tide_rs_stage_to_shards_sdma", "tide_plan_rank_tiles",
                  "tide_stream_create_cu_range", "tide_pipeline_create", "tide_pipeline_run",
                  "tide_pipeline_destroy", "tide_rs_two_phase_noalloc",
-                 "tide_rs_bf16_to_fp32_trace", "tide_rs_bf16_to_fp32_streams"):
+                 "tide_rs_bf16_to_fp32_trace", "tide_rs_bf16_to_fp32_streams",
+                 "tide_act8_bytes", "tide_act8_pack", "tide_act8_unpack",
+                 "tide_linear_forward_workspace", "tide_linear_forward",
+                 "tide_linear_backward_workspace", "tide_linear_backward"):
         getattr(L, name).restype = ctypes.c_int
     if L.tide_abi_version() != 2:
         raise RuntimeError("libtide ABI version %d, expected 2" % L.tide_abi_version())

@@ -21,9 +21,11 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._lib import TideError, TideOpts, TidePlanInfo, TideShape, check
+from ._lib import (TideError, TideLinearBackwardArgs, TideLinearForwardArgs, TideOpts,
+                   TidePlanInfo, TideShape, check)
 
 ORDERS = {"fixed": 0, "tree": 1}
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
 def _shapes(shapes: Sequence[Sequence[int]]):
@@ -311,6 +313,170 @@ def _require(t: torch.Tensor, dtype, what: str) -> None:
         raise TideError(-6, "%s is on %s, expected a GPU tensor" % (what, t.device))
     if not t.is_contiguous():
         raise TideError(-6, "%s is not contiguous" % what)
+
+
+def _device_call(device, stream, call):
+    """call(stream handle) with ``device`` current and ``stream`` (default:
+    the device's current stream) the one that allocations belong to."""
+    if device.index == torch.cuda.current_device() and stream is None:
+        return call(ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream))
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream))
+        with torch.cuda.stream(stream):
+            return call(ctypes.c_void_p(int(stream.cuda_stream)))
+
+
+def _matrix(t: torch.Tensor, rows: int, cols: int, what: str, device=None):
+    """(address, row distance) of a [rows, cols] bf16 GPU matrix whose rows
+    may lie apart but are contiguous themselves."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % what)
+    if t.dtype != torch.bfloat16:
+        raise TideError(-6, "%s has dtype %s, expected %s" % (what, t.dtype, torch.bfloat16))
+    if t.device.type != "cuda" or (device is not None and t.device != device):
+        raise TideError(-6, "%s is on %s, expected %s" % (what, t.device, device or "a GPU"))
+    if tuple(t.shape) != (rows, cols):
+        raise TideError(-1, "%s is %s, expected [%d, %d]" % (what, list(t.shape), rows, cols))
+    if cols > 1 and t.stride(1) != 1:
+        raise TideError(-6, "%s has rows that are not contiguous" % what)
+    if rows > 1 and t.stride(0) < cols:
+        raise TideError(-6, "%s has rows that share memory" % what)
+    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+
+
+def _whole(t: torch.Tensor, shape, what: str, device) -> int:
+    """Address of a contiguous bf16 tensor of this shape on ``device``."""
+    _require(t, torch.bfloat16, what)
+    if tuple(t.shape) != tuple(shape):
+        raise TideError(-1, "%s is %s, expected %s" % (what, list(t.shape), list(shape)))
+    if t.device != device:
+        raise TideError(-6, "%s is on %s, expected %s" % (what, t.device, device))
+    return t.data_ptr()
+
+
+def _kept(t: torch.Tensor, rows: int, cols: int, what: str, device) -> int:
+    """Address of a checkpoint of a [rows, cols] matrix (a flat uint8 tensor)."""
+    _require(t, torch.uint8, what)
+    if t.device != device:
+        raise TideError(-6, "%s is on %s, expected %s" % (what, t.device, device))
+    need = tide_act8_bytes(rows, cols)
+    if t.numel() < need:
+        raise TideError(-1, "%s holds %d bytes, need %d" % (what, t.numel(), need))
+    return t.data_ptr()
+
+
+def _act(act: str) -> int:
+    if act not in ACTS:
+        raise TideError(-1, "act is %r, expected one of %s" % (act, ", ".join(ACTS)))
+    return ACTS[act]
+
+
+def _workspace(query, args, device):
+    """(tensor, address, bytes) of the call's workspace.  It is taken from
+    torch's allocator for each call: calls on different streams, or captured
+    into different graphs, never share one."""
+    n = ctypes.c_size_t(0)
+    check(query(ctypes.byref(args), ctypes.byref(n)), query.__name__)
+    if not n.value:
+        return None, None, 0
+    t = torch.empty(n.value, dtype=torch.uint8, device=device)
+    return t, t.data_ptr(), n.value
+
+
+def tide_act8_bytes(rows: int, cols: int) -> int:
+    """Bytes of an 8-bit checkpoint of a [rows, cols] matrix."""
+    n = ctypes.c_size_t(0)
+    check(_lib.lib().tide_act8_bytes(int(rows), int(cols), ctypes.byref(n)), "tide_act8_bytes")
+    return int(n.value)
+
+
+def tide_act8_pack(x: torch.Tensor, kept: torch.Tensor, stream=None) -> None:
+    """Write the checkpoint of the bf16 matrix ``x`` into ``kept`` (uint8)."""
+    if x.dim() != 2:
+        raise TideError(-1, "x has %d dimensions, expected 2" % x.dim())
+    rows, cols = x.shape
+    px, ldx = _matrix(x, rows, cols, "x")
+    pk = _kept(kept, rows, cols, "kept", x.device)
+    _device_call(x.device, stream, lambda s: check(
+        _lib.lib().tide_act8_pack(px, ldx, rows, cols, pk, s), "tide_act8_pack"))
+
+
+def tide_act8_unpack(kept: torch.Tensor, x: torch.Tensor, stream=None) -> None:
+    """Write the values of the checkpoint ``kept`` into the bf16 matrix ``x``."""
+    if x.dim() != 2:
+        raise TideError(-1, "x has %d dimensions, expected 2" % x.dim())
+    rows, cols = x.shape
+    px, ldx = _matrix(x, rows, cols, "x")
+    pk = _kept(kept, rows, cols, "kept", x.device)
+    _device_call(x.device, stream, lambda s: check(
+        _lib.lib().tide_act8_unpack(pk, rows, cols, px, ldx, s), "tide_act8_unpack"))
+
+
+def tide_linear_forward(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor = None, bias=None,
+                        residual=None, act: str = "none", z_kept=None, stream=None) -> torch.Tensor:
+    """y = act(x weight^T + bias) + residual; z_kept (uint8), where given,
+    receives the checkpoint of act's argument.  Returns y (allocated when not
+    given)."""
+    if x.dim() != 2 or weight.dim() != 2:
+        raise TideError(-1, "x and weight are matrices")
+    (T, K), N, dev = x.shape, weight.shape[0], x.device
+    a = TideLinearForwardArgs()
+    a.tokens, a.out_features, a.in_features, a.act = T, N, K, _act(act)
+    a.x, a.ldx = _matrix(x, T, K, "x")
+    a.weight = _whole(weight, (N, K), "weight", dev)
+    if bias is not None:
+        a.bias = _whole(bias, (N,), "bias", dev)
+    if residual is not None:
+        a.residual, a.ldr = _matrix(residual, T, N, "residual", dev)
+    if z_kept is not None:
+        a.z_kept = _kept(z_kept, T, N, "z_kept", dev)
+    L = _lib.lib()
+
+    def call(s):
+        out = torch.empty(T, N, dtype=torch.bfloat16, device=dev) if y is None else y
+        a.y, a.ldy = _matrix(out, T, N, "y", dev)
+        ws, ptr, n = _workspace(L.tide_linear_forward_workspace, a, dev)
+        check(L.tide_linear_forward(ctypes.byref(a), ptr, n, s), "tide_linear_forward")
+        return out
+
+    return _device_call(dev, stream, call)
+
+
+def tide_linear_backward(dy: torch.Tensor, in_features: int, weight=None, x_kept=None,
+                         z_kept=None, act: str = "none", dx=None, dweight=None, dbias=None,
+                         stream=None) -> None:
+    """The gradients that are given: dx = dz weight, dweight = dz^T x, dbias =
+    the sum of dz over the tokens, dz = dy act'(z)."""
+    if dy.dim() != 2:
+        raise TideError(-1, "dy has %d dimensions, expected 2" % dy.dim())
+    (T, N), K, dev = dy.shape, int(in_features), dy.device
+    a = TideLinearBackwardArgs()
+    a.tokens, a.out_features, a.in_features, a.act = T, N, K, _act(act)
+    a.dy, a.lddy = _matrix(dy, T, N, "dy")
+    if a.act:
+        if z_kept is None:
+            raise TideError(-1, "act %r needs the checkpoint of its argument" % act)
+        a.z_kept = _kept(z_kept, T, N, "z_kept", dev)
+    if dx is not None:
+        if weight is None:
+            raise TideError(-1, "dx needs the weight")
+        a.weight = _whole(weight, (N, K), "weight", dev)
+        a.dx, a.lddx = _matrix(dx, T, K, "dx", dev)
+    if dweight is not None:
+        if x_kept is None:
+            raise TideError(-1, "dweight needs the checkpoint of x")
+        a.x_kept = _kept(x_kept, T, K, "x_kept", dev)
+        a.dweight = _whole(dweight, (N, K), "dweight", dev)
+    if dbias is not None:
+        a.dbias = _whole(dbias, (N,), "dbias", dev)
+    L = _lib.lib()
+
+    def call(s):
+        ws, ptr, n = _workspace(L.tide_linear_backward_workspace, a, dev)
+        check(L.tide_linear_backward(ctypes.byref(a), ptr, n, s), "tide_linear_backward")
+
+    _device_call(dev, stream, call)
 
 
 class Plan:

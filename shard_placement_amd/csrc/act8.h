@@ -1,0 +1,80 @@
+// act8.h -- the 8-bit activation checkpoint's format, shared by its kernels
+// (act8.hip) and the products that write or read it (linear.hip).
+//
+// A checkpoint of a [rows, cols] matrix is rows * pitch bytes of e4m3 values
+// (row-major, pitch = cols rounded up to 32, the padding columns 0) followed
+// by rows * pitch / 32 scale bytes, one for each 32 consecutive columns of a
+// row.  Scale byte e + 127 stands for 2^e; an element's value is its e4m3
+// value times its block's scale.  With a the largest finite |x| of the block,
+//   e = the smallest integer with a <= 448 * 2^e, but at least -110,
+// so nothing saturates, and the scale being a power of two, dividing by it is
+// exact and the only rounding is the one to e4m3 (half a step: 2^-4 relative,
+// 2^-10 of the scale for e4m3's subnormals).  With e >= -110 every non-zero
+// value is at least 2^-119, so values are normal binary32 and, having four
+// significant bits, exactly bf16: reading a checkpoint back rounds nothing (in
+// a block that reaches 2^127, values that round up to 2^128 read back as
+// infinity).
+// Elements that are not finite become the e4m3 NaN and leave the block's
+// scale to the others.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace tide {
+
+constexpr int kActBlock = 32;
+constexpr int kActMinExp = -110;
+
+__host__ __device__ constexpr int64_t act8_pitch(int64_t cols) {
+    return (cols + kActBlock - 1) / kActBlock * kActBlock;
+}
+__host__ __device__ constexpr int64_t act8_scale_offset(int64_t rows, int64_t cols) {
+    return rows * act8_pitch(cols);
+}
+__host__ __device__ constexpr int64_t act8_bytes(int64_t rows, int64_t cols) {
+    return rows * (act8_pitch(cols) + act8_pitch(cols) / kActBlock);
+}
+
+// |x| for the block's maximum: 0 for an element that is not finite.
+__device__ __forceinline__ float act8_mag(float x) {
+    const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
+    return b < 0x7f800000u ? __uint_as_float(b) : 0.0f;
+}
+
+// The block's exponent from its maximum.  448 = 1.75 * 2^8: a = m * 2^k has
+// exponent k - 8 for m <= 1.75 and k - 7 above, and adding one less than
+// 2^23 - 0x600000 to the bits carries into the exponent exactly then.
+__device__ __forceinline__ int act8_exp(float amax) {
+    const int e = (int)((__float_as_uint(amax) + 0x1fffffu) >> 23) - 127 - 8;
+    return e > kActMinExp ? e : kActMinExp;
+}
+
+// A scale byte's scale.
+__device__ __forceinline__ float act8_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
+__device__ __forceinline__ float act8_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Four elements to four e4m3 bytes (round to nearest even); inv = 2^-e.
+__device__ __forceinline__ uint32_t act8_pack4(float a, float b, float c, float d, float inv) {
+    // infinities are stored as NaN (the conversion alone could saturate them)
+    a = __builtin_isfinite(a) ? a * inv : __builtin_nanf("");
+    b = __builtin_isfinite(b) ? b * inv : __builtin_nanf("");
+    c = __builtin_isfinite(c) ? c * inv : __builtin_nanf("");
+    d = __builtin_isfinite(d) ? d * inv : __builtin_nanf("");
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+}
+
+// The four values of a word of e4m3 bytes, times the scale.
+__device__ __forceinline__ void act8_unpack4(uint32_t w, float s, float (&v)[4]) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+    const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    v[0] = lo.x * s;
+    v[1] = lo.y * s;
+    v[2] = hi.x * s;
+    v[3] = hi.y * s;
+}
+
+}  // namespace tide

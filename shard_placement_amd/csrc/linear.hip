@@ -1,0 +1,737 @@
+// linear.hip -- a layer's product on a placed weight, with bias, activation
+// and residual in its epilogue, and its gradients from 8-bit checkpoints, for
+// gfx950.
+//
+//   forward   z = x W^T + bias, y = act(z) + residual
+//   backward  dz = dy act'(z), dx = dz W, dW = dz^T x, dbias = column sums of dz
+//
+// W is a full tensor as the all-gather placement writes it, dW and dbias are
+// gradients as the reduce-scatter reads them.  All three products run
+// through one tile loop (tile_product.h); the epilogue works on the
+// accumulators in registers, so z is never written in more than 8 bits.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "act8.h"
+#include "bf16_io.h"
+#include "linear_check.h"
+#include "tide.h"
+#include "tile_product.h"
+
+using namespace tide;
+
+namespace {
+
+// ---- activation functions ------------------------------------------------
+
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kTanhC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kTanhA = 0.044715f;
+
+// 1 / (1 + exp(-u)); 0.5 (1 + tanh(v)) is this at u = 2 v, so the tanh form
+// of gelu is z * sigmoid(2 sqrt(2/pi) (z + 0.044715 z^3)).
+__device__ __forceinline__ float sigmoid(float u) { return 1.0f / (1.0f + __expf(-u)); }
+
+__device__ __forceinline__ float act_value(float z, int act) {
+    switch (act) {
+        case TIDE_ACT_RELU: return z > 0.0f ? z : 0.0f * z;
+        case TIDE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+        case TIDE_ACT_GELU_TANH: return z * sigmoid(kTanhC * (z + kTanhA * z * z * z));
+        case TIDE_ACT_SILU: return z * sigmoid(z);
+        default: return z;
+    }
+}
+
+__device__ __forceinline__ float act_slope(float z, int act) {
+    switch (act) {
+        case TIDE_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f * z;
+        case TIDE_ACT_GELU:
+            return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * __expf(-0.5f * z * z) * kInvSqrt2Pi;
+        case TIDE_ACT_GELU_TANH: {
+            const float s = sigmoid(kTanhC * (z + kTanhA * z * z * z));
+            return s + z * s * (1.0f - s) * kTanhC * (1.0f + 3.0f * kTanhA * z * z);
+        }
+        case TIDE_ACT_SILU: {
+            const float s = sigmoid(z);
+            return s * (1.0f + z * (1.0f - s));
+        }
+        default: return 1.0f;
+    }
+}
+
+// ---- epilogue ------------------------------------------------------------
+
+// What happens to a finished sum at output column i of row j.
+struct Epilogue {
+    int64_t I, J;
+    uint16_t* out;
+    int64_t ldo;
+    const uint16_t* bias;
+    const uint16_t* res;
+    int64_t ldr;
+    uint8_t* kept;  // the checkpoint of z
+    int32_t act;
+};
+
+// Eight sums at columns i .. i + 7 of row j through the epilogue.  A
+// checkpoint's block of 32 columns lies in four consecutive lanes, all of
+// which call this (`there`: the lane's row and columns exist).
+__device__ __forceinline__ void finish(const Epilogue& e, int64_t i, int64_t j, bool there,
+                                       float (&v)[8]) {
+    const int64_t n = there ? e.I - i : 0;
+    if (e.bias) {
+        float b[8];
+        load8(e.bias + i, n, b);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] += b[r];
+    }
+    if (e.kept) {
+        float a = 0.0f;
+        float z[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            z[r] = r < n ? v[r] : 0.0f;
+            a = fmaxf(a, act8_mag(z[r]));
+        }
+        a = fmaxf(a, __shfl_xor(a, 1));
+        a = fmaxf(a, __shfl_xor(a, 2));
+        const int64_t pitch = act8_pitch(e.I);
+        if (j < e.J && i < pitch) {
+            const int x = act8_exp(a);
+            const float inv = act8_pow2(-x);
+            const u32x2 q = {act8_pack4(z[0], z[1], z[2], z[3], inv),
+                             act8_pack4(z[4], z[5], z[6], z[7], inv)};
+            *(TIDE_GLOBAL_AS u32x2*)(e.kept + j * pitch + i) = q;
+            if (i % kActBlock == 0)
+                *(TIDE_GLOBAL_AS uint8_t*)(e.kept + e.J * pitch + (j * pitch + i) / kActBlock) =
+                    (uint8_t)(x + 127);
+        }
+    }
+    if (n <= 0) return;
+    if (e.act != TIDE_ACT_NONE) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] = act_value(v[r], e.act);
+    }
+    if (e.res) {
+        float x[8];
+        load8(e.res + j * e.ldr + i, n, x);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] += x[r];
+    }
+    store8(e.out + j * e.ldo + i, n, v);
+}
+
+// ---- products ------------------------------------------------------------
+
+struct Product {
+    Operand A, B;
+    int64_t depth;        // contraction elements
+    int64_t split_depth;  // of one split (a multiple of kStepK)
+    int32_t tiles_i, tiles_j, splits;
+    float* partial;       // [splits][J][pitch] sums where splits > 1
+    int64_t partial_pitch;
+    Epilogue e;
+};
+
+// Workgroup -> (tile, split).  Consecutive workgroups go to the 8 XCDs in
+// turn, so each XCD is given a run of consecutive tiles of its own, and tiles
+// are numbered in bands of kBand tiles of j (all of i inside a band): the
+// tiles an XCD works on together share rows of both operands in its L2.
+constexpr int kXcdCount = 8;
+constexpr int kBand = 4;
+
+__device__ __forceinline__ void tile_at(const Product& p, int64_t* ti, int64_t* tj, int64_t* sp) {
+    const int64_t total = gridDim.x;
+    int64_t b = blockIdx.x;
+    const int64_t each = total / kXcdCount, extra = total % kXcdCount;
+    const int64_t x = b % kXcdCount, n = b / kXcdCount;
+    b = x * each + (x < extra ? x : extra) + n;
+    const int64_t tiles = (int64_t)p.tiles_i * p.tiles_j;
+    *sp = b / tiles;
+    b -= *sp * tiles;
+    const int64_t band = b / ((int64_t)kBand * p.tiles_i);
+    const int64_t width = min((int64_t)kBand, p.tiles_j - band * kBand);
+    b -= band * kBand * p.tiles_i;
+    *ti = b / width;
+    *tj = band * kBand + b % width;
+}
+
+// A wave's LDS writes have arrived before its reads, and its reads have
+// returned before it writes again.
+__device__ __forceinline__ void wave_lds_order() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+template <int BI, int BJ, int WI, int WJ, bool CA, bool CB>
+__global__ __launch_bounds__(WI* WJ * 64, BI == 256 ? 2 : 1) void product_kernel(Product p) {
+    constexpr int TI = BI / WI / 16, TJ = BJ / WJ / 16;
+    static_assert(TI % 2 == 0, "a wave holds whole checkpoint blocks");
+    __shared__ __attribute__((aligned(1024))) char lds[2 * (BI + BJ) * kStepK * 2];
+    int64_t ti, tj, sp;
+    tile_at(p, &ti, &tj, &sp);
+    const int64_t i0 = ti * BI, j0 = tj * BJ;
+    const int64_t k0 = sp * p.split_depth;
+    const int64_t k1 = min(p.depth, k0 + p.split_depth);
+    f32x4v acc[TI][TJ];
+    tile_loop<BI, BJ, WI, WJ, CA, CB>(p.A, p.B, p.depth, k0, k1, i0, j0, (TIDE_LDS char*)lds, acc);
+
+    // The accumulators pass through LDS, 16 rows of a wave at a time, so that
+    // each lane ends with 8 consecutive columns and a row's stores are whole
+    // lines.  The row pitch's extra 4 floats keep the writes off each other's
+    // banks.
+    constexpr int kRow = TI * 16, kPitch = kRow + 4, kLanes = kRow / 8;
+    static_assert(WI * WJ * 16 * kPitch * 4 <= (int)sizeof(lds), "the staging fits");
+    tile_barrier();
+    const int lane = threadIdx.x & 63;
+    const int wave = threadIdx.x >> 6;
+    TIDE_LDS float* mine = (TIDE_LDS float*)(TIDE_LDS char*)lds + wave * 16 * kPitch;
+    const int64_t iw = i0 + (wave / WJ) * kRow + (lane % kLanes) * 8;
+    const int64_t jw = j0 + (wave % WJ) * TJ * 16 + lane / kLanes;
+#pragma unroll
+    for (int y = 0; y < TJ; ++y) {
+#pragma unroll
+        for (int x = 0; x < TI; ++x)
+            *(TIDE_LDS f32x4v*)(mine + (lane & 15) * kPitch + x * 16 + (lane >> 4) * 4) = acc[x][y];
+        wave_lds_order();
+#pragma unroll 1
+        for (int r = 0; r < 16; r += 64 / kLanes) {
+            const int64_t j = jw + 16 * y + r;
+            const TIDE_LDS float* row = mine + (r + lane / kLanes) * kPitch + (lane % kLanes) * 8;
+            const f32x4v lo = *(const TIDE_LDS f32x4v*)row, hi = *(const TIDE_LDS f32x4v*)(row + 4);
+            const bool there = j < p.e.J && iw < p.e.I;
+            if (p.splits > 1) {
+                if (!there) continue;
+                float* to = p.partial + (sp * p.e.J + j) * p.partial_pitch + iw;
+                *(TIDE_GLOBAL_AS f32x4v*)to = lo;
+                *(TIDE_GLOBAL_AS f32x4v*)(to + 4) = hi;
+                continue;
+            }
+            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            finish(p.e, iw, j, there, v);
+        }
+        wave_lds_order();
+    }
+}
+
+// The sums of a split contraction added up in the splits' order, then the
+// epilogue.
+constexpr int kJoinThreads = 256;
+
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(Product p) {
+    const int64_t per_row = p.partial_pitch / 8;
+    const int64_t u = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
+    const int64_t j = u / per_row, i = (u - j * per_row) * 8;
+    const bool there = j < p.e.J && i < p.e.I;
+    float v[8] = {};
+    if (there) {
+        for (int s = 0; s < p.splits; ++s) {
+            const float* from = p.partial + ((int64_t)s * p.e.J + j) * p.partial_pitch + i;
+            const f32x4v lo = *(const TIDE_GLOBAL_AS f32x4v*)from;
+            const f32x4v hi = *(const TIDE_GLOBAL_AS f32x4v*)(from + 4);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                v[r] += lo[r];
+                v[r + 4] += hi[r];
+            }
+        }
+    }
+    finish(p.e, i, j, there, v);
+}
+
+// ---- operand preparation -------------------------------------------------
+
+// Rows of `cols` elements copied to rows of `width` (a multiple of 8), the
+// rest 0: operands whose rows do not start on 16 bytes, or whose length is
+// not a multiple of 8.
+constexpr int kPadThreads = 256;
+
+__global__ __launch_bounds__(kPadThreads) void pad_kernel(const uint16_t* in, int64_t ld,
+                                                          int64_t rows, int64_t cols,
+                                                          uint16_t* out, int64_t width) {
+    const int64_t per_row = width / 8;
+    const int64_t u = (int64_t)blockIdx.x * kPadThreads + threadIdx.x;
+    const int64_t r = u / per_row, c = (u - r * per_row) * 8;
+    if (r >= rows) return;
+    float v[8];
+    load8(in + r * ld + c, cols - c, v);
+    store8(out + r * width + c, 8, v);
+}
+
+// dz = dy act'(z) rounded to bf16, rows of `width` elements with zeros behind
+// the N-th, and the column sums of dz before the rounding over each chunk of
+// rows (one row of `sums` for each chunk).  A workgroup takes 256 columns of a
+// chunk: 32 lanes of 8 columns, 8 rows at a time.
+constexpr int kDzThreads = 256;
+constexpr int kDzCols = 256;
+
+struct DzArgs {
+    const uint16_t* dy;
+    int64_t ld;
+    const uint8_t* z;  // its checkpoint, or NULL (act none)
+    uint16_t* dz;      // or NULL: sums only
+    int64_t width;
+    float* sums;       // or NULL
+    int64_t T, N, chunk;
+    int32_t col_groups;
+    int32_t act;
+};
+
+__global__ __launch_bounds__(kDzThreads) void dz_kernel(DzArgs p) {
+    __shared__ float part[8][kDzCols];
+    const int64_t cg = blockIdx.x % p.col_groups, ch = blockIdx.x / p.col_groups;
+    const int lc = threadIdx.x & 31, lr = threadIdx.x >> 5;
+    const int64_t c = cg * kDzCols + lc * 8;
+    const int64_t t1 = min(p.T, (ch + 1) * p.chunk);
+    const int64_t pitch = act8_pitch(p.N);
+    float sum[8] = {};
+    if (c < p.N) {
+        for (int64_t t = ch * p.chunk + lr; t < t1; t += 8) {
+            float v[8];
+            load8(p.dy + t * p.ld + c, p.N - c, v);
+            if (p.z) {
+                const u32x2 q = *(const TIDE_GLOBAL_AS u32x2*)(p.z + t * pitch + c);
+                const float s = act8_scale(
+                    *(const TIDE_GLOBAL_AS uint8_t*)(p.z + p.T * pitch + (t * pitch + c) / kActBlock));
+                float lo[4], hi[4];
+                act8_unpack4(q.x, s, lo);
+                act8_unpack4(q.y, s, hi);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    v[r] *= act_slope(lo[r], p.act);
+                    v[r + 4] *= act_slope(hi[r], p.act);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                if (c + r >= p.N) v[r] = 0.0f;
+                sum[r] += v[r];
+            }
+            if (p.dz) store8(p.dz + t * p.width + c, 8, v);
+        }
+    }
+    if (!p.sums) return;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) part[lr][lc * 8 + r] = sum[r];
+    __syncthreads();
+    const int64_t col = cg * kDzCols + threadIdx.x;
+    if (col >= p.N) return;
+    float s = part[0][threadIdx.x];
+#pragma unroll
+    for (int r = 1; r < 8; ++r) s += part[r][threadIdx.x];
+    p.sums[ch * p.N + col] = s;
+}
+
+__global__ __launch_bounds__(256) void dbias_kernel(const float* sums, int64_t chunks, int64_t N,
+                                                    uint16_t* out) {
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= N) return;
+    float s = 0.0f;
+    for (int64_t k = 0; k < chunks; ++k) s += sums[k * N + c];
+    out[c] = to_bf16(s);
+}
+
+// ---- host ----------------------------------------------------------------
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+// The workspace's pieces, handed out in order, each on 256 bytes.
+struct Carver {
+    char* base;
+    int64_t used = 0;
+    template <typename T>
+    T* take(int64_t count) {
+        T* p = base ? reinterpret_cast<T*>(base + used) : nullptr;
+        used += round_up(count * (int64_t)sizeof(T), 256);
+        return p;
+    }
+};
+
+enum Kind { kForward, kGradInput, kGradWeight };
+
+// Tile and split for a product of I x J outputs.
+struct Shape {
+    int bi, bj;
+    int32_t tiles_i, tiles_j, splits;
+    int64_t split_depth;
+};
+
+Shape choose(int64_t I, int64_t J, int64_t depth) {
+    Shape s;
+    int64_t want;  // workgroups that fill the chip
+    if (J <= 64) {
+        s.bi = 128;
+        s.bj = J <= 16 ? 16 : J <= 32 ? 32 : 64;
+        want = 1024;
+    } else if (ceil_div(I, 256) * ceil_div(J, 256) >= 192) {
+        s.bi = s.bj = 256;
+        want = 0;
+    } else {
+        s.bi = s.bj = 128;
+        want = 512;
+    }
+    s.tiles_i = (int32_t)ceil_div(I, s.bi);
+    s.tiles_j = (int32_t)ceil_div(J, s.bj);
+    const int64_t tiles = (int64_t)s.tiles_i * s.tiles_j;
+    const int64_t steps = ceil_div(depth, kStepK);
+    int64_t splits = std::max<int64_t>(1, std::min(want / std::max<int64_t>(1, tiles), steps / 4));
+    const int64_t each = std::max<int64_t>(1, ceil_div(steps, splits));
+    s.split_depth = each * kStepK;
+    s.splits = (int32_t)std::max<int64_t>(1, ceil_div(steps, each));
+    return s;
+}
+
+int64_t partial_floats(const Shape& s, int64_t I, int64_t J) {
+    return s.splits > 1 ? s.splits * J * round_up(I, kActBlock) : 0;
+}
+
+using ProductKernel = void (*)(Product);
+
+template <int BI, int BJ, int WI, int WJ>
+ProductKernel of_kind(Kind k) {
+    switch (k) {
+        case kForward: return product_kernel<BI, BJ, WI, WJ, false, false>;
+        case kGradInput: return product_kernel<BI, BJ, WI, WJ, true, false>;
+        default: return product_kernel<BI, BJ, WI, WJ, true, true>;
+    }
+}
+
+tide_status run_product(Kind kind, Product p, const Shape& s, float* partial,
+                        tide_stream_t stream) {
+    if (p.e.I == 0 || p.e.J == 0) return TIDE_OK;
+    p.tiles_i = s.tiles_i;
+    p.tiles_j = s.tiles_j;
+    p.splits = s.splits;
+    p.split_depth = s.split_depth;
+    p.partial = partial;
+    p.partial_pitch = round_up(p.e.I, kActBlock);
+    ProductKernel k;
+    int threads = 256;
+    if (s.bi == 256) {
+        k = of_kind<256, 256, 2, 4>(kind);
+        threads = 512;
+    } else if (s.bj == 128) {
+        k = of_kind<128, 128, 2, 2>(kind);
+    } else if (s.bj == 64) {
+        k = of_kind<128, 64, 2, 2>(kind);
+    } else if (s.bj == 32) {
+        k = of_kind<128, 32, 4, 1>(kind);
+    } else {
+        k = of_kind<128, 16, 4, 1>(kind);
+    }
+    const int64_t grid = (int64_t)s.tiles_i * s.tiles_j * s.splits;
+    tide_status st = launch(k, grid, threads, stream, p);
+    if (st != TIDE_OK || s.splits == 1) return st;
+    return launch(join_kernel, ceil_div(p.e.J * p.partial_pitch / 8, kJoinThreads), kJoinThreads,
+                  stream, p);
+}
+
+// Whether the kernels can read rows of this matrix where they lie.
+bool direct(const void* p, int64_t ld, int64_t rows, int64_t cols) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && cols % 8 == 0 && (rows <= 1 || ld % 8 == 0);
+}
+
+tide_status pad(const void* in, int64_t ld, int64_t rows, int64_t cols, uint16_t* out,
+                tide_stream_t stream) {
+    const int64_t width = round_up(cols, 8);
+    return launch(pad_kernel, ceil_div(rows * (width / 8), kPadThreads), kPadThreads, stream,
+                  static_cast<const uint16_t*>(in), ld, rows, cols, out, width);
+}
+
+// An operand: the matrix itself, or its copy in the workspace.
+struct Source {
+    const void* p;
+    int64_t ld, rows, cols;
+    uint16_t* copy = nullptr;
+    bool copied = false;
+    void plan(Carver& c) {
+        copied = rows > 0 && cols > 0 && !direct(p, ld, rows, cols);
+        if (copied) copy = c.take<uint16_t>(rows * round_up(cols, 8));
+    }
+    tide_status fill(tide_stream_t stream) const {
+        return copied ? pad(p, ld, rows, cols, copy, stream) : TIDE_OK;
+    }
+    // `count` is what the tile loop calls it: the rows, or the columns
+    Operand operand(bool columns) const {
+        const int64_t width = round_up(cols, 8);
+        Operand o;
+        o.p = copied ? copy : static_cast<const uint16_t*>(p);
+        o.ld = copied || rows <= 1 ? width : ld;
+        o.count = columns ? width : rows;
+        o.depth = columns ? rows : width;
+        return o;
+    }
+};
+
+tide_status check_dims(int64_t T, int64_t N, int64_t K, int32_t act, int32_t reserved) {
+    if (T < 0 || N < 0 || K < 0 || act < TIDE_ACT_NONE || act > TIDE_ACT_SILU || reserved != 0)
+        return TIDE_EINVAL;
+    if (T > kMaxTokens || N > kMaxWidth || K > kMaxWidth) return TIDE_EUNSUPPORTED;
+    return TIDE_OK;
+}
+
+tide_status check_kept(const void* p, int64_t rows, int64_t cols) {
+    if (rows == 0 || cols == 0) return TIDE_OK;
+    if (!p) return TIDE_EINVAL;
+    return reinterpret_cast<uintptr_t>(p) % 16 ? TIDE_EALIGN : TIDE_OK;
+}
+
+// No output shares a byte with an input or another output.
+tide_status check_apart(const Extent* in, int n_in, const Extent* out, int n_out) {
+    for (int a = 0; a < n_out; ++a) {
+        for (int b = 0; b < n_in; ++b)
+            if (overlaps(out[a], in[b])) return TIDE_EOVERLAP;
+        for (int b = 0; b < a; ++b)
+            if (overlaps(out[a], out[b])) return TIDE_EOVERLAP;
+    }
+    return TIDE_OK;
+}
+
+tide_status check_workspace(void* ws, size_t have, int64_t need, const Extent* other, int n) {
+    if (need == 0) return TIDE_OK;
+    if (!ws || have < (size_t)need) return TIDE_ENOSPACE;
+    if (reinterpret_cast<uintptr_t>(ws) % 16) return TIDE_EALIGN;
+    const Extent e = bytes_extent(ws, need);
+    for (int k = 0; k < n; ++k)
+        if (overlaps(e, other[k])) return TIDE_EOVERLAP;
+    return TIDE_OK;
+}
+
+#define TIDE_TRY(call)                                \
+    do {                                              \
+        const tide_status try_st = (call);            \
+        if (try_st != TIDE_OK) return try_st;         \
+    } while (0)
+
+// ---- forward -------------------------------------------------------------
+
+struct ForwardPlan {
+    Source x, w;
+    Shape shape;
+    float* partial;
+    int64_t bytes;
+};
+
+tide_status check_forward(const tide_linear_forward_args& a) {
+    TIDE_TRY(check_dims(a.tokens, a.out_features, a.in_features, a.act, a.reserved));
+    const int64_t T = a.tokens, N = a.out_features, K = a.in_features;
+    if (T == 0 || N == 0) return TIDE_OK;
+    TIDE_TRY(check_rows(a.x, a.ldx, T, K));
+    TIDE_TRY(check_rows(a.weight, K, N, K));
+    if (a.bias) TIDE_TRY(check_rows(a.bias, N, 1, N));
+    if (a.residual) TIDE_TRY(check_rows(a.residual, a.ldr, T, N));
+    TIDE_TRY(check_rows(a.y, a.ldy, T, N));
+    if (a.z_kept) TIDE_TRY(check_kept(a.z_kept, T, N));
+    return TIDE_OK;
+}
+
+int forward_extents(const tide_linear_forward_args& a, Extent* in, Extent* out) {
+    const int64_t T = a.tokens, N = a.out_features, K = a.in_features;
+    const bool in_place = a.residual == a.y && (T <= 1 || a.ldr == a.ldy);
+    in[0] = rows_extent(a.x, a.ldx, T, K);
+    in[1] = rows_extent(a.weight, K, N, K);
+    in[2] = rows_extent(a.bias, N, 1, N);
+    in[3] = in_place ? Extent() : rows_extent(a.residual, a.ldr, T, N);
+    out[0] = rows_extent(a.y, a.ldy, T, N);
+    out[1] = bytes_extent(a.z_kept, act8_bytes(T, N));
+    return 4;
+}
+
+ForwardPlan plan_forward(const tide_linear_forward_args& a, void* ws) {
+    ForwardPlan f;
+    Carver c{static_cast<char*>(ws)};
+    const int64_t T = a.tokens, N = a.out_features, K = a.in_features;
+    f.x = {a.x, a.ldx, T, K};
+    f.w = {a.weight, K, N, K};
+    f.x.plan(c);
+    f.w.plan(c);
+    f.shape = choose(N, T, round_up(K, 8));
+    f.partial = c.take<float>(partial_floats(f.shape, N, T));
+    f.bytes = c.used;
+    return f;
+}
+
+}  // namespace
+
+extern "C" tide_status tide_linear_forward_workspace(const tide_linear_forward_args* args,
+                                                     size_t* bytes) {
+    if (!args || !bytes) return TIDE_EINVAL;
+    TIDE_TRY(check_forward(*args));
+    *bytes = args->tokens && args->out_features ? (size_t)plan_forward(*args, nullptr).bytes : 0;
+    return TIDE_OK;
+}
+
+extern "C" tide_status tide_linear_forward(const tide_linear_forward_args* args, void* workspace,
+                                           size_t workspace_bytes, tide_stream_t stream) {
+    if (!args) return TIDE_EINVAL;
+    const tide_linear_forward_args& a = *args;
+    TIDE_TRY(check_forward(a));
+    const int64_t T = a.tokens, N = a.out_features, K = a.in_features;
+    if (T == 0 || N == 0) return TIDE_OK;
+    Extent ext[6];
+    const int n_in = forward_extents(a, ext, ext + 4);
+    TIDE_TRY(check_apart(ext, n_in, ext + 4, 2));
+    const ForwardPlan f = plan_forward(a, workspace);
+    TIDE_TRY(check_workspace(workspace, workspace_bytes, f.bytes, ext, 6));
+    TIDE_TRY(check_stream_device(stream));
+    TIDE_TRY(f.x.fill(stream));
+    TIDE_TRY(f.w.fill(stream));
+    Product p = {};
+    p.A = f.w.operand(false);
+    p.B = f.x.operand(false);
+    p.depth = round_up(K, 8);
+    p.e.I = N;
+    p.e.J = T;
+    p.e.out = static_cast<uint16_t*>(a.y);
+    p.e.ldo = a.ldy;
+    p.e.bias = static_cast<const uint16_t*>(a.bias);
+    p.e.res = static_cast<const uint16_t*>(a.residual);
+    p.e.ldr = a.ldr;
+    p.e.kept = static_cast<uint8_t*>(a.z_kept);
+    p.e.act = a.act;
+    return run_product(kForward, p, f.shape, f.partial, stream);
+}
+
+// ---- backward ------------------------------------------------------------
+
+namespace {
+
+struct BackwardPlan {
+    bool make_dz;       // dz is written (to the workspace), not dy itself
+    int64_t width;      // of dz's rows there
+    int64_t chunk, chunks;
+    Source w;
+    uint16_t* dz = nullptr;
+    float* sums = nullptr;
+    uint16_t* x = nullptr;  // x in bf16, rows of `x_width`
+    int64_t x_width;
+    Shape in_shape, w_shape;
+    float* partial = nullptr;
+    int64_t bytes;
+};
+
+tide_status check_backward(const tide_linear_backward_args& a) {
+    TIDE_TRY(check_dims(a.tokens, a.out_features, a.in_features, a.act, a.reserved));
+    const int64_t T = a.tokens, N = a.out_features, K = a.in_features;
+    if (!a.dx && !a.dweight && !a.dbias) return TIDE_OK;
+    TIDE_TRY(check_rows(a.dy, a.lddy, T, N));
+    if (a.act != TIDE_ACT_NONE) TIDE_TRY(check_kept(a.z_kept, T, N));
+    if (a.dx) {
+        TIDE_TRY(check_rows(a.weight, K, N, K));
+        TIDE_TRY(check_rows(a.dx, a.lddx, T, K));
+    }
+    if (a.dweight) {
+        TIDE_TRY(check_kept(a.x_kept, T, K));
+        TIDE_TRY(check_rows(a.dweight, K, N, K));
+    }
+    if (a.dbias) TIDE_TRY(check_rows(a.dbias, N, 1, N));
+    return TIDE_OK;
+}
+
+BackwardPlan plan_backward(const tide_linear_backward_args& a, void* ws) {
+    BackwardPlan b;
+    Carver c{static_cast<char*>(ws)};
+    const int64_t T = a.tokens, N = a.out_features, K = a.in_features;
+    const bool products = (a.dx && T && K) || (a.dweight && N && K);
+    b.make_dz = products && T && N && (a.act != TIDE_ACT_NONE || !direct(a.dy, a.lddy, T, N));
+    b.width = round_up(N, 8);
+    if (b.make_dz) b.dz = c.take<uint16_t>(T * b.width);
+    // Chunks of rows for the column sums: enough workgroups to fill the chip,
+    // at most 256 chunks for the second pass to add up.
+    const int64_t groups = ceil_div(std::max<int64_t>(N, 1), kDzCols);
+    b.chunk = std::max<int64_t>(8, round_up(ceil_div(T, std::min<int64_t>(256, std::max<int64_t>(1, 2048 / groups))), 8));
+    b.chunks = ceil_div(T, b.chunk);
+    if (a.dbias) b.sums = c.take<float>(b.chunks * N);
+    b.w = {a.weight, K, a.dx && T ? N : 0, K};
+    b.w.plan(c);
+    b.x_width = act8_pitch(K);
+    if (a.dweight && N) b.x = c.take<uint16_t>(T * b.x_width);
+    b.in_shape = choose(K, T, b.width);
+    b.w_shape = choose(K, N, T);
+    int64_t floats = 0;
+    if (a.dx) floats = std::max(floats, partial_floats(b.in_shape, K, T));
+    if (a.dweight) floats = std::max(floats, partial_floats(b.w_shape, K, N));
+    b.partial = c.take<float>(floats);
+    b.bytes = c.used;
+    return b;
+}
+
+}  // namespace
+
+extern "C" tide_status tide_linear_backward_workspace(const tide_linear_backward_args* args,
+                                                      size_t* bytes) {
+    if (!args || !bytes) return TIDE_EINVAL;
+    TIDE_TRY(check_backward(*args));
+    *bytes = (size_t)plan_backward(*args, nullptr).bytes;
+    return TIDE_OK;
+}
+
+extern "C" tide_status tide_linear_backward(const tide_linear_backward_args* args, void* workspace,
+                                            size_t workspace_bytes, tide_stream_t stream) {
+    if (!args) return TIDE_EINVAL;
+    const tide_linear_backward_args& a = *args;
+    TIDE_TRY(check_backward(a));
+    if (!a.dx && !a.dweight && !a.dbias) return TIDE_OK;
+    const int64_t T = a.tokens, N = a.out_features, K = a.in_features;
+    Extent ext[7] = {rows_extent(a.dy, a.lddy, T, N),
+                     a.dx ? rows_extent(a.weight, K, N, K) : Extent(),
+                     a.dweight ? bytes_extent(a.x_kept, act8_bytes(T, K)) : Extent(),
+                     a.act != TIDE_ACT_NONE ? bytes_extent(a.z_kept, act8_bytes(T, N)) : Extent(),
+                     rows_extent(a.dx, a.lddx, T, K),
+                     rows_extent(a.dweight, K, N, K),
+                     rows_extent(a.dbias, N, 1, N)};
+    TIDE_TRY(check_apart(ext, 4, ext + 4, 3));
+    const BackwardPlan b = plan_backward(a, workspace);
+    TIDE_TRY(check_workspace(workspace, workspace_bytes, b.bytes, ext, 7));
+    TIDE_TRY(check_stream_device(stream));
+
+    if (T && N && (b.make_dz || a.dbias)) {
+        DzArgs d = {};
+        d.dy = static_cast<const uint16_t*>(a.dy);
+        d.ld = a.lddy;
+        d.z = a.act != TIDE_ACT_NONE ? static_cast<const uint8_t*>(a.z_kept) : nullptr;
+        d.dz = b.make_dz ? b.dz : nullptr;
+        d.width = b.width;
+        d.sums = b.sums;
+        d.T = T;
+        d.N = N;
+        d.chunk = b.chunk;
+        d.col_groups = (int32_t)ceil_div(N, kDzCols);
+        d.act = a.act;
+        TIDE_TRY(launch(dz_kernel, d.col_groups * b.chunks, kDzThreads, stream, d));
+    }
+    if (a.dbias && N)
+        TIDE_TRY(launch(dbias_kernel, ceil_div(N, 256), 256, stream,
+                        static_cast<const float*>(b.sums), b.chunks, N,
+                        static_cast<uint16_t*>(a.dbias)));
+    if (K == 0) return TIDE_OK;
+
+    Source dz = {b.make_dz ? b.dz : a.dy, b.make_dz ? b.width : a.lddy, T, b.make_dz ? b.width : N};
+    if (a.dx && T) {
+        TIDE_TRY(b.w.fill(stream));
+        Product p = {};
+        p.A = b.w.operand(true);
+        p.B = dz.operand(false);
+        p.depth = b.width;  // dz's columns behind the N-th are 0
+        p.e.I = K;
+        p.e.J = T;
+        p.e.out = static_cast<uint16_t*>(a.dx);
+        p.e.ldo = a.lddx;
+        TIDE_TRY(run_product(kGradInput, p, b.in_shape, b.partial, stream));
+    }
+    if (a.dweight && N) {
+        if (T) TIDE_TRY(tide_act8_unpack(a.x_kept, T, K, b.x, b.x_width, stream));
+        Source x = {b.x, b.x_width, T, K};
+        Product p = {};
+        p.A = x.operand(true);
+        p.B = dz.operand(true);
+        p.depth = T;
+        p.e.I = K;
+        p.e.J = N;
+        p.e.out = static_cast<uint16_t*>(a.dweight);
+        p.e.ldo = K;
+        TIDE_TRY(run_product(kGradWeight, p, b.w_shape, b.partial, stream));
+    }
+    return TIDE_OK;
+}

@@ -1,0 +1,237 @@
+// tile_product.h -- the matrix-core tile loop behind the layer products
+// (linear.hip), for gfx950.
+//
+// One workgroup computes D[i, j] = sum over k of A[i, k] B[j, k] for a BI x BJ
+// tile.  i is always the index along which the product's output is
+// contiguous: the 16x16x32 matrix instruction leaves 4 consecutive rows of D
+// in a lane, so with A's index as the row a lane ends with 4 consecutive
+// output elements.  The layer's three products are this
+// one, with operands whose contraction index runs along memory ("rows": A[i]
+// is a row) or across it ("columns": row k of memory holds A[., k]):
+//   forward  y[t, n]:  A = W rows,       B = x rows
+//   dx[t, k]:          A = W columns,    B = dz rows
+//   dW[n, k]:          A = x columns,    B = dz columns
+//
+// Operands go from memory to LDS without passing registers (16 bytes a lane);
+// the LDS side of such a load is contiguous over the wave, so the bank
+// swizzle is put on the memory side: a lane fetches the 16-byte chunk that
+// belongs at its place.  A "rows" tile holds 64 k of each index as 8 chunks,
+// chunk c of row r at place c ^ (r & 7), read with 16-byte LDS reads.  A
+// "columns" tile holds BI (BJ) indices of each k, 16 indices (32 bytes) at a
+// time at place p ^ swizzle(k); the transposing LDS read gives each lane 4
+// consecutive k of its index, and the 8 rows of k that two 16-lane groups
+// read together lie in 8 different 32-byte places.
+//
+// Loads go through buffer descriptors that end at the operand's last
+// element: rows past the end read as 0 and need no branch.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace tide {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+
+#define TIDE_LDS __attribute__((address_space(3)))
+
+constexpr int kStepK = 64;  // contraction elements of one staged tile
+
+// An operand as the kernel reads it: 16-byte aligned, ld % 8 == 0, and either
+// (rows) `count` rows of `depth` contraction elements, or (columns) `depth`
+// rows of `count` elements; the contiguous length is a multiple of 8.  Of two
+// operands one may be up to 7 contraction elements longer than the other,
+// whose missing elements read as 0 (the longer one's then have to be finite).
+struct Operand {
+    const uint16_t* p;
+    int64_t ld;
+    int64_t count;
+    int64_t depth;
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* base, int64_t bytes) {
+    const int64_t most = (int64_t)1 << 31;
+    const int32_t n = (int32_t)(uint32_t)(bytes < 0 ? 0 : bytes > most ? most : bytes);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, n, 0x00020000);
+}
+
+constexpr uint32_t kNowhere = 0xf0000000u;  // an offset past every descriptor's end
+
+// A tile of N indices from `first` on, staged by WAVES waves.
+template <int N, int WAVES, bool COLUMNS>
+struct Stager {
+    static constexpr int kBytes = N * kStepK * 2;
+    static constexpr int kLoads = kBytes / 1024;                       // of a whole wave
+    static constexpr int kMine = (kLoads + WAVES - 1) / WAVES;
+    static constexpr int kRowChunks = COLUMNS ? N / 8 : kStepK / 8;    // 16-byte chunks of a row
+    static constexpr int kPairMask = COLUMNS ? (N / 16 < 8 ? N / 16 - 1 : 7) : 0;
+
+    const char* base;
+    int64_t step;        // bytes from one k tile to the next
+    int64_t left;        // bytes from base to the operand's end
+    uint32_t offset[kMine];
+    int wave;
+    int chunk_k;         // rows: first contraction element of the lane's chunk
+
+    __device__ __forceinline__ static int swizzle(int k) {
+        return ((k & 3) | ((k >> 1) & 4)) & kPairMask;
+    }
+
+    __device__ __forceinline__ void init(const Operand& o, int64_t first, int64_t k0, int lane,
+                                         int wave_) {
+        wave = wave_;
+        chunk_k = 0;
+        if constexpr (COLUMNS) {
+            base = reinterpret_cast<const char*>(o.p + k0 * o.ld + first);
+            left = 2 * ((o.depth - k0 - 1) * o.ld + o.count - first);
+            step = 2 * kStepK * o.ld;
+        } else {
+            base = reinterpret_cast<const char*>(o.p + first * o.ld + k0);
+            left = 2 * ((o.count - first - 1) * o.ld + o.depth - k0);
+            step = 2 * kStepK;
+        }
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) {
+            const int place = (q * WAVES + wave) * 64 + lane;
+            const int row = place / kRowChunks, at = place % kRowChunks;
+            int c;
+            if constexpr (COLUMNS) {
+                c = at ^ (swizzle(row) << 1);
+            } else {
+                c = at ^ (row & 7);
+                chunk_k = c * 8;  // the same for every q: WAVES * 64 / 8 rows keep row & 7
+            }
+            offset[q] = (uint32_t)((int64_t)row * o.ld * 2 + c * 16);
+        }
+    }
+
+    // Stage the current k tile into `lds` and move on to the next.  valid:
+    // contraction elements left from the tile's first on.
+    __device__ __forceinline__ void stage(TIDE_LDS char* lds, int64_t valid) {
+        const __amdgpu_buffer_rsrc_t r = resource(base, left);
+        // a "columns" tile's rows past the end are past the descriptor's end
+        const bool none = !COLUMNS && valid < kStepK && chunk_k >= valid;
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) {
+            const int load = q * WAVES + wave;
+            if (kLoads % WAVES && load >= kLoads) break;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                r, lds + load * 1024, 16, none ? kNowhere : offset[q], 0, 0, 0);
+        }
+        base += step;
+        left -= step;
+    }
+};
+
+// The 16 x 32 piece of a staged tile that a matrix instruction takes: index
+// m0 + (lane & 15), contraction k = 32 * s + 8 * (lane >> 4) .. + 7.
+template <int N, bool COLUMNS>
+struct Reader {
+    template <int S>
+    __device__ __forceinline__ static bf16x8 read(const TIDE_LDS char* lds, int m0, int lane) {
+        if constexpr (COLUMNS) {
+            constexpr int kRow = 2 * N;
+            const int g = lane >> 4, i = lane & 15;
+            const int k = 32 * S + 8 * g + (i >> 2);
+            const int pair = (m0 >> 4) ^ Stager<N, 1, true>::swizzle(k);
+            const TIDE_LDS char* p = lds + k * kRow + pair * 32 + (i & 3) * 8;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TIDE_LDS s16x4*)p);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TIDE_LDS s16x4*)(p + 4 * kRow));
+            const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            return __builtin_bit_cast(bf16x8, v);
+        } else {
+            const int row = m0 + (lane & 15);
+            const int c = (4 * S + (lane >> 4)) ^ (lane & 7);
+            return *(const TIDE_LDS bf16x8*)(lds + row * (2 * kStepK) + c * 16);
+        }
+    }
+};
+
+// One staged k tile into a wave's TI x TJ accumulators.
+template <int BI, int BJ, int TI, int TJ, bool CA, bool CB>
+__device__ __forceinline__ void multiply(const TIDE_LDS char* la, const TIDE_LDS char* lb, int i0,
+                                         int j0, int lane, f32x4v (&acc)[TI][TJ]) {
+    bf16x8 a[TI], b[TJ];
+#pragma unroll
+    for (int t = 0; t < TI; ++t) a[t] = Reader<BI, CA>::template read<0>(la, i0 + 16 * t, lane);
+#pragma unroll
+    for (int t = 0; t < TJ; ++t) b[t] = Reader<BJ, CB>::template read<0>(lb, j0 + 16 * t, lane);
+#pragma unroll
+    for (int x = 0; x < TI; ++x)
+#pragma unroll
+        for (int y = 0; y < TJ; ++y)
+            acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[x], b[y], acc[x][y], 0, 0, 0);
+#pragma unroll
+    for (int t = 0; t < TI; ++t) a[t] = Reader<BI, CA>::template read<1>(la, i0 + 16 * t, lane);
+#pragma unroll
+    for (int t = 0; t < TJ; ++t) b[t] = Reader<BJ, CB>::template read<1>(lb, j0 + 16 * t, lane);
+#pragma unroll
+    for (int x = 0; x < TI; ++x)
+#pragma unroll
+        for (int y = 0; y < TJ; ++y)
+            acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[x], b[y], acc[x][y], 0, 0, 0);
+}
+
+// Every load into LDS has landed and every LDS read has returned, in every
+// wave: the staged tile can be read and the other one overwritten.
+__device__ __forceinline__ void tile_barrier() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Stage the next k tile and multiply the current one.  The two lie in
+// different halves of LDS, and saying so (__restrict__) keeps the compiler
+// from making the reads wait for the loads.
+template <int BI, int BJ, int TI, int TJ, bool CA, bool CB, typename SA, typename SB>
+__device__ __forceinline__ void tile_step(TIDE_LDS char* __restrict__ next,
+                                          const TIDE_LDS char* __restrict__ now, bool more, SA& sa,
+                                          SB& sb, int64_t valid, int wi, int wj, int lane,
+                                          f32x4v (&acc)[TI][TJ]) {
+    if (more) {
+        sa.stage(next, valid);
+        sb.stage(next + SA::kBytes, valid);
+    }
+    multiply<BI, BJ, TI, TJ, CA, CB>(now, now + SA::kBytes, wi, wj, lane, acc);
+}
+
+// The loop over the contraction elements [k0, k1) of `depth` (the longer
+// operand's) of the tile at (i0, j0),
+// two tiles in LDS: one is read while the next one arrives.
+template <int BI, int BJ, int WI, int WJ, bool CA, bool CB>
+__device__ __forceinline__ void tile_loop(const Operand& A, const Operand& B, int64_t depth,
+                                          int64_t k0, int64_t k1, int64_t i0, int64_t j0,
+                                          TIDE_LDS char* lds,
+                                          f32x4v (&acc)[BI / WI / 16][BJ / WJ / 16]) {
+    constexpr int kWaves = WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
+    using SA = Stager<BI, kWaves, CA>;
+    using SB = Stager<BJ, kWaves, CB>;
+    constexpr int kTile = SA::kBytes + SB::kBytes;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wi = (wave / WJ) * TI * 16, wj = (wave % WJ) * TJ * 16;
+    SA sa;
+    SB sb;
+    sa.init(A, i0, k0, lane, wave);
+    sb.init(B, j0, k0, lane, wave);
+#pragma unroll
+    for (int x = 0; x < TI; ++x)
+#pragma unroll
+        for (int y = 0; y < TJ; ++y) acc[x][y] = 0;
+    if (k0 >= k1) return;
+    const int steps = (int)((k1 - k0 + kStepK - 1) / kStepK);
+    int64_t valid = depth - k0;
+    sa.stage(lds, valid);
+    sb.stage(lds + SA::kBytes, valid);
+    int at = 0;
+    for (int s = 0; s < steps; ++s) {
+        tile_barrier();
+        valid -= kStepK;
+        tile_step<BI, BJ, TI, TJ, CA, CB>(lds + (at ^ kTile), lds + at, s + 1 < steps, sa, sb, valid,
+                                          wi, wj, lane, acc);
+        at ^= kTile;
+    }
+}
+
+}  // namespace tide
