@@ -77,4 +77,16 @@ __device__ __forceinline__ void act8_unpack4(uint32_t w, float s, float (&v)[4])
     v[3] = hi.y * s;
 }
 
+__device__ __forceinline__ void act8_unpack8(uint32_t __attribute__((ext_vector_type(2))) w, float s,
+                                             float (&v)[8]) {
+    float lo[4], hi[4];
+    act8_unpack4(w.x, s, lo);
+    act8_unpack4(w.y, s, hi);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        v[k] = lo[k];
+        v[k + 4] = hi[k];
+    }
+}
+
 }  // namespace tide

@@ -91,11 +91,8 @@ __global__ __launch_bounds__(kThreads) void unpack_kernel(const uint8_t* in, int
     for (int k = 0; k < kUnits; ++k) {
         if (at[k].row >= rows) continue;
         const int64_t c = (int64_t)at[k].unit * 8;
-        const float scale = act8_scale(s[k]);
-        float lo[4], hi[4];
-        act8_unpack4(q[k].x, scale, lo);
-        act8_unpack4(q[k].y, scale, hi);
-        const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        float v[8];
+        act8_unpack8(q[k], act8_scale(s[k]), v);
         store8(x + at[k].row * ldx + c, cols - c, v);
     }
 }

@@ -31,35 +31,62 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kTanhA = 0.044715f;
 
-// 1 / (1 + exp(-u)); 0.5 (1 + tanh(v)) is this at u = 2 v, so the tanh form
-// of gelu is z * sigmoid(2 sqrt(2/pi) (z + 0.044715 z^3)).
-__device__ __forceinline__ float sigmoid(float u) { return 1.0f / (1.0f + __expf(-u)); }
+// 1 / (1 + exp(-u)), off by a few binary32 steps; 0.5 (1 + tanh(v)) is this at
+// u = 2 v, so the tanh form of gelu is z * sigmoid(2 sqrt(2/pi) (z + 0.044715 z^3)).
+// The reciprocal instruction is within one step; a division written out would
+// be most of the epilogue's work.
+__device__ __forceinline__ float sigmoid(float u) {
+    return __builtin_amdgcn_rcpf(1.0f + __expf(-u));
+}
 
-__device__ __forceinline__ float act_value(float z, int act) {
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+    if constexpr (ACT == TIDE_ACT_RELU) return z > 0.0f ? z : 0.0f * z;
+    if constexpr (ACT == TIDE_ACT_GELU) return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+    if constexpr (ACT == TIDE_ACT_GELU_TANH) return z * sigmoid(kTanhC * (z + kTanhA * z * z * z));
+    if constexpr (ACT == TIDE_ACT_SILU) return z * sigmoid(z);
+    return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+    if constexpr (ACT == TIDE_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f * z;
+    if constexpr (ACT == TIDE_ACT_GELU)
+        return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * __expf(-0.5f * z * z) * kInvSqrt2Pi;
+    if constexpr (ACT == TIDE_ACT_GELU_TANH) {
+        const float s = sigmoid(kTanhC * (z + kTanhA * z * z * z));
+        // where the sigmoid is 0 or 1 the polynomial may be infinite already
+        const float q = s * (1.0f - s);
+        return s + (q > 0.0f ? z * q * kTanhC * (1.0f + 3.0f * kTanhA * z * z) : 0.0f);
+    }
+    if constexpr (ACT == TIDE_ACT_SILU) {
+        const float s = sigmoid(z);
+        return s * (1.0f + z * (1.0f - s));
+    }
+    return 1.0f;
+}
+
+// v to act(v), eight at a time: the choice is made once for all of them.
+template <int ACT>
+__device__ __forceinline__ void apply_act(float (&v)[8]) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) v[r] = act_value<ACT>(v[r]);
+}
+__device__ __forceinline__ void apply_act(float (&v)[8], int act) {
     switch (act) {
-        case TIDE_ACT_RELU: return z > 0.0f ? z : 0.0f * z;
-        case TIDE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
-        case TIDE_ACT_GELU_TANH: return z * sigmoid(kTanhC * (z + kTanhA * z * z * z));
-        case TIDE_ACT_SILU: return z * sigmoid(z);
-        default: return z;
+        case TIDE_ACT_RELU: return apply_act<TIDE_ACT_RELU>(v);
+        case TIDE_ACT_GELU: return apply_act<TIDE_ACT_GELU>(v);
+        case TIDE_ACT_GELU_TANH: return apply_act<TIDE_ACT_GELU_TANH>(v);
+        case TIDE_ACT_SILU: return apply_act<TIDE_ACT_SILU>(v);
+        default: return;
     }
 }
 
-__device__ __forceinline__ float act_slope(float z, int act) {
-    switch (act) {
-        case TIDE_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f * z;
-        case TIDE_ACT_GELU:
-            return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * __expf(-0.5f * z * z) * kInvSqrt2Pi;
-        case TIDE_ACT_GELU_TANH: {
-            const float s = sigmoid(kTanhC * (z + kTanhA * z * z * z));
-            return s + z * s * (1.0f - s) * kTanhC * (1.0f + 3.0f * kTanhA * z * z);
-        }
-        case TIDE_ACT_SILU: {
-            const float s = sigmoid(z);
-            return s * (1.0f + z * (1.0f - s));
-        }
-        default: return 1.0f;
-    }
+// v times act'(z).
+template <int ACT>
+__device__ __forceinline__ void apply_slope(const float (&z)[8], float (&v)[8]) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) v[r] *= act_slope<ACT>(z[r]);
 }
 
 // ---- epilogue ------------------------------------------------------------
@@ -111,10 +138,7 @@ __device__ __forceinline__ void finish(const Epilogue& e, int64_t i, int64_t j, 
         }
     }
     if (n <= 0) return;
-    if (e.act != TIDE_ACT_NONE) {
-#pragma unroll
-        for (int r = 0; r < 8; ++r) v[r] = act_value(v[r], e.act);
-    }
+    apply_act(v, e.act);
     if (e.res) {
         float x[8];
         load8(e.res + j * e.ldr + i, n, x);
@@ -239,6 +263,232 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(Product p) {
     finish(p.e, i, j, there, v);
 }
 
+// ---- forward for one to four tokens -----------------------------------------
+
+// The weight's bytes bound this product, and how fast they come depends on how
+// they are asked for: of W's rows of 16 KB, reads of 64 bytes of 16 rows an
+// instruction reach 4.7 TB/s, 1 KB of one row an instruction in runs of 1 KB a
+// row 5.3, in runs of 4 KB 6.6 (nontemporal; plain loads 0.5 less).  So a
+// workgroup takes 8 rows, its 4 waves side by side 4 KB of each at a time; a
+// lane multiplies its 8 elements of every row by its 8 elements of each
+// token in binary32 and the lanes' sums are added at the end.
+struct Gemv {
+    const uint16_t* x;
+    int64_t ldx;
+    const uint16_t* w;
+    int64_t K;
+    Epilogue e;  // I = N, J = T
+};
+
+constexpr int kGemvRows = 8;
+constexpr int kGemvThreads = 256;
+
+__device__ __forceinline__ u32x4v load_once(const uint16_t* p) {
+    return __builtin_nontemporal_load((const TIDE_GLOBAL_AS u32x4_any*)p);
+}
+
+__device__ __forceinline__ void widen(u32x4v w, float (&v)[8]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        v[2 * k] = bf16_lo(w[k]);
+        v[2 * k + 1] = bf16_hi(w[k]);
+    }
+}
+
+template <int T>
+__global__ __launch_bounds__(kGemvThreads, 4) void gemv_kernel(Gemv p) {
+    __shared__ float part[kGemvThreads / 64][T][kGemvRows];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n0 = (int64_t)blockIdx.x * kGemvRows;
+    const int64_t c = (int64_t)threadIdx.x * 8;
+    const uint16_t* w[kGemvRows];
+#pragma unroll
+    for (int r = 0; r < kGemvRows; ++r) w[r] = p.w + min(n0 + r, p.e.I - 1) * p.K + c;
+    const uint16_t* x[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) x[t] = p.x + min((int64_t)t, p.e.J - 1) * p.ldx + c;
+    float acc[kGemvRows][T] = {};
+    // elements k .. k + 7 of the lane's piece, of which the first `seen` do not count
+    auto step = [&](int64_t k, int seen) __attribute__((always_inline)) {
+        u32x4v wv[kGemvRows], xv[T];
+#pragma unroll
+        for (int r = 0; r < kGemvRows; ++r) wv[r] = load_once(w[r] + k);
+#pragma unroll
+        for (int t = 0; t < T; ++t) xv[t] = *(const TIDE_GLOBAL_AS u32x4_any*)(x[t] + k);
+#pragma unroll
+        for (int r = 0; r < kGemvRows; ++r) {
+            float v[8];
+            widen(wv[r], v);
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                float u[8];
+                widen(xv[t], u);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    acc[r][t] = __builtin_fmaf(q < seen ? 0.0f : v[q], q < seen ? 0.0f : u[q], acc[r][t]);
+            }
+        }
+    };
+    int64_t k = 0;
+#pragma unroll 1
+    for (; k + c + 8 <= p.K; k += kGemvThreads * 8) step(k, 0);
+    // the one lane whose piece ends inside: the row's last 8 elements, those
+    // that the lane before it has had left out
+    if (k + c < p.K) step(p.K - 8 - c, (int)(k + c + 8 - p.K));
+#pragma unroll
+    for (int r = 0; r < kGemvRows; ++r)
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            float s = acc[r][t];
+#pragma unroll
+            for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+            if (lane == 0) part[wave][t][r] = s;
+        }
+    __syncthreads();
+    if (threadIdx.x >= T) return;
+    float v[kGemvRows];
+#pragma unroll
+    for (int r = 0; r < kGemvRows; ++r) {
+        v[r] = part[0][threadIdx.x][r];
+#pragma unroll
+        for (int u = 1; u < kGemvThreads / 64; ++u) v[r] += part[u][threadIdx.x][r];
+    }
+    finish(p.e, n0, threadIdx.x, threadIdx.x < p.e.J, v);
+}
+
+// ---- forward for few tokens ------------------------------------------------
+
+// With at most 32 tokens the weight's bytes bound the product, and it is read
+// straight from memory into the matrix instructions' registers: a wave takes
+// 32 of W's rows, 128 contraction elements at a time, the next 128 in flight
+// while these are multiplied.  The waves of a workgroup share the 32 rows and
+// take the 128-element pieces in turn, so that they read runs of whole rows;
+// their sums meet in LDS, in the waves' order, before the epilogue.  Loads need
+// no alignment.
+struct Few {
+    const uint16_t* x;
+    int64_t ldx;
+    const uint16_t* w;
+    int64_t K;
+    Epilogue e;  // I = N, J = T
+};
+
+constexpr int kFewRows = 32;
+constexpr int kFewStep = 128;
+constexpr int kFewPitch = kFewRows + 4;  // floats of a token's sums in LDS
+
+__device__ __forceinline__ bf16x8 load_frag(const uint16_t* p) {
+    return __builtin_bit_cast(bf16x8, *(const TIDE_GLOBAL_AS u32x4_any*)p);
+}
+// The first n of 8 elements, the others 0.
+__device__ __forceinline__ bf16x8 load_frag(const uint16_t* p, int64_t n) {
+    if (n >= 8) return load_frag(p);
+    s16x8 v;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        v[k] = k < n ? (short)*(const TIDE_GLOBAL_AS uint16_t*)(p + k) : (short)0;
+    return __builtin_bit_cast(bf16x8, v);
+}
+
+template <int TJ>
+__global__ __launch_bounds__(512) void few_kernel(Few p) {
+    extern __shared__ __attribute__((aligned(16))) float sums[];  // [waves][16 TJ][kFewPitch]
+    constexpr int kSteps = kFewStep / 32;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int waves = blockDim.x >> 6;
+    const int r = lane & 15, g = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * kFewRows;
+    // rows and tokens past the last one repeat it; their sums are not stored
+    const uint16_t* w[2];
+    const uint16_t* x[TJ];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) w[h] = p.w + min(n0 + 16 * h + r, p.e.I - 1) * p.K + g * 8;
+#pragma unroll
+    for (int y = 0; y < TJ; ++y) x[y] = p.x + min((int64_t)(16 * y + r), p.e.J - 1) * p.ldx + g * 8;
+
+    struct Piece {
+        bf16x8 w[2][kSteps], x[TJ][kSteps];
+    };
+    f32x4v acc[2][TJ];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int y = 0; y < TJ; ++y) acc[h][y] = 0;
+    auto load = [&](Piece& f, int64_t k) __attribute__((always_inline)) {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) f.w[h][s] = load_frag(w[h] + k + 32 * s);
+#pragma unroll
+            for (int y = 0; y < TJ; ++y) f.x[y][s] = load_frag(x[y] + k + 32 * s);
+        }
+    };
+    auto multiply = [&](const Piece& f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int y = 0; y < TJ; ++y)
+                    acc[h][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.w[h][s], f.x[y][s],
+                                                                        acc[h][y], 0, 0, 0);
+    };
+    const int64_t whole = p.K / kFewStep;
+    const int64_t stride = (int64_t)waves * kFewStep, end = whole * kFewStep;
+    int64_t k = (int64_t)wave * kFewStep;
+    Piece a, b;
+    if (k < end) load(a, k);
+    while (k < end) {
+        k += stride;
+        if (k < end) load(b, k);
+        multiply(a);
+        if (k >= end) break;
+        k += stride;
+        if (k < end) load(a, k);
+        multiply(b);
+    }
+    if (p.K > end && wave == whole % waves) {
+#pragma unroll 1
+        for (int64_t t = end; t < p.K; t += 32) {
+            const int64_t n = p.K - t - g * 8;
+            bf16x8 fw[2], fx[TJ];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) fw[h] = load_frag(w[h] + t, n);
+#pragma unroll
+            for (int y = 0; y < TJ; ++y) fx[y] = load_frag(x[y] + t, n);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int y = 0; y < TJ; ++y)
+                    acc[h][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[h], fx[y], acc[h][y], 0,
+                                                                        0, 0);
+        }
+    }
+    TIDE_LDS float* mine = (TIDE_LDS float*)sums + (wave * 16 * TJ + r) * kFewPitch + g * 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int y = 0; y < TJ; ++y)
+            *(TIDE_LDS f32x4v*)(mine + 16 * y * kFewPitch + 16 * h) = acc[h][y];
+    __syncthreads();
+    // 4 lanes of 8 columns for each token: the first TJ waves
+    if (wave >= TJ) return;
+    const int64_t j = threadIdx.x >> 2;
+    const int c = (threadIdx.x & 3) * 8;
+    float v[8] = {};
+    for (int u = 0; u < waves; ++u) {
+        const TIDE_LDS float* from = (TIDE_LDS float*)sums + (u * 16 * TJ + j) * kFewPitch + c;
+        const f32x4v lo = *(const TIDE_LDS f32x4v*)from, hi = *(const TIDE_LDS f32x4v*)(from + 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            v[q] += lo[q];
+            v[q + 4] += hi[q];
+        }
+    }
+    finish(p.e, n0 + c, j, j < p.e.J && n0 + c < p.e.I, v);
+}
+
 // ---- operand preparation -------------------------------------------------
 
 // Rows of `cols` elements copied to rows of `width` (a multiple of 8), the
@@ -261,9 +511,11 @@ __global__ __launch_bounds__(kPadThreads) void pad_kernel(const uint16_t* in, in
 // dz = dy act'(z) rounded to bf16, rows of `width` elements with zeros behind
 // the N-th, and the column sums of dz before the rounding over each chunk of
 // rows (one row of `sums` for each chunk).  A workgroup takes 256 columns of a
-// chunk: 32 lanes of 8 columns, 8 rows at a time.
+// chunk: 32 lanes of 8 columns, 8 rows at a time, and a lane has the loads of
+// kDzRows such rows in flight.
 constexpr int kDzThreads = 256;
 constexpr int kDzCols = 256;
+constexpr int kDzRows = 4;
 
 struct DzArgs {
     const uint16_t* dy;
@@ -274,9 +526,9 @@ struct DzArgs {
     float* sums;       // or NULL
     int64_t T, N, chunk;
     int32_t col_groups;
-    int32_t act;
 };
 
+template <int ACT>
 __global__ __launch_bounds__(kDzThreads) void dz_kernel(DzArgs p) {
     __shared__ float part[8][kDzCols];
     const int64_t cg = blockIdx.x % p.col_groups, ch = blockIdx.x / p.col_groups;
@@ -286,28 +538,40 @@ __global__ __launch_bounds__(kDzThreads) void dz_kernel(DzArgs p) {
     const int64_t pitch = act8_pitch(p.N);
     float sum[8] = {};
     if (c < p.N) {
-        for (int64_t t = ch * p.chunk + lr; t < t1; t += 8) {
-            float v[8];
-            load8(p.dy + t * p.ld + c, p.N - c, v);
-            if (p.z) {
-                const u32x2 q = *(const TIDE_GLOBAL_AS u32x2*)(p.z + t * pitch + c);
-                const float s = act8_scale(
-                    *(const TIDE_GLOBAL_AS uint8_t*)(p.z + p.T * pitch + (t * pitch + c) / kActBlock));
-                float lo[4], hi[4];
-                act8_unpack4(q.x, s, lo);
-                act8_unpack4(q.y, s, hi);
+        for (int64_t t0 = ch * p.chunk + lr; t0 < t1; t0 += 8 * kDzRows) {
+            float v[kDzRows][8];
+            u32x2 q[kDzRows];
+            uint32_t s[kDzRows];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    v[r] *= act_slope(lo[r], p.act);
-                    v[r + 4] *= act_slope(hi[r], p.act);
+            for (int u = 0; u < kDzRows; ++u) {
+                const int64_t t = t0 + 8 * u;
+                load8(p.dy + t * p.ld + c, t < t1 ? p.N - c : 0, v[u]);
+                if constexpr (ACT != TIDE_ACT_NONE) {
+                    q[u] = 0;
+                    s[u] = 0;
+                    if (t < t1) {
+                        q[u] = *(const TIDE_GLOBAL_AS u32x2*)(p.z + t * pitch + c);
+                        s[u] = *(const TIDE_GLOBAL_AS uint8_t*)(p.z + p.T * pitch +
+                                                               (t * pitch + c) / kActBlock);
+                    }
                 }
             }
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                if (c + r >= p.N) v[r] = 0.0f;
-                sum[r] += v[r];
+            for (int u = 0; u < kDzRows; ++u) {
+                const int64_t t = t0 + 8 * u;
+                if (t >= t1) break;
+                if constexpr (ACT != TIDE_ACT_NONE) {
+                    float z[8];
+                    act8_unpack8(q[u], act8_scale(s[u]), z);
+                    apply_slope<ACT>(z, v[u]);
+                }
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    if (c + r >= p.N) v[u][r] = 0.0f;
+                    sum[r] += v[u][r];
+                }
+                if (p.dz) store8(p.dz + t * p.width + c, 8, v[u]);
             }
-            if (p.dz) store8(p.dz + t * p.width + c, 8, v);
         }
     }
     if (!p.sums) return;
@@ -322,13 +586,26 @@ __global__ __launch_bounds__(kDzThreads) void dz_kernel(DzArgs p) {
     p.sums[ch * p.N + col] = s;
 }
 
-__global__ __launch_bounds__(256) void dbias_kernel(const float* sums, int64_t chunks, int64_t N,
-                                                    uint16_t* out) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= N) return;
+// dbias from the chunks' sums: a wave's lane takes a column, the workgroup's
+// waves every kDbWaves-th chunk.
+constexpr int kDbWaves = 8;
+
+__global__ __launch_bounds__(64 * kDbWaves) void dbias_kernel(const float* sums, int64_t chunks,
+                                                              int64_t N, uint16_t* out) {
+    __shared__ float part[kDbWaves][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
     float s = 0.0f;
-    for (int64_t k = 0; k < chunks; ++k) s += sums[k * N + c];
-    out[c] = to_bf16(s);
+    if (c < N) {
+#pragma unroll 4
+        for (int64_t k = wave; k < chunks; k += kDbWaves) s += sums[k * N + c];
+    }
+    part[wave][lane] = s;
+    __syncthreads();
+    if (wave || c >= N) return;
+#pragma unroll
+    for (int w = 1; w < kDbWaves; ++w) s += part[w][lane];
+    *(TIDE_GLOBAL_AS uint16_t*)(out + c) = to_bf16(s);
 }
 
 // ---- host ----------------------------------------------------------------
@@ -506,7 +783,15 @@ tide_status check_workspace(void* ws, size_t have, int64_t need, const Extent* o
 
 // ---- forward -------------------------------------------------------------
 
+constexpr int64_t kGemvTokens = 4;
+constexpr int64_t kFewTokens = 32;
+
+// Waves of a workgroup of few_kernel: 8 where 4 would give the chip less than
+// 16 waves a compute unit.
+int few_waves(int64_t N) { return ceil_div(N, kFewRows) * 4 < 4096 ? 8 : 4; }
+
 struct ForwardPlan {
+    bool few;
     Source x, w;
     Shape shape;
     float* partial;
@@ -542,6 +827,9 @@ ForwardPlan plan_forward(const tide_linear_forward_args& a, void* ws) {
     ForwardPlan f;
     Carver c{static_cast<char*>(ws)};
     const int64_t T = a.tokens, N = a.out_features, K = a.in_features;
+    f.few = T <= kFewTokens;
+    f.bytes = 0;
+    if (f.few) return f;
     f.x = {a.x, a.ldx, T, K};
     f.w = {a.weight, K, N, K};
     f.x.plan(c);
@@ -575,21 +863,37 @@ extern "C" tide_status tide_linear_forward(const tide_linear_forward_args* args,
     const ForwardPlan f = plan_forward(a, workspace);
     TIDE_TRY(check_workspace(workspace, workspace_bytes, f.bytes, ext, 6));
     TIDE_TRY(check_stream_device(stream));
+    Epilogue e = {};
+    e.I = N;
+    e.J = T;
+    e.out = static_cast<uint16_t*>(a.y);
+    e.ldo = a.ldy;
+    e.bias = static_cast<const uint16_t*>(a.bias);
+    e.res = static_cast<const uint16_t*>(a.residual);
+    e.ldr = a.ldr;
+    e.kept = static_cast<uint8_t*>(a.z_kept);
+    e.act = a.act;
+    if (T <= kGemvTokens && K >= 8 && !a.z_kept) {
+        const Gemv gemv = {static_cast<const uint16_t*>(a.x), T > 1 ? a.ldx : K,
+                           static_cast<const uint16_t*>(a.weight), K, e};
+        return launch(T == 1 ? gemv_kernel<1> : T == 2 ? gemv_kernel<2> : gemv_kernel<4>,
+                      ceil_div(N, kGemvRows), kGemvThreads, stream, gemv);
+    }
+    if (f.few) {
+        const Few few = {static_cast<const uint16_t*>(a.x), T > 1 ? a.ldx : K,
+                         static_cast<const uint16_t*>(a.weight), K, e};
+        const int waves = few_waves(N), tj = T <= 16 ? 1 : 2;
+        return launch_lds(tj == 1 ? few_kernel<1> : few_kernel<2>, ceil_div(N, kFewRows),
+                          64 * waves, (unsigned)(waves * 16 * tj * kFewPitch * sizeof(float)),
+                          stream, few);
+    }
     TIDE_TRY(f.x.fill(stream));
     TIDE_TRY(f.w.fill(stream));
     Product p = {};
     p.A = f.w.operand(false);
     p.B = f.x.operand(false);
     p.depth = round_up(K, 8);
-    p.e.I = N;
-    p.e.J = T;
-    p.e.out = static_cast<uint16_t*>(a.y);
-    p.e.ldo = a.ldy;
-    p.e.bias = static_cast<const uint16_t*>(a.bias);
-    p.e.res = static_cast<const uint16_t*>(a.residual);
-    p.e.ldr = a.ldr;
-    p.e.kept = static_cast<uint8_t*>(a.z_kept);
-    p.e.act = a.act;
+    p.e = e;
     return run_product(kForward, p, f.shape, f.partial, stream);
 }
 
@@ -627,6 +931,18 @@ tide_status check_backward(const tide_linear_backward_args& a) {
     }
     if (a.dbias) TIDE_TRY(check_rows(a.dbias, N, 1, N));
     return TIDE_OK;
+}
+
+using DzKernel = void (*)(DzArgs);
+
+DzKernel dz_kernel_of(int32_t act) {
+    switch (act) {
+        case TIDE_ACT_RELU: return dz_kernel<TIDE_ACT_RELU>;
+        case TIDE_ACT_GELU: return dz_kernel<TIDE_ACT_GELU>;
+        case TIDE_ACT_GELU_TANH: return dz_kernel<TIDE_ACT_GELU_TANH>;
+        case TIDE_ACT_SILU: return dz_kernel<TIDE_ACT_SILU>;
+        default: return dz_kernel<TIDE_ACT_NONE>;
+    }
 }
 
 BackwardPlan plan_backward(const tide_linear_backward_args& a, void* ws) {
@@ -698,11 +1014,10 @@ extern "C" tide_status tide_linear_backward(const tide_linear_backward_args* arg
         d.N = N;
         d.chunk = b.chunk;
         d.col_groups = (int32_t)ceil_div(N, kDzCols);
-        d.act = a.act;
-        TIDE_TRY(launch(dz_kernel, d.col_groups * b.chunks, kDzThreads, stream, d));
+        TIDE_TRY(launch(dz_kernel_of(a.act), d.col_groups * b.chunks, kDzThreads, stream, d));
     }
     if (a.dbias && N)
-        TIDE_TRY(launch(dbias_kernel, ceil_div(N, 256), 256, stream,
+        TIDE_TRY(launch(dbias_kernel, ceil_div(N, 64), 64 * kDbWaves, stream,
                         static_cast<const float*>(b.sums), b.chunks, N,
                         static_cast<uint16_t*>(a.dbias)));
     if (K == 0) return TIDE_OK;

@@ -69,17 +69,22 @@ inline tide_status check_stream_device(tide_stream_t stream) {
 }
 
 template <typename... P, typename... A>
-tide_status launch(void (*kernel)(P...), int64_t grid, int threads, tide_stream_t stream, A... a) {
+tide_status launch_lds(void (*kernel)(P...), int64_t grid, int threads, unsigned lds_bytes,
+                       tide_stream_t stream, A... a) {
     if (grid <= 0) return TIDE_OK;
     if (grid > kMaxGrid) return TIDE_EUNSUPPORTED;
     void* args[] = {&a...};
     static_assert(sizeof...(P) == sizeof...(A), "one argument for each parameter");
     static_assert((__is_same(P, A) && ...), "arguments of the parameters' own types");
     return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((unsigned)grid),
-                           dim3((unsigned)threads), args, 0,
+                           dim3((unsigned)threads), args, lds_bytes,
                            reinterpret_cast<hipStream_t>(stream)) == hipSuccess
                ? TIDE_OK
                : TIDE_EHIP;
+}
+template <typename... P, typename... A>
+tide_status launch(void (*kernel)(P...), int64_t grid, int threads, tide_stream_t stream, A... a) {
+    return launch_lds(kernel, grid, threads, 0, stream, a...);
 }
 
 }  // namespace tide
