@@ -153,7 +153,7 @@ __device__ __forceinline__ void finish(const Epilogue& e, int64_t i, int64_t j, 
 struct Product {
     Operand A, B;
     int64_t depth;        // contraction elements
-    int64_t split_depth;  // of one split (a multiple of kStepK)
+    int64_t split_depth;  // of one split (a multiple of kSplitUnit)
     int32_t tiles_i, tiles_j, splits;
     float* partial;       // [splits][J][pitch] sums where splits > 1
     int64_t partial_pitch;
@@ -187,18 +187,18 @@ __device__ __forceinline__ void tile_at(const Product& p, int64_t* ti, int64_t* 
 // returned before it writes again.
 __device__ __forceinline__ void wave_lds_order() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-template <int BI, int BJ, int WI, int WJ, bool CA, bool CB>
+template <int BI, int BJ, int K, int WI, int WJ, bool CA, bool CB>
 __global__ __launch_bounds__(WI* WJ * 64, BI == 256 ? 2 : 1) void product_kernel(Product p) {
     constexpr int TI = BI / WI / 16, TJ = BJ / WJ / 16;
     static_assert(TI % 2 == 0, "a wave holds whole checkpoint blocks");
-    __shared__ __attribute__((aligned(1024))) char lds[2 * (BI + BJ) * kStepK * 2];
+    __shared__ __attribute__((aligned(1024))) char lds[2 * (BI + BJ) * K * 2];
     int64_t ti, tj, sp;
     tile_at(p, &ti, &tj, &sp);
     const int64_t i0 = ti * BI, j0 = tj * BJ;
     const int64_t k0 = sp * p.split_depth;
     const int64_t k1 = min(p.depth, k0 + p.split_depth);
     f32x4v acc[TI][TJ];
-    tile_loop<BI, BJ, WI, WJ, CA, CB>(p.A, p.B, p.depth, k0, k1, i0, j0, (TIDE_LDS char*)lds, acc);
+    tile_loop<BI, BJ, K, WI, WJ, CA, CB>(p.A, p.B, p.depth, k0, k1, i0, j0, (TIDE_LDS char*)lds, acc);
 
     // The accumulators pass through LDS, 16 rows of a wave at a time, so that
     // each lane ends with 8 consecutive columns and a row's stores are whole
@@ -241,6 +241,7 @@ __global__ __launch_bounds__(WI* WJ * 64, BI == 256 ? 2 : 1) void product_kernel
 // The sums of a split contraction added up in the splits' order, then the
 // epilogue.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinAhead = 8;  // splits whose loads are in flight together
 
 __global__ __launch_bounds__(kJoinThreads) void join_kernel(Product p) {
     const int64_t per_row = p.partial_pitch / 8;
@@ -249,15 +250,24 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(Product p) {
     const bool there = j < p.e.J && i < p.e.I;
     float v[8] = {};
     if (there) {
-        for (int s = 0; s < p.splits; ++s) {
-            const float* from = p.partial + ((int64_t)s * p.e.J + j) * p.partial_pitch + i;
-            const f32x4v lo = *(const TIDE_GLOBAL_AS f32x4v*)from;
-            const f32x4v hi = *(const TIDE_GLOBAL_AS f32x4v*)(from + 4);
+        const float* from = p.partial + j * p.partial_pitch + i;
+        const int64_t next = p.e.J * p.partial_pitch;
+        for (int s = 0; s < p.splits; s += kJoinAhead) {
+            f32x4v lo[kJoinAhead], hi[kJoinAhead];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                v[r] += lo[r];
-                v[r + 4] += hi[r];
+            for (int u = 0; u < kJoinAhead; ++u) {
+                const bool have = s + u < p.splits;
+                lo[u] = have ? *(const TIDE_GLOBAL_AS f32x4v*)from : (f32x4v)0.0f;
+                hi[u] = have ? *(const TIDE_GLOBAL_AS f32x4v*)(from + 4) : (f32x4v)0.0f;
+                from += next;
             }
+#pragma unroll
+            for (int u = 0; u < kJoinAhead; ++u)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    v[r] += lo[u][r];
+                    v[r + 4] += hi[u][r];
+                }
         }
     }
     finish(p.e, i, j, there, v);
@@ -625,37 +635,95 @@ struct Carver {
     }
 };
 
+constexpr int64_t kSplitUnit = 256;  // contraction elements
+
 enum Kind { kForward, kGradInput, kGradWeight };
 
 // Tile and split for a product of I x J outputs.
 struct Shape {
-    int bi, bj;
+    int bi, bj, bk;
     int32_t tiles_i, tiles_j, splits;
     int64_t split_depth;
 };
 
-Shape choose(int64_t I, int64_t J, int64_t depth) {
-    Shape s;
-    int64_t want;  // workgroups that fill the chip
+void set_split(Shape* s, int64_t I, int64_t J, int64_t depth, int64_t splits) {
+    const int64_t units = ceil_div(depth, kSplitUnit);
+    const int64_t each = std::max<int64_t>(1, ceil_div(units, std::max<int64_t>(1, splits)));
+    s->tiles_i = (int32_t)ceil_div(I, s->bi);
+    s->tiles_j = (int32_t)ceil_div(J, s->bj);
+    s->split_depth = each * kSplitUnit;
+    s->splits = (int32_t)std::max<int64_t>(1, ceil_div(units, each));
+}
+
+// What a tile costs, in microseconds, measured at K = 8192: a step of 64
+// contraction elements when a quarter of the compute units have one (`step`)
+// and what it takes longer when all have (`power`: the clock falls), and the
+// rest of a tile's life (first loads, epilogue).
+struct TileCost {
+    int bi, bj;
+    double step, power, rest;
+};
+constexpr TileCost kTiles[] = {{256, 256, 1.25, 0.30, 7.0},
+                               {256, 192, 0.95, 0.36, 6.0},
+                               {256, 128, 0.72, 0.33, 5.0},
+                               {128, 128, 0.60, 0.00, 4.0}};
+// Two 128 x 128 tiles on a compute unit take a step each in this time.
+constexpr double kPairStep = 0.95;
+constexpr int kCus = 256;
+
+double product_us(const TileCost& c, const Shape& s, int64_t I, int64_t J) {
+    const int64_t groups = (int64_t)s.tiles_i * s.tiles_j * s.splits;
+    const double rounds = (double)ceil_div(groups, kCus);
+    const double steps = (double)(s.split_depth / 64);
+    double us;
+    if (c.bi == 128) {
+        const double pairs = (double)(int64_t)(rounds / 2), single = rounds - 2 * pairs;
+        us = pairs * (steps * kPairStep + c.rest) + single * (steps * c.step + c.rest);
+    } else {
+        const double used = (double)groups / (rounds * kCus);
+        us = rounds * (steps * (c.step + c.power * used * used) + c.rest);
+    }
+    // the partial sums are written and read once, at about 3.8 MB/us in all,
+    // and the join is a launch of its own
+    if (s.splits > 1) us += 3.0 + 4.0 * (double)s.splits * (double)I * (double)J / 3.8e6;
+    return us;
+}
+
+// Up to 64 rows of outputs the A operand's bytes bound the product: narrow
+// tiles, and the contraction split until about 1024 workgroups keep loads in
+// flight (four on a compute unit).  A forward weight of more bytes than the
+// 256 MB cache holds is read 512 bytes of a row at a time and past the cache:
+// 91-104 us against 115-121 for 28672 x 8192 and 5 to 32 tokens; smaller
+// weights are faster from the cache (5120 x 5120: 20 us against 30).
+// Otherwise the tile and split of the least estimated time.  2048 x 5120
+// outputs of depth 13824: 264 us with the 256 x 192 tiles this takes, 290 with
+// 256 x 256, 313 with 128 x 128.
+Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth) {
+    Shape s = {};
+    s.bk = 64;
     if (J <= 64) {
         s.bi = 128;
         s.bj = J <= 16 ? 16 : J <= 32 ? 32 : 64;
-        want = 1024;
-    } else if (ceil_div(I, 256) * ceil_div(J, 256) >= 192) {
-        s.bi = s.bj = 256;
-        want = 0;
-    } else {
-        s.bi = s.bj = 128;
-        want = 512;
+        if (kind == kForward && s.bj <= 32 && I * depth > ((int64_t)128 << 20)) s.bk = 256;
+        set_split(&s, I, J, depth, 1024 / std::max<int64_t>(1, ceil_div(I, s.bi)));
+        return s;
     }
-    s.tiles_i = (int32_t)ceil_div(I, s.bi);
-    s.tiles_j = (int32_t)ceil_div(J, s.bj);
-    const int64_t tiles = (int64_t)s.tiles_i * s.tiles_j;
-    const int64_t steps = ceil_div(depth, kStepK);
-    int64_t splits = std::max<int64_t>(1, std::min(want / std::max<int64_t>(1, tiles), steps / 4));
-    const int64_t each = std::max<int64_t>(1, ceil_div(steps, splits));
-    s.split_depth = each * kStepK;
-    s.splits = (int32_t)std::max<int64_t>(1, ceil_div(steps, each));
+    double best = 0.0;
+    for (const TileCost& c : kTiles) {
+        for (int64_t splits = 1; splits <= 16; ++splits) {
+            Shape t = s;
+            t.bi = c.bi;
+            t.bj = c.bj;
+            set_split(&t, I, J, depth, splits);
+            if (t.splits < splits) break;  // the contraction has no more units
+            const double us = product_us(c, t, I, J);
+            if (best == 0.0 || us < best) {
+                best = us;
+                s = t;
+            }
+            if ((int64_t)t.tiles_i * t.tiles_j >= 4 * kCus) break;  // enough without
+        }
+    }
     return s;
 }
 
@@ -665,12 +733,12 @@ int64_t partial_floats(const Shape& s, int64_t I, int64_t J) {
 
 using ProductKernel = void (*)(Product);
 
-template <int BI, int BJ, int WI, int WJ>
+template <int BI, int BJ, int K, int WI, int WJ>
 ProductKernel of_kind(Kind k) {
     switch (k) {
-        case kForward: return product_kernel<BI, BJ, WI, WJ, false, false>;
-        case kGradInput: return product_kernel<BI, BJ, WI, WJ, true, false>;
-        default: return product_kernel<BI, BJ, WI, WJ, true, true>;
+        case kForward: return product_kernel<BI, BJ, K, WI, WJ, false, false>;
+        case kGradInput: return product_kernel<BI, BJ, K, WI, WJ, true, false>;
+        default: return product_kernel<BI, BJ, K, WI, WJ, true, true>;
     }
 }
 
@@ -686,16 +754,18 @@ tide_status run_product(Kind kind, Product p, const Shape& s, float* partial,
     ProductKernel k;
     int threads = 256;
     if (s.bi == 256) {
-        k = of_kind<256, 256, 2, 4>(kind);
+        k = s.bj == 256   ? of_kind<256, 256, 64, 2, 4>(kind)
+            : s.bj == 192 ? of_kind<256, 192, 64, 2, 4>(kind)
+                          : of_kind<256, 128, 64, 2, 4>(kind);
         threads = 512;
     } else if (s.bj == 128) {
-        k = of_kind<128, 128, 2, 2>(kind);
+        k = of_kind<128, 128, 64, 2, 2>(kind);
     } else if (s.bj == 64) {
-        k = of_kind<128, 64, 2, 2>(kind);
+        k = of_kind<128, 64, 64, 2, 2>(kind);
     } else if (s.bj == 32) {
-        k = of_kind<128, 32, 4, 1>(kind);
+        k = s.bk == 256 ? product_kernel<128, 32, 256, 4, 1, false, false> : of_kind<128, 32, 64, 4, 1>(kind);
     } else {
-        k = of_kind<128, 16, 4, 1>(kind);
+        k = s.bk == 256 ? product_kernel<128, 16, 256, 4, 1, false, false> : of_kind<128, 16, 64, 4, 1>(kind);
     }
     const int64_t grid = (int64_t)s.tiles_i * s.tiles_j * s.splits;
     tide_status st = launch(k, grid, threads, stream, p);
@@ -834,7 +904,7 @@ ForwardPlan plan_forward(const tide_linear_forward_args& a, void* ws) {
     f.w = {a.weight, K, N, K};
     f.x.plan(c);
     f.w.plan(c);
-    f.shape = choose(N, T, round_up(K, 8));
+    f.shape = choose(kForward, N, T, round_up(K, 8));
     f.partial = c.take<float>(partial_floats(f.shape, N, T));
     f.bytes = c.used;
     return f;
@@ -963,8 +1033,8 @@ BackwardPlan plan_backward(const tide_linear_backward_args& a, void* ws) {
     b.w.plan(c);
     b.x_width = act8_pitch(K);
     if (a.dweight && N) b.x = c.take<uint16_t>(T * b.x_width);
-    b.in_shape = choose(K, T, b.width);
-    b.w_shape = choose(K, N, T);
+    b.in_shape = choose(kGradInput, K, T, b.width);
+    b.w_shape = choose(kGradWeight, K, N, T);
     int64_t floats = 0;
     if (a.dx) floats = std::max(floats, partial_floats(b.in_shape, K, T));
     if (a.dweight) floats = std::max(floats, partial_floats(b.w_shape, K, N));

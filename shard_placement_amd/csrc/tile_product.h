@@ -38,7 +38,6 @@ typedef float f32x4v __attribute__((ext_vector_type(4)));
 
 #define TIDE_LDS __attribute__((address_space(3)))
 
-constexpr int kStepK = 64;  // contraction elements of one staged tile
 
 // An operand as the kernel reads it: 16-byte aligned, ld % 8 == 0, and either
 // (rows) `count` rows of `depth` contraction elements, or (columns) `depth`
@@ -60,14 +59,32 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* base, int
 
 constexpr uint32_t kNowhere = 0xf0000000u;  // an offset past every descriptor's end
 
-// A tile of N indices from `first` on, staged by WAVES waves.
-template <int N, int WAVES, bool COLUMNS>
+// The swizzles: a "rows" tile's chunk c of row r lies at c ^ row_swizzle(r), a
+// "columns" tile's 32-byte pair p of row k at p ^ column_swizzle(k).
+template <int K>
+__device__ __forceinline__ constexpr int row_swizzle(int r) {
+    return r & (K == 128 ? 15 : 7);
+}
+template <int N>
+__device__ __forceinline__ constexpr int column_swizzle(int k) {
+    constexpr int kPairs = N / 16;
+    return ((k & 3) | ((k >> 1) & 4)) & (kPairs % 8 == 0 ? 7 : kPairs % 4 == 0 ? 3 : kPairs - 1);
+}
+
+// A tile of N indices and K contraction elements from `first` on, staged by
+// WAVES waves.  ONCE: no other workgroup reads the operand's elements.
+constexpr int kNonTemporal = 2;
+
+template <int N, int K, int WAVES, bool COLUMNS, bool ONCE = false>
 struct Stager {
-    static constexpr int kBytes = N * kStepK * 2;
+    static constexpr int kBytes = N * K * 2;
     static constexpr int kLoads = kBytes / 1024;                       // of a whole wave
     static constexpr int kMine = (kLoads + WAVES - 1) / WAVES;
-    static constexpr int kRowChunks = COLUMNS ? N / 8 : kStepK / 8;    // 16-byte chunks of a row
-    static constexpr int kPairMask = COLUMNS ? (N / 16 < 8 ? N / 16 - 1 : 7) : 0;
+    static constexpr int kRowChunks = COLUMNS ? N / 8 : K / 8;    // 16-byte chunks of a row
+
+    // a lane's chunk is the same in all its loads: they are a multiple of the
+    // swizzle's period of rows apart
+    static_assert(COLUMNS || kMine == 1 || WAVES * 64 / kRowChunks % (K == 128 ? 16 : 8) == 0, "");
 
     const char* base;
     int64_t step;        // bytes from one k tile to the next
@@ -76,10 +93,6 @@ struct Stager {
     int wave;
     int chunk_k;         // rows: first contraction element of the lane's chunk
 
-    __device__ __forceinline__ static int swizzle(int k) {
-        return ((k & 3) | ((k >> 1) & 4)) & kPairMask;
-    }
-
     __device__ __forceinline__ void init(const Operand& o, int64_t first, int64_t k0, int lane,
                                          int wave_) {
         wave = wave_;
@@ -87,11 +100,11 @@ struct Stager {
         if constexpr (COLUMNS) {
             base = reinterpret_cast<const char*>(o.p + k0 * o.ld + first);
             left = 2 * ((o.depth - k0 - 1) * o.ld + o.count - first);
-            step = 2 * kStepK * o.ld;
+            step = 2 * K * o.ld;
         } else {
             base = reinterpret_cast<const char*>(o.p + first * o.ld + k0);
             left = 2 * ((o.count - first - 1) * o.ld + o.depth - k0);
-            step = 2 * kStepK;
+            step = 2 * K;
         }
 #pragma unroll
         for (int q = 0; q < kMine; ++q) {
@@ -99,10 +112,10 @@ struct Stager {
             const int row = place / kRowChunks, at = place % kRowChunks;
             int c;
             if constexpr (COLUMNS) {
-                c = at ^ (swizzle(row) << 1);
+                c = at ^ (column_swizzle<N>(row) << 1);
             } else {
-                c = at ^ (row & 7);
-                chunk_k = c * 8;  // the same for every q: WAVES * 64 / 8 rows keep row & 7
+                c = at ^ row_swizzle<K>(row);
+                chunk_k = c * 8;
             }
             offset[q] = (uint32_t)((int64_t)row * o.ld * 2 + c * 16);
         }
@@ -113,13 +126,13 @@ struct Stager {
     __device__ __forceinline__ void stage(TIDE_LDS char* lds, int64_t valid) {
         const __amdgpu_buffer_rsrc_t r = resource(base, left);
         // a "columns" tile's rows past the end are past the descriptor's end
-        const bool none = !COLUMNS && valid < kStepK && chunk_k >= valid;
+        const bool none = !COLUMNS && valid < K && chunk_k >= valid;
 #pragma unroll
         for (int q = 0; q < kMine; ++q) {
             const int load = q * WAVES + wave;
             if (kLoads % WAVES && load >= kLoads) break;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                r, lds + load * 1024, 16, none ? kNowhere : offset[q], 0, 0, 0);
+                r, lds + load * 1024, 16, none ? kNowhere : offset[q], 0, 0, ONCE ? kNonTemporal : 0);
         }
         base += step;
         left -= step;
@@ -128,7 +141,7 @@ struct Stager {
 
 // The 16 x 32 piece of a staged tile that a matrix instruction takes: index
 // m0 + (lane & 15), contraction k = 32 * s + 8 * (lane >> 4) .. + 7.
-template <int N, bool COLUMNS>
+template <int N, int K, bool COLUMNS>
 struct Reader {
     template <int S>
     __device__ __forceinline__ static bf16x8 read(const TIDE_LDS char* lds, int m0, int lane) {
@@ -136,7 +149,7 @@ struct Reader {
             constexpr int kRow = 2 * N;
             const int g = lane >> 4, i = lane & 15;
             const int k = 32 * S + 8 * g + (i >> 2);
-            const int pair = (m0 >> 4) ^ Stager<N, 1, true>::swizzle(k);
+            const int pair = (m0 >> 4) ^ column_swizzle<N>(k);
             const TIDE_LDS char* p = lds + k * kRow + pair * 32 + (i & 3) * 8;
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TIDE_LDS s16x4*)p);
             const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TIDE_LDS s16x4*)(p + 4 * kRow));
@@ -144,8 +157,8 @@ struct Reader {
             return __builtin_bit_cast(bf16x8, v);
         } else {
             const int row = m0 + (lane & 15);
-            const int c = (4 * S + (lane >> 4)) ^ (lane & 7);
-            return *(const TIDE_LDS bf16x8*)(lds + row * (2 * kStepK) + c * 16);
+            const int c = (4 * S + (lane >> 4)) ^ row_swizzle<K>(lane & 15);
+            return *(const TIDE_LDS bf16x8*)(lds + row * (2 * K) + c * 16);
         }
     }
 };
@@ -156,19 +169,19 @@ __device__ __forceinline__ void tile_barrier() {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// One half (32 contraction elements) of a staged tile: its reads, and its
-// matrix instructions.
-template <int BI, int BJ, int TI, int TJ, bool CA, bool CB, int S>
-__device__ __forceinline__ void read_half(const TIDE_LDS char* la, const TIDE_LDS char* lb, int i0,
+// The S-th 32 contraction elements of a staged tile of K: their reads, and
+// their matrix instructions.
+template <int BI, int BJ, int K, int TI, int TJ, bool CA, bool CB, int S>
+__device__ __forceinline__ void read_part(const TIDE_LDS char* la, const TIDE_LDS char* lb, int i0,
                                           int j0, int lane, bf16x8 (&a)[TI], bf16x8 (&b)[TJ]) {
 #pragma unroll
-    for (int t = 0; t < TI; ++t) a[t] = Reader<BI, CA>::template read<S>(la, i0 + 16 * t, lane);
+    for (int t = 0; t < TI; ++t) a[t] = Reader<BI, K, CA>::template read<S>(la, i0 + 16 * t, lane);
 #pragma unroll
-    for (int t = 0; t < TJ; ++t) b[t] = Reader<BJ, CB>::template read<S>(lb, j0 + 16 * t, lane);
+    for (int t = 0; t < TJ; ++t) b[t] = Reader<BJ, K, CB>::template read<S>(lb, j0 + 16 * t, lane);
 }
 
 template <int TI, int TJ>
-__device__ __forceinline__ void multiply_half(const bf16x8 (&a)[TI], const bf16x8 (&b)[TJ],
+__device__ __forceinline__ void multiply_part(const bf16x8 (&a)[TI], const bf16x8 (&b)[TJ],
                                               f32x4v (&acc)[TI][TJ]) {
 #pragma unroll
     for (int x = 0; x < TI; ++x)
@@ -203,7 +216,7 @@ __device__ __forceinline__ void interleave() {
 // of four waves in opposite phases (four barriers a step) 1175, 32x32x16
 // instructions 1300.  The matrix pipes are busy 66% of the cycles then, and the
 // clock is down to 1.75 GHz: what bounds it is power.
-template <int BI, int BJ, int TI, int TJ, bool CA, bool CB, typename SA, typename SB>
+template <int BI, int BJ, int K, int TI, int TJ, bool CA, bool CB, typename SA, typename SB>
 __device__ __forceinline__ void deep_step(TIDE_LDS char* __restrict__ next,
                                           TIDE_LDS char* __restrict__ now, bool more, bool more2,
                                           SA& sa, SB& sb, int64_t valid, int wi, int wj, int lane,
@@ -211,18 +224,18 @@ __device__ __forceinline__ void deep_step(TIDE_LDS char* __restrict__ next,
                                           f32x4v (&acc)[TI][TJ]) {
     constexpr int kReads = TI * (CA ? 2 : 1) + TJ * (CB ? 2 : 1);
     bf16x8 a1[TI], b1[TJ];
-    read_half<BI, BJ, TI, TJ, CA, CB, 1>(now, now + SA::kBytes, wi, wj, lane, a1, b1);
-    multiply_half<TI, TJ>(a0, b0, acc);
+    read_part<BI, BJ, K, TI, TJ, CA, CB, 1>(now, now + SA::kBytes, wi, wj, lane, a1, b1);
+    multiply_part<TI, TJ>(a0, b0, acc);
     interleave<kReads>();
     __builtin_amdgcn_sched_barrier(0);
     tile_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    if (more) read_half<BI, BJ, TI, TJ, CA, CB, 0>(next, next + SA::kBytes, wi, wj, lane, a0, b0);
+    if (more) read_part<BI, BJ, K, TI, TJ, CA, CB, 0>(next, next + SA::kBytes, wi, wj, lane, a0, b0);
     if (more2) {
         sa.stage(now, valid);
         sb.stage(now + SA::kBytes, valid);
     }
-    multiply_half<TI, TJ>(a1, b1, acc);
+    multiply_part<TI, TJ>(a1, b1, acc);
     __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -231,7 +244,7 @@ __device__ __forceinline__ void deep_step(TIDE_LDS char* __restrict__ next,
 // holds several: other workgroups fill the gaps, and fewer registers let more
 // of them in (the step above on 128 x 128 tiles: 8% slower on 1003 x 1001 x
 // 8192, 15% on 2048 x 5120 x 13824).
-template <int BI, int BJ, int TI, int TJ, bool CA, bool CB, typename SA, typename SB>
+template <int BI, int BJ, int K, int TI, int TJ, bool CA, bool CB, typename SA, typename SB>
 __device__ __forceinline__ void plain_step(TIDE_LDS char* __restrict__ next,
                                            const TIDE_LDS char* __restrict__ now, bool more, SA& sa,
                                            SB& sb, int64_t valid, int wi, int wj, int lane,
@@ -241,22 +254,34 @@ __device__ __forceinline__ void plain_step(TIDE_LDS char* __restrict__ next,
         sb.stage(next + SA::kBytes, valid);
     }
     bf16x8 a[TI], b[TJ];
-    read_half<BI, BJ, TI, TJ, CA, CB, 0>(now, now + SA::kBytes, wi, wj, lane, a, b);
-    multiply_half<TI, TJ>(a, b, acc);
-    read_half<BI, BJ, TI, TJ, CA, CB, 1>(now, now + SA::kBytes, wi, wj, lane, a, b);
-    multiply_half<TI, TJ>(a, b, acc);
+    auto part = [&]<int S>() __attribute__((always_inline)) {
+        read_part<BI, BJ, K, TI, TJ, CA, CB, S>(now, now + SA::kBytes, wi, wj, lane, a, b);
+        multiply_part<TI, TJ>(a, b, acc);
+    };
+    part.template operator()<0>();
+    part.template operator()<1>();
+    if constexpr (K >= 128) {
+        part.template operator()<2>();
+        part.template operator()<3>();
+    }
+    if constexpr (K >= 256) {
+        part.template operator()<4>();
+        part.template operator()<5>();
+        part.template operator()<6>();
+        part.template operator()<7>();
+    }
 }
 
 // The loop over the contraction elements [k0, k1) of `depth` (the longer
-// operand's) of the tile at (i0, j0), with two k tiles in LDS.
-template <int BI, int BJ, int WI, int WJ, bool CA, bool CB>
+// operand's) of the tile at (i0, j0), with two tiles of K of them in LDS.
+template <int BI, int BJ, int K, int WI, int WJ, bool CA, bool CB>
 __device__ __forceinline__ void tile_loop(const Operand& A, const Operand& B, int64_t depth,
                                           int64_t k0, int64_t k1, int64_t i0, int64_t j0,
                                           TIDE_LDS char* lds,
                                           f32x4v (&acc)[BI / WI / 16][BJ / WJ / 16]) {
     constexpr int kWaves = WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
-    using SA = Stager<BI, kWaves, CA>;
-    using SB = Stager<BJ, kWaves, CB>;
+    using SA = Stager<BI, K, kWaves, CA, (K > 64)>;
+    using SB = Stager<BJ, K, kWaves, CB>;
     constexpr int kTile = SA::kBytes + SB::kBytes;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -270,23 +295,23 @@ __device__ __forceinline__ void tile_loop(const Operand& A, const Operand& B, in
 #pragma unroll
         for (int y = 0; y < TJ; ++y) acc[x][y] = 0;
     if (k0 >= k1) return;
-    const int steps = (int)((k1 - k0 + kStepK - 1) / kStepK);
+    const int steps = (int)((k1 - k0 + K - 1) / K);
     int64_t valid = depth - k0;
     int at = 0;
     sa.stage(lds, valid);
     sb.stage(lds + SA::kBytes, valid);
     if constexpr (kWaves == 8) {
         tile_barrier();
-        valid -= kStepK;
+        valid -= K;
         if (steps > 1) {
             sa.stage(lds + kTile, valid);
             sb.stage(lds + kTile + SA::kBytes, valid);
         }
         bf16x8 a0[TI], b0[TJ];
-        read_half<BI, BJ, TI, TJ, CA, CB, 0>(lds, lds + SA::kBytes, wi, wj, lane, a0, b0);
+        read_part<BI, BJ, K, TI, TJ, CA, CB, 0>(lds, lds + SA::kBytes, wi, wj, lane, a0, b0);
         auto step = [&](bool more, bool more2) __attribute__((always_inline)) {
-            valid -= kStepK;
-            deep_step<BI, BJ, TI, TJ, CA, CB>(lds + (at ^ kTile), lds + at, more, more2, sa, sb,
+            valid -= K;
+            deep_step<BI, BJ, K, TI, TJ, CA, CB>(lds + (at ^ kTile), lds + at, more, more2, sa, sb,
                                               valid, wi, wj, lane, a0, b0, acc);
             at ^= kTile;
         };
@@ -297,8 +322,8 @@ __device__ __forceinline__ void tile_loop(const Operand& A, const Operand& B, in
     } else {
         for (int s = 0; s < steps; ++s) {
             tile_barrier();
-            valid -= kStepK;
-            plain_step<BI, BJ, TI, TJ, CA, CB>(lds + (at ^ kTile), lds + at, s + 1 < steps, sa, sb,
+            valid -= K;
+            plain_step<BI, BJ, K, TI, TJ, CA, CB>(lds + (at ^ kTile), lds + at, s + 1 < steps, sa, sb,
                                                valid, wi, wj, lane, acc);
             at ^= kTile;
         }
