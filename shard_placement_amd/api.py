@@ -315,52 +315,75 @@ def _require(t: torch.Tensor, dtype, what: str) -> None:
         raise TideError(-6, "%s is not contiguous" % what)
 
 
-def _device_call(device, stream, call):
-    """call(stream handle) with ``device`` current and ``stream`` (default:
-    the device's current stream) the one that allocations belong to."""
-    if device.index == torch.cuda.current_device() and stream is None:
-        return call(ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream))
-    with torch.cuda.device(device):
+# What torch.cuda.current_stream / current_device wrap, without the objects.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _on_device(index: int, stream, call, *args):
+    """call(stream handle, *args) with device ``index`` current and ``stream``
+    (default: the device's current stream) the one that allocations belong to."""
+    if stream is None and index == _current_device():
+        return call(_raw_stream(index), *args)
+    with torch.cuda.device(index):
         if stream is None:
-            return call(ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream))
+            return call(_raw_stream(index), *args)
         with torch.cuda.stream(stream):
-            return call(ctypes.c_void_p(int(stream.cuda_stream)))
+            return call(int(stream.cuda_stream), *args)
 
 
-def _matrix(t: torch.Tensor, rows: int, cols: int, what: str, device=None):
-    """(address, row distance) of a [rows, cols] bf16 GPU matrix whose rows
-    may lie apart but are contiguous themselves."""
+def _index(t: torch.Tensor, what: str) -> int:
+    """Index of the GPU that the bf16 matrix ``t`` is on."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % what)
     if t.dtype != torch.bfloat16:
         raise TideError(-6, "%s has dtype %s, expected %s" % (what, t.dtype, torch.bfloat16))
-    if t.device.type != "cuda" or (device is not None and t.device != device):
-        raise TideError(-6, "%s is on %s, expected %s" % (what, t.device, device or "a GPU"))
-    if tuple(t.shape) != (rows, cols):
-        raise TideError(-1, "%s is %s, expected [%d, %d]" % (what, list(t.shape), rows, cols))
-    if cols > 1 and t.stride(1) != 1:
+    if not t.is_cuda:
+        raise TideError(-6, "%s is on %s, expected a GPU" % (what, t.device))
+    if t.dim() != 2:
+        raise TideError(-1, "%s has %d dimensions, expected 2" % (what, t.dim()))
+    return t.get_device()
+
+
+def _rows(t: torch.Tensor, what: str):
+    """(address, row distance) of a matrix whose rows may lie apart but are
+    contiguous themselves."""
+    rows, cols = t.shape
+    ld, one = t.stride()
+    if rows <= 1:
+        ld = cols
+    if one != 1 and cols > 1:
         raise TideError(-6, "%s has rows that are not contiguous" % what)
-    if rows > 1 and t.stride(0) < cols:
+    if ld < cols:
         raise TideError(-6, "%s has rows that share memory" % what)
-    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+    return t.data_ptr(), ld
 
 
-def _whole(t: torch.Tensor, shape, what: str, device) -> int:
-    """Address of a contiguous bf16 tensor of this shape on ``device``."""
+def _matrix(t: torch.Tensor, rows: int, cols: int, what: str, index: int):
+    """The same of a bf16 [rows, cols] matrix on GPU ``index``."""
+    if _index(t, what) != index:
+        raise TideError(-6, "%s is on %s, expected cuda:%d" % (what, t.device, index))
+    if t.shape != (rows, cols):
+        raise TideError(-1, "%s is %s, expected [%d, %d]" % (what, list(t.shape), rows, cols))
+    return _rows(t, what)
+
+
+def _whole(t: torch.Tensor, shape, what: str, index: int) -> int:
+    """Address of a contiguous bf16 tensor of this shape on GPU ``index``."""
     _require(t, torch.bfloat16, what)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise TideError(-1, "%s is %s, expected %s" % (what, list(t.shape), list(shape)))
-    if t.device != device:
-        raise TideError(-6, "%s is on %s, expected %s" % (what, t.device, device))
+    if t.get_device() != index:
+        raise TideError(-6, "%s is on %s, expected cuda:%d" % (what, t.device, index))
     return t.data_ptr()
 
 
-def _kept(t: torch.Tensor, rows: int, cols: int, what: str, device) -> int:
+def _kept(t: torch.Tensor, rows: int, cols: int, what: str, index: int) -> int:
     """Address of a checkpoint of a [rows, cols] matrix (a flat uint8 tensor)."""
     _require(t, torch.uint8, what)
-    if t.device != device:
-        raise TideError(-6, "%s is on %s, expected %s" % (what, t.device, device))
-    need = tide_act8_bytes(rows, cols)
+    if t.get_device() != index:
+        raise TideError(-6, "%s is on %s, expected cuda:%d" % (what, t.device, index))
+    need = rows * (-(-cols // 32)) * 33
     if t.numel() < need:
         raise TideError(-1, "%s holds %d bytes, need %d" % (what, t.numel(), need))
     return t.data_ptr()
@@ -372,7 +395,7 @@ def _act(act: str) -> int:
     return ACTS[act]
 
 
-def _workspace(query, args, device):
+def _workspace(query, args, index):
     """(tensor, address, bytes) of the call's workspace.  It is taken from
     torch's allocator for each call: calls on different streams, or captured
     into different graphs, never share one."""
@@ -380,7 +403,7 @@ def _workspace(query, args, device):
     check(query(ctypes.byref(args), ctypes.byref(n)), query.__name__)
     if not n.value:
         return None, None, 0
-    t = torch.empty(n.value, dtype=torch.uint8, device=device)
+    t = torch.empty(n.value, dtype=torch.uint8, device=index)
     return t, t.data_ptr(), n.value
 
 
@@ -391,26 +414,40 @@ def tide_act8_bytes(rows: int, cols: int) -> int:
     return int(n.value)
 
 
+def _pack_on(s, px, ldx, rows, cols, pk):
+    check(_lib.lib().tide_act8_pack(px, ldx, rows, cols, pk, s), "tide_act8_pack")
+
+
+def _unpack_on(s, pk, rows, cols, px, ldx):
+    check(_lib.lib().tide_act8_unpack(pk, rows, cols, px, ldx, s), "tide_act8_unpack")
+
+
 def tide_act8_pack(x: torch.Tensor, kept: torch.Tensor, stream=None) -> None:
     """Write the checkpoint of the bf16 matrix ``x`` into ``kept`` (uint8)."""
-    if x.dim() != 2:
-        raise TideError(-1, "x has %d dimensions, expected 2" % x.dim())
+    index = _index(x, "x")
     rows, cols = x.shape
-    px, ldx = _matrix(x, rows, cols, "x")
-    pk = _kept(kept, rows, cols, "kept", x.device)
-    _device_call(x.device, stream, lambda s: check(
-        _lib.lib().tide_act8_pack(px, ldx, rows, cols, pk, s), "tide_act8_pack"))
+    px, ldx = _rows(x, "x")
+    _on_device(index, stream, _pack_on, px, ldx, rows, cols,
+               _kept(kept, rows, cols, "kept", index))
 
 
 def tide_act8_unpack(kept: torch.Tensor, x: torch.Tensor, stream=None) -> None:
     """Write the values of the checkpoint ``kept`` into the bf16 matrix ``x``."""
-    if x.dim() != 2:
-        raise TideError(-1, "x has %d dimensions, expected 2" % x.dim())
+    index = _index(x, "x")
     rows, cols = x.shape
-    px, ldx = _matrix(x, rows, cols, "x")
-    pk = _kept(kept, rows, cols, "kept", x.device)
-    _device_call(x.device, stream, lambda s: check(
-        _lib.lib().tide_act8_unpack(pk, rows, cols, px, ldx, s), "tide_act8_unpack"))
+    px, ldx = _rows(x, "x")
+    _on_device(index, stream, _unpack_on, _kept(kept, rows, cols, "kept", index), rows, cols, px,
+               ldx)
+
+
+def _forward_on(s, a, y, index):
+    if y is None:
+        y = torch.empty(a.tokens, a.out_features, dtype=torch.bfloat16, device=index)
+        a.y, a.ldy = y.data_ptr(), a.out_features
+    L = _lib.lib()
+    ws, ptr, n = _workspace(L.tide_linear_forward_workspace, a, index)
+    check(L.tide_linear_forward(ctypes.byref(a), ptr, n, s), "tide_linear_forward")
+    return y
 
 
 def tide_linear_forward(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor = None, bias=None,
@@ -418,65 +455,64 @@ def tide_linear_forward(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor =
     """y = act(x weight^T + bias) + residual; z_kept (uint8), where given,
     receives the checkpoint of act's argument.  Returns y (allocated when not
     given)."""
-    if x.dim() != 2 or weight.dim() != 2:
-        raise TideError(-1, "x and weight are matrices")
-    (T, K), N, dev = x.shape, weight.shape[0], x.device
-    a = TideLinearForwardArgs()
-    a.tokens, a.out_features, a.in_features, a.act = T, N, K, _act(act)
-    a.x, a.ldx = _matrix(x, T, K, "x")
-    a.weight = _whole(weight, (N, K), "weight", dev)
+    index = _index(x, "x")
+    T, K = x.shape
+    if weight.dim() != 2:
+        raise TideError(-1, "weight has %d dimensions, expected 2" % weight.dim())
+    N = weight.shape[0]
+    px, ldx = _rows(x, "x")
+    a = TideLinearForwardArgs(T, N, K, _act(act), 0, px, ldx,
+                              _whole(weight, (N, K), "weight", index))
     if bias is not None:
-        a.bias = _whole(bias, (N,), "bias", dev)
+        a.bias = _whole(bias, (N,), "bias", index)
     if residual is not None:
-        a.residual, a.ldr = _matrix(residual, T, N, "residual", dev)
+        a.residual, a.ldr = _matrix(residual, T, N, "residual", index)
+    if y is not None:
+        a.y, a.ldy = _matrix(y, T, N, "y", index)
     if z_kept is not None:
-        a.z_kept = _kept(z_kept, T, N, "z_kept", dev)
+        a.z_kept = _kept(z_kept, T, N, "z_kept", index)
+    return _on_device(index, stream, _forward_on, a, y, index)
+
+
+def _backward_on(s, a, dx, index):
+    if dx is True:
+        dx = torch.empty(a.tokens, a.in_features, dtype=torch.bfloat16, device=index)
+        a.dx, a.lddx = dx.data_ptr(), a.in_features
     L = _lib.lib()
-
-    def call(s):
-        out = torch.empty(T, N, dtype=torch.bfloat16, device=dev) if y is None else y
-        a.y, a.ldy = _matrix(out, T, N, "y", dev)
-        ws, ptr, n = _workspace(L.tide_linear_forward_workspace, a, dev)
-        check(L.tide_linear_forward(ctypes.byref(a), ptr, n, s), "tide_linear_forward")
-        return out
-
-    return _device_call(dev, stream, call)
+    ws, ptr, n = _workspace(L.tide_linear_backward_workspace, a, index)
+    check(L.tide_linear_backward(ctypes.byref(a), ptr, n, s), "tide_linear_backward")
+    return dx
 
 
 def tide_linear_backward(dy: torch.Tensor, in_features: int, weight=None, x_kept=None,
                          z_kept=None, act: str = "none", dx=None, dweight=None, dbias=None,
-                         stream=None) -> None:
+                         stream=None):
     """The gradients that are given: dx = dz weight, dweight = dz^T x, dbias =
-    the sum of dz over the tokens, dz = dy act'(z)."""
-    if dy.dim() != 2:
-        raise TideError(-1, "dy has %d dimensions, expected 2" % dy.dim())
-    (T, N), K, dev = dy.shape, int(in_features), dy.device
-    a = TideLinearBackwardArgs()
-    a.tokens, a.out_features, a.in_features, a.act = T, N, K, _act(act)
-    a.dy, a.lddy = _matrix(dy, T, N, "dy")
+    the sum of dz over the tokens, dz = dy act'(z).  dx=True allocates it.
+    Returns dx."""
+    index = _index(dy, "dy")
+    T, N = dy.shape
+    K = int(in_features)
+    pdy, lddy = _rows(dy, "dy")
+    a = TideLinearBackwardArgs(T, N, K, _act(act), 0, pdy, lddy)
     if a.act:
         if z_kept is None:
             raise TideError(-1, "act %r needs the checkpoint of its argument" % act)
-        a.z_kept = _kept(z_kept, T, N, "z_kept", dev)
+        a.z_kept = _kept(z_kept, T, N, "z_kept", index)
     if dx is not None:
         if weight is None:
             raise TideError(-1, "dx needs the weight")
-        a.weight = _whole(weight, (N, K), "weight", dev)
-        a.dx, a.lddx = _matrix(dx, T, K, "dx", dev)
+        a.weight = _whole(weight, (N, K), "weight", index)
+        if dx is not True:
+            a.dx, a.lddx = _matrix(dx, T, K, "dx", index)
     if dweight is not None:
         if x_kept is None:
             raise TideError(-1, "dweight needs the checkpoint of x")
-        a.x_kept = _kept(x_kept, T, K, "x_kept", dev)
-        a.dweight = _whole(dweight, (N, K), "dweight", dev)
+        a.x_kept = _kept(x_kept, T, K, "x_kept", index)
+        a.dweight = _whole(dweight, (N, K), "dweight", index)
     if dbias is not None:
-        a.dbias = _whole(dbias, (N,), "dbias", dev)
-    L = _lib.lib()
-
-    def call(s):
-        ws, ptr, n = _workspace(L.tide_linear_backward_workspace, a, dev)
-        check(L.tide_linear_backward(ctypes.byref(a), ptr, n, s), "tide_linear_backward")
-
-    _device_call(dev, stream, call)
+        a.dbias = _whole(dbias, (N,), "dbias", index)
+    return _on_device(index, stream, _backward_on, a, dx, index)
 
 
 class Plan:

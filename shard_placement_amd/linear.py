@@ -19,6 +19,7 @@ tensors together.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import torch
@@ -26,6 +27,7 @@ import torch
 from . import api
 from ._lib import TideError
 
+_nothing = contextlib.nullcontext()
 BLOCK = 32  # columns of a checkpoint that share a scale
 
 
@@ -58,17 +60,17 @@ class Act8:
         return api.tide_act8_bytes(rows, cols)
 
     def pack(self, x: torch.Tensor, stream=None) -> "Act8":
-        if tuple(x.shape) != (self.rows, self.cols):
+        if x.shape != (self.rows, self.cols):
             raise TideError(-1, "x is %s, expected [%d, %d]" % (list(x.shape), self.rows, self.cols))
         api.tide_act8_pack(x, self.buffer, stream)
         return self
 
     def unpack(self, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         if out is None:
-            with torch.cuda.stream(stream):
+            with torch.cuda.stream(stream) if stream is not None else _nothing:
                 out = torch.empty(self.rows, self.cols, dtype=torch.bfloat16,
                                   device=self.buffer.device)
-        elif tuple(out.shape) != (self.rows, self.cols):
+        elif out.shape != (self.rows, self.cols):
             raise TideError(-1, "out is %s, expected [%d, %d]"
                             % (list(out.shape), self.rows, self.cols))
         api.tide_act8_unpack(self.buffer, out, stream)
@@ -112,14 +114,13 @@ class Linear:
             self._same(x, dy.shape[0], K, "x")
         if z is not None:
             self._same(z, dy.shape[0], N, "z")
-        if input_grad and dx is None:
-            with torch.cuda.stream(stream):
-                dx = torch.empty(dy.shape[0], K, dtype=torch.bfloat16, device=dy.device)
-        api.tide_linear_backward(dy, K, self.weight, None if x is None else x.buffer,
-                                 None if z is None else z.buffer, self.act,
-                                 dx if input_grad else None, self.weight_grad, self.bias_grad,
-                                 stream)
-        return dx if input_grad else None
+        if not input_grad:
+            dx = None
+        elif dx is None:
+            dx = True
+        return api.tide_linear_backward(dy, K, self.weight, None if x is None else x.buffer,
+                                        None if z is None else z.buffer, self.act, dx,
+                                        self.weight_grad, self.bias_grad, stream)
 
     @staticmethod
     def _same(kept: Act8, rows: int, cols: int, what: str) -> None:
