@@ -37,12 +37,6 @@ __host__ __device__ constexpr int64_t act8_bytes(int64_t rows, int64_t cols) {
     return rows * (act8_pitch(cols) + act8_pitch(cols) / kActBlock);
 }
 
-// |x| for the block's maximum: 0 for an element that is not finite.
-__device__ __forceinline__ float act8_mag(float x) {
-    const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
-    return b < 0x7f800000u ? __uint_as_float(b) : 0.0f;
-}
-
 // The block's exponent from its maximum.  448 = 1.75 * 2^8: a = m * 2^k has
 // exponent k - 8 for m <= 1.75 and k - 7 above, and adding one less than
 // 2^23 - 0x600000 to the bits carries into the exponent exactly then.
@@ -56,14 +50,44 @@ __device__ __forceinline__ float act8_scale(uint32_t byte) { return __uint_as_fl
 __device__ __forceinline__ float act8_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // Four elements to four e4m3 bytes (round to nearest even); inv = 2^-e.
-__device__ __forceinline__ uint32_t act8_pack4(float a, float b, float c, float d, float inv) {
-    // infinities are stored as NaN (the conversion alone could saturate them)
-    a = __builtin_isfinite(a) ? a * inv : __builtin_nanf("");
-    b = __builtin_isfinite(b) ? b * inv : __builtin_nanf("");
-    c = __builtin_isfinite(c) ? c * inv : __builtin_nanf("");
-    d = __builtin_isfinite(d) ? d * inv : __builtin_nanf("");
-    int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+__device__ __forceinline__ uint32_t act8_pack4(const float* x, float inv) {
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * inv, x[1] * inv, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[2] * inv, x[3] * inv, v, true);
+}
+
+// A lane's 8 of a block's 32 elements, the four lanes of a quad together:
+// their bytes, and the block's exponent.  Magnitudes are compared as integers,
+// which orders them, with whatever is not finite above the rest: only a block
+// that has such elements looks at each.
+typedef uint32_t act8_u32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t act8_quad_max(uint32_t m) {
+    m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+    return max(m, (uint32_t)__shfl_xor((int)m, 2));
+}
+
+__device__ __forceinline__ int act8_pack8(float (&x)[8], act8_u32x2* q) {
+    constexpr uint32_t kInf = 0x7f800000u;
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[k]) & 0x7fffffffu);
+    m = act8_quad_max(m);
+    if (m >= kInf) {
+        m = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t b = __float_as_uint(x[k]) & 0x7fffffffu;
+            if (b < kInf)
+                m = max(m, b);
+            else
+                x[k] = __builtin_nanf("");  // the conversion could saturate an infinity
+        }
+        m = act8_quad_max(m);
+    }
+    const int e = act8_exp(__uint_as_float(m));
+    const float inv = act8_pow2(-e);
+    *q = act8_u32x2{act8_pack4(x, inv), act8_pack4(x + 4, inv)};
+    return e;
 }
 
 // The four values of a word of e4m3 bytes, times the scale.
@@ -77,8 +101,16 @@ __device__ __forceinline__ void act8_unpack4(uint32_t w, float s, float (&v)[4])
     v[3] = hi.y * s;
 }
 
-__device__ __forceinline__ void act8_unpack8(uint32_t __attribute__((ext_vector_type(2))) w, float s,
-                                             float (&v)[8]) {
+// Two bytes of a word (the upper two with HIGH) as bf16, times the scale: no
+// rounding, bf16 has the value's four significant bits.
+template <bool HIGH>
+__device__ __forceinline__ uint32_t act8_bf16x2(uint32_t w, float s) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, s, HIGH);
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+__device__ __forceinline__ void act8_unpack8(act8_u32x2 w, float s, float (&v)[8]) {
     float lo[4], hi[4];
     act8_unpack4(w.x, s, lo);
     act8_unpack4(w.y, s, hi);

@@ -51,16 +51,9 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const uint16_t* x, int64
     }
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
-        float a = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a = fmaxf(a, act8_mag(v[k][i]));
-        a = fmaxf(a, __shfl_xor(a, 1));
-        a = fmaxf(a, __shfl_xor(a, 2));
+        act8_u32x2 q;
+        const int e = act8_pack8(v[k], &q);
         if (at[k].row >= rows) continue;
-        const int e = act8_exp(a);
-        const float inv = act8_pow2(-e);
-        const u32x2 q = {act8_pack4(v[k][0], v[k][1], v[k][2], v[k][3], inv),
-                         act8_pack4(v[k][4], v[k][5], v[k][6], v[k][7], inv)};
         const int64_t u = at[k].row * per_row + at[k].unit;
         *(TIDE_GLOBAL_AS u32x2*)(out + u * 8) = q;
         if ((at[k].unit & 3) == 0) *(TIDE_GLOBAL_AS uint8_t*)(scales + u / 4) = (uint8_t)(e + 127);

@@ -28,22 +28,25 @@ namespace {
 
 constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
-constexpr float kTanhC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-constexpr float kTanhA = 0.044715f;
+constexpr float kLog2E = 1.4426950408889634f;
+// 2 sqrt(2 / pi) (z + 0.044715 z^3) = z (kTanhC + kTanhA z^2)
+constexpr float kTanhC = 1.5957691216057308f;
+constexpr float kTanhA = kTanhC * 0.044715f;
 
 // 1 / (1 + exp(-u)), off by a few binary32 steps; 0.5 (1 + tanh(v)) is this at
-// u = 2 v, so the tanh form of gelu is z * sigmoid(2 sqrt(2/pi) (z + 0.044715 z^3)).
-// The reciprocal instruction is within one step; a division written out would
-// be most of the epilogue's work.
+// u = 2 v, so the tanh form of gelu is z * sigmoid(z (kTanhC + kTanhA z^2)).
+// The exponential's and the reciprocal's instructions are within one step; a
+// division written out would be most of the epilogue's work.
 __device__ __forceinline__ float sigmoid(float u) {
-    return __builtin_amdgcn_rcpf(1.0f + __expf(-u));
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2E * u));
 }
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
     if constexpr (ACT == TIDE_ACT_RELU) return z > 0.0f ? z : 0.0f * z;
     if constexpr (ACT == TIDE_ACT_GELU) return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
-    if constexpr (ACT == TIDE_ACT_GELU_TANH) return z * sigmoid(kTanhC * (z + kTanhA * z * z * z));
+    if constexpr (ACT == TIDE_ACT_GELU_TANH)
+        return z * sigmoid(z * __builtin_fmaf(kTanhA, z * z, kTanhC));
     if constexpr (ACT == TIDE_ACT_SILU) return z * sigmoid(z);
     return z;
 }
@@ -52,16 +55,18 @@ template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == TIDE_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f * z;
     if constexpr (ACT == TIDE_ACT_GELU)
-        return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * __expf(-0.5f * z * z) * kInvSqrt2Pi;
+        return 0.5f * (1.0f + erff(z * kSqrtHalf)) +
+               z * __builtin_amdgcn_exp2f(-0.5f * kLog2E * (z * z)) * kInvSqrt2Pi;
     if constexpr (ACT == TIDE_ACT_GELU_TANH) {
-        const float s = sigmoid(kTanhC * (z + kTanhA * z * z * z));
+        const float t = z * z;
+        const float s = sigmoid(z * __builtin_fmaf(kTanhA, t, kTanhC));
         // where the sigmoid is 0 or 1 the polynomial may be infinite already
-        const float q = s * (1.0f - s);
-        return s + (q > 0.0f ? z * q * kTanhC * (1.0f + 3.0f * kTanhA * z * z) : 0.0f);
+        const float q = __builtin_fmaf(-s, s, s);
+        return q > 0.0f ? __builtin_fmaf(z * q, __builtin_fmaf(3.0f * kTanhA, t, kTanhC), s) : s;
     }
     if constexpr (ACT == TIDE_ACT_SILU) {
         const float s = sigmoid(z);
-        return s * (1.0f + z * (1.0f - s));
+        return s * __builtin_fmaf(z, 1.0f - s, 1.0f);
     }
     return 1.0f;
 }
@@ -116,21 +121,18 @@ __device__ __forceinline__ void finish(const Epilogue& e, int64_t i, int64_t j, 
         for (int r = 0; r < 8; ++r) v[r] += b[r];
     }
     if (e.kept) {
-        float a = 0.0f;
         float z[8];
+        if (n >= 8) {
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            z[r] = r < n ? v[r] : 0.0f;
-            a = fmaxf(a, act8_mag(z[r]));
+            for (int r = 0; r < 8; ++r) z[r] = v[r];
+        } else {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) z[r] = r < n ? v[r] : 0.0f;
         }
-        a = fmaxf(a, __shfl_xor(a, 1));
-        a = fmaxf(a, __shfl_xor(a, 2));
+        u32x2 q;
+        const int x = act8_pack8(z, &q);
         const int64_t pitch = act8_pitch(e.I);
         if (j < e.J && i < pitch) {
-            const int x = act8_exp(a);
-            const float inv = act8_pow2(-x);
-            const u32x2 q = {act8_pack4(z[0], z[1], z[2], z[3], inv),
-                             act8_pack4(z[4], z[5], z[6], z[7], inv)};
             *(TIDE_GLOBAL_AS u32x2*)(e.kept + j * pitch + i) = q;
             if (i % kActBlock == 0)
                 *(TIDE_GLOBAL_AS uint8_t*)(e.kept + e.J * pitch + (j * pitch + i) / kActBlock) =
@@ -187,7 +189,7 @@ __device__ __forceinline__ void tile_at(const Product& p, int64_t* ti, int64_t* 
 // returned before it writes again.
 __device__ __forceinline__ void wave_lds_order() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-template <int BI, int BJ, int K, int WI, int WJ, bool CA, bool CB>
+template <int BI, int BJ, int K, int WI, int WJ, Layout CA, Layout CB>
 __global__ __launch_bounds__(WI* WJ * 64, BI == 256 ? 2 : 1) void product_kernel(Product p) {
     constexpr int TI = BI / WI / 16, TJ = BJ / WJ / 16;
     static_assert(TI % 2 == 0, "a wave holds whole checkpoint blocks");
@@ -575,11 +577,13 @@ __global__ __launch_bounds__(kDzThreads) void dz_kernel(DzArgs p) {
                     act8_unpack8(q[u], act8_scale(s[u]), z);
                     apply_slope<ACT>(z, v[u]);
                 }
+                if (c + 8 > p.N) {
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    if (c + r >= p.N) v[u][r] = 0.0f;
-                    sum[r] += v[u][r];
+                    for (int r = 0; r < 8; ++r)
+                        if (c + r >= p.N) v[u][r] = 0.0f;
                 }
+#pragma unroll
+                for (int r = 0; r < 8; ++r) sum[r] += v[u][r];
                 if (p.dz) store8(p.dz + t * p.width + c, 8, v[u]);
             }
         }
@@ -736,9 +740,9 @@ using ProductKernel = void (*)(Product);
 template <int BI, int BJ, int K, int WI, int WJ>
 ProductKernel of_kind(Kind k) {
     switch (k) {
-        case kForward: return product_kernel<BI, BJ, K, WI, WJ, false, false>;
-        case kGradInput: return product_kernel<BI, BJ, K, WI, WJ, true, false>;
-        default: return product_kernel<BI, BJ, K, WI, WJ, true, true>;
+        case kForward: return product_kernel<BI, BJ, K, WI, WJ, kRows, kRows>;
+        case kGradInput: return product_kernel<BI, BJ, K, WI, WJ, kColumns, kRows>;
+        default: return product_kernel<BI, BJ, K, WI, WJ, BI == 256 ? kColumns : kKept, kColumns>;
     }
 }
 
@@ -763,9 +767,9 @@ tide_status run_product(Kind kind, Product p, const Shape& s, float* partial,
     } else if (s.bj == 64) {
         k = of_kind<128, 64, 64, 2, 2>(kind);
     } else if (s.bj == 32) {
-        k = s.bk == 256 ? product_kernel<128, 32, 256, 4, 1, false, false> : of_kind<128, 32, 64, 4, 1>(kind);
+        k = s.bk == 256 ? product_kernel<128, 32, 256, 4, 1, kRows, kRows> : of_kind<128, 32, 64, 4, 1>(kind);
     } else {
-        k = s.bk == 256 ? product_kernel<128, 16, 256, 4, 1, false, false> : of_kind<128, 16, 64, 4, 1>(kind);
+        k = s.bk == 256 ? product_kernel<128, 16, 256, 4, 1, kRows, kRows> : of_kind<128, 16, 64, 4, 1>(kind);
     }
     const int64_t grid = (int64_t)s.tiles_i * s.tiles_j * s.splits;
     tide_status st = launch(k, grid, threads, stream, p);
@@ -803,7 +807,7 @@ struct Source {
     Operand operand(bool columns) const {
         const int64_t width = round_up(cols, 8);
         Operand o;
-        o.p = copied ? copy : static_cast<const uint16_t*>(p);
+        o.p = copied ? copy : p;
         o.ld = copied || rows <= 1 ? width : ld;
         o.count = columns ? width : rows;
         o.depth = columns ? rows : width;
@@ -978,8 +982,7 @@ struct BackwardPlan {
     Source w;
     uint16_t* dz = nullptr;
     float* sums = nullptr;
-    uint16_t* x = nullptr;  // x in bf16, rows of `x_width`
-    int64_t x_width;
+    uint16_t* x = nullptr;
     Shape in_shape, w_shape;
     float* partial = nullptr;
     int64_t bytes;
@@ -1031,10 +1034,10 @@ BackwardPlan plan_backward(const tide_linear_backward_args& a, void* ws) {
     if (a.dbias) b.sums = c.take<float>(b.chunks * N);
     b.w = {a.weight, K, a.dx && T ? N : 0, K};
     b.w.plan(c);
-    b.x_width = act8_pitch(K);
-    if (a.dweight && N) b.x = c.take<uint16_t>(T * b.x_width);
-    b.in_shape = choose(kGradInput, K, T, b.width);
     b.w_shape = choose(kGradWeight, K, N, T);
+    // the 256-wide tiles read x from here, widened (tile_product.h)
+    if (a.dweight && N && b.w_shape.bi == 256) b.x = c.take<uint16_t>(T * act8_pitch(K));
+    b.in_shape = choose(kGradInput, K, T, b.width);
     int64_t floats = 0;
     if (a.dx) floats = std::max(floats, partial_floats(b.in_shape, K, T));
     if (a.dweight) floats = std::max(floats, partial_floats(b.w_shape, K, N));
@@ -1106,10 +1109,12 @@ extern "C" tide_status tide_linear_backward(const tide_linear_backward_args* arg
         TIDE_TRY(run_product(kGradInput, p, b.in_shape, b.partial, stream));
     }
     if (a.dweight && N) {
-        if (T) TIDE_TRY(tide_act8_unpack(a.x_kept, T, K, b.x, b.x_width, stream));
-        Source x = {b.x, b.x_width, T, K};
         Product p = {};
-        p.A = x.operand(true);
+        p.A = {a.x_kept, act8_pitch(K), act8_pitch(K), T};
+        if (b.w_shape.bi == 256) {
+            TIDE_TRY(tide_act8_unpack(a.x_kept, T, K, b.x, act8_pitch(K), stream));
+            p.A.p = b.x;
+        }
         p.B = dz.operand(true);
         p.depth = T;
         p.e.I = K;

@@ -29,6 +29,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "act8.h"
+#include "bf16_io.h"
+
 namespace tide {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -44,8 +47,13 @@ typedef float f32x4v __attribute__((ext_vector_type(4)));
 // rows of `count` elements; the contiguous length is a multiple of 8.  Of two
 // operands one may be up to 7 contraction elements longer than the other,
 // whose missing elements read as 0 (the longer one's then have to be finite).
+//
+// A "kept" operand is the columns of a checkpoint (act8.h): `depth` rows of
+// `count` = ld = its pitch.
+enum Layout { kRows, kColumns, kKept };
+
 struct Operand {
-    const uint16_t* p;
+    const void* p;
     int64_t ld;
     int64_t count;
     int64_t depth;
@@ -98,11 +106,11 @@ struct Stager {
         wave = wave_;
         chunk_k = 0;
         if constexpr (COLUMNS) {
-            base = reinterpret_cast<const char*>(o.p + k0 * o.ld + first);
+            base = static_cast<const char*>(o.p) + 2 * (k0 * o.ld + first);
             left = 2 * ((o.depth - k0 - 1) * o.ld + o.count - first);
             step = 2 * K * o.ld;
         } else {
-            base = reinterpret_cast<const char*>(o.p + first * o.ld + k0);
+            base = static_cast<const char*>(o.p) + 2 * (first * o.ld + k0);
             left = 2 * ((o.count - first - 1) * o.ld + o.depth - k0);
             step = 2 * K;
         }
@@ -120,6 +128,8 @@ struct Stager {
             offset[q] = (uint32_t)((int64_t)row * o.ld * 2 + c * 16);
         }
     }
+
+    __device__ __forceinline__ void prime() {}
 
     // Stage the current k tile into `lds` and move on to the next.  valid:
     // contraction elements left from the tile's first on.
@@ -139,13 +149,91 @@ struct Stager {
     }
 };
 
+// The same for a "columns" tile whose operand is kept in 8 bits: it passes
+// registers, where it is widened to bf16 (exactly).  A lane takes 16 columns
+// of a row of k, half a block: 16 bytes, one scale, and 32 bytes in LDS.  The
+// next tile's bytes are loaded while this one is multiplied.  For tiles of
+// four waves, where it saves writing and reading x in bf16: dW of 1003 x 1001
+// x 8192 31.4 us against 39.1, of 77 x 768 x 2048 8.9 against 12.7.  256 x 256
+// tiles, power-bound, pay more for widening x once in every row of tiles:
+// 4096 x 28672 x 8192 1553 us against 1467 with x widened beforehand.
+template <int N, int K, int WAVES>
+struct KeptStager {
+    static constexpr int kBytes = N * K * 2;
+    static constexpr int kRowPairs = N / 16;
+    static constexpr int kMine = N * K / 16 / (WAVES * 64);
+    static_assert(kMine * WAVES * 64 * 16 == N * K, "every lane has as many pieces");
+
+    const char *base, *scales;
+    int64_t step, left;
+    uint32_t offset[kMine], place[kMine];
+    u32x4v bytes[kMine];
+    uint32_t scale[kMine];
+
+    __device__ __forceinline__ void init(const Operand& o, int64_t first, int64_t k0, int lane,
+                                         int wave) {
+        base = static_cast<const char*>(o.p) + k0 * o.ld + first;
+        scales = static_cast<const char*>(o.p) + o.depth * o.ld + (k0 * o.ld + first) / kActBlock;
+        left = (o.depth - k0) * o.ld - first;
+        step = K * o.ld;
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) {
+            const int piece = (q * WAVES + wave) * 64 + lane;
+            const int row = piece / kRowPairs, pair = piece % kRowPairs;
+            offset[q] = (uint32_t)((int64_t)row * o.ld + pair * 16);
+            place[q] = (uint32_t)(row * 2 * N + (pair ^ column_swizzle<N>(row)) * 32);
+        }
+    }
+
+    // Rows past the end read as zeros with a scale of zero.
+    __device__ __forceinline__ void prime() {
+        const __amdgpu_buffer_rsrc_t r = resource(base, left);
+        const __amdgpu_buffer_rsrc_t s = resource(scales, left / kActBlock);
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) {
+            bytes[q] = __builtin_amdgcn_raw_buffer_load_b128(r, offset[q], 0, 0);
+            scale[q] = __builtin_amdgcn_raw_buffer_load_b8(s, offset[q] / kActBlock, 0, 0);
+        }
+        base += step;
+        scales += step / kActBlock;
+        left -= step;
+    }
+
+    __device__ __forceinline__ void stage(TIDE_LDS char* lds, int64_t) {
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) {
+            const float f = act8_scale(scale[q]);
+            u32x4v lo, hi;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                lo[2 * w] = act8_bf16x2<false>(bytes[q][w], f);
+                lo[2 * w + 1] = act8_bf16x2<true>(bytes[q][w], f);
+                hi[2 * w] = act8_bf16x2<false>(bytes[q][w + 2], f);
+                hi[2 * w + 1] = act8_bf16x2<true>(bytes[q][w + 2], f);
+            }
+            *(TIDE_LDS u32x4v*)(lds + place[q]) = lo;
+            *(TIDE_LDS u32x4v*)(lds + place[q] + 16) = hi;
+        }
+        prime();
+    }
+};
+
+template <int N, int K, int WAVES, Layout L, bool ONCE>
+struct StagerOf {
+    using type = Stager<N, K, WAVES, L == kColumns, ONCE>;
+};
+template <int N, int K, int WAVES, bool ONCE>
+struct StagerOf<N, K, WAVES, kKept, ONCE> {
+    using type = KeptStager<N, K, WAVES>;
+};
+
 // The 16 x 32 piece of a staged tile that a matrix instruction takes: index
 // m0 + (lane & 15), contraction k = 32 * s + 8 * (lane >> 4) .. + 7.
-template <int N, int K, bool COLUMNS>
+template <int N, int K, Layout L>
 struct Reader {
     template <int S>
     __device__ __forceinline__ static bf16x8 read(const TIDE_LDS char* lds, int m0, int lane) {
-        if constexpr (COLUMNS) {
+        if constexpr (L != kRows) {
             constexpr int kRow = 2 * N;
             const int g = lane >> 4, i = lane & 15;
             const int k = 32 * S + 8 * g + (i >> 2);
@@ -171,7 +259,7 @@ __device__ __forceinline__ void tile_barrier() {
 
 // The S-th 32 contraction elements of a staged tile of K: their reads, and
 // their matrix instructions.
-template <int BI, int BJ, int K, int TI, int TJ, bool CA, bool CB, int S>
+template <int BI, int BJ, int K, int TI, int TJ, Layout CA, Layout CB, int S>
 __device__ __forceinline__ void read_part(const TIDE_LDS char* la, const TIDE_LDS char* lb, int i0,
                                           int j0, int lane, bf16x8 (&a)[TI], bf16x8 (&b)[TJ]) {
 #pragma unroll
@@ -216,13 +304,13 @@ __device__ __forceinline__ void interleave() {
 // of four waves in opposite phases (four barriers a step) 1175, 32x32x16
 // instructions 1300.  The matrix pipes are busy 66% of the cycles then, and the
 // clock is down to 1.75 GHz: what bounds it is power.
-template <int BI, int BJ, int K, int TI, int TJ, bool CA, bool CB, typename SA, typename SB>
+template <int BI, int BJ, int K, int TI, int TJ, Layout CA, Layout CB, typename SA, typename SB>
 __device__ __forceinline__ void deep_step(TIDE_LDS char* __restrict__ next,
                                           TIDE_LDS char* __restrict__ now, bool more, bool more2,
                                           SA& sa, SB& sb, int64_t valid, int wi, int wj, int lane,
                                           bf16x8 (&a0)[TI], bf16x8 (&b0)[TJ],
                                           f32x4v (&acc)[TI][TJ]) {
-    constexpr int kReads = TI * (CA ? 2 : 1) + TJ * (CB ? 2 : 1);
+    constexpr int kReads = TI * (CA == kRows ? 1 : 2) + TJ * (CB == kRows ? 1 : 2);
     bf16x8 a1[TI], b1[TJ];
     read_part<BI, BJ, K, TI, TJ, CA, CB, 1>(now, now + SA::kBytes, wi, wj, lane, a1, b1);
     multiply_part<TI, TJ>(a0, b0, acc);
@@ -244,7 +332,7 @@ __device__ __forceinline__ void deep_step(TIDE_LDS char* __restrict__ next,
 // holds several: other workgroups fill the gaps, and fewer registers let more
 // of them in (the step above on 128 x 128 tiles: 8% slower on 1003 x 1001 x
 // 8192, 15% on 2048 x 5120 x 13824).
-template <int BI, int BJ, int K, int TI, int TJ, bool CA, bool CB, typename SA, typename SB>
+template <int BI, int BJ, int K, int TI, int TJ, Layout CA, Layout CB, typename SA, typename SB>
 __device__ __forceinline__ void plain_step(TIDE_LDS char* __restrict__ next,
                                            const TIDE_LDS char* __restrict__ now, bool more, SA& sa,
                                            SB& sb, int64_t valid, int wi, int wj, int lane,
@@ -274,14 +362,14 @@ __device__ __forceinline__ void plain_step(TIDE_LDS char* __restrict__ next,
 
 // The loop over the contraction elements [k0, k1) of `depth` (the longer
 // operand's) of the tile at (i0, j0), with two tiles of K of them in LDS.
-template <int BI, int BJ, int K, int WI, int WJ, bool CA, bool CB>
+template <int BI, int BJ, int K, int WI, int WJ, Layout CA, Layout CB>
 __device__ __forceinline__ void tile_loop(const Operand& A, const Operand& B, int64_t depth,
                                           int64_t k0, int64_t k1, int64_t i0, int64_t j0,
                                           TIDE_LDS char* lds,
                                           f32x4v (&acc)[BI / WI / 16][BJ / WJ / 16]) {
     constexpr int kWaves = WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
-    using SA = Stager<BI, K, kWaves, CA, (K > 64)>;
-    using SB = Stager<BJ, K, kWaves, CB>;
+    using SA = typename StagerOf<BI, K, kWaves, CA, (K > 64)>::type;
+    using SB = typename StagerOf<BJ, K, kWaves, CB, false>::type;
     constexpr int kTile = SA::kBytes + SB::kBytes;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -298,6 +386,8 @@ __device__ __forceinline__ void tile_loop(const Operand& A, const Operand& B, in
     const int steps = (int)((k1 - k0 + K - 1) / K);
     int64_t valid = depth - k0;
     int at = 0;
+    sa.prime();
+    sb.prime();
     sa.stage(lds, valid);
     sb.stage(lds + SA::kBytes, valid);
     if constexpr (kWaves == 8) {
