@@ -7,7 +7,9 @@
 // contiguous over the wave), so the 4 lanes of a quad hold a block and its
 // maximum takes two lane exchanges.  Rows are cut into units of 8 columns and
 // the units of all rows dealt out in order, so that narrow and wide matrices
-// fill the chip alike.
+// fill the chip alike.  Nontemporal accesses measured (8192 x 8192): pack 35.4
+// us with both, 40.0 with the loads only, 38.2 with the stores only, 43.8 with
+// none; unpack 30.0 with the stores only, 36.0 with both, 39.6 with none.
 #include <hip/hip_runtime.h>
 
 #include "act8.h"
@@ -41,21 +43,27 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const uint16_t* x, int64
     const int64_t row0 = first / per_row;
     const uint32_t unit0 = (uint32_t)(first - row0 * per_row);
     uint8_t* scales = out + act8_scale_offset(rows, cols);
-    float v[kUnits][8];
+    u32x4v w[kUnits];
     UnitAt at[kUnits];
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
         at[k] = unit_at(row0, unit0, per_row, k);
         const int64_t c = (int64_t)at[k].unit * 8;
-        load8(x + at[k].row * ldx + c, at[k].row < rows ? cols - c : 0, v[k]);
+        w[k] = 0;
+        if (at[k].row < rows && c + 8 <= cols) w[k] = load8_raw<true>(x + at[k].row * ldx + c);
     }
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
+        const int64_t c = (int64_t)at[k].unit * 8;
+        float v[8];
+        widen(w[k], v);
+        if (at[k].row < rows && c < cols && c + 8 > cols)
+            load8(x + at[k].row * ldx + c, cols - c, v);
         act8_u32x2 q;
-        const int e = act8_pack8(v[k], &q);
+        const int e = act8_pack8(v, &q);
         if (at[k].row >= rows) continue;
         const int64_t u = at[k].row * per_row + at[k].unit;
-        *(TIDE_GLOBAL_AS u32x2*)(out + u * 8) = q;
+        __builtin_nontemporal_store(q, (TIDE_GLOBAL_AS u32x2*)(out + u * 8));
         if ((at[k].unit & 3) == 0) *(TIDE_GLOBAL_AS uint8_t*)(scales + u / 4) = (uint8_t)(e + 127);
     }
 }
@@ -86,7 +94,7 @@ __global__ __launch_bounds__(kThreads) void unpack_kernel(const uint8_t* in, int
         const int64_t c = (int64_t)at[k].unit * 8;
         float v[8];
         act8_unpack8(q[k], act8_scale(s[k]), v);
-        store8(x + at[k].row * ldx + c, cols - c, v);
+        store8<true>(x + at[k].row * ldx + c, cols - c, v);
     }
 }
 

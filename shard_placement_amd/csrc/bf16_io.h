@@ -10,7 +10,6 @@ namespace tide {
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
 // The same without alignment beyond the element's: rows may start anywhere.
-typedef u32x2 u32x2_any __attribute__((aligned(2)));
 typedef u32x4v u32x4_any __attribute__((aligned(2)));
 
 #define TIDE_GLOBAL_AS __attribute__((address_space(1)))
@@ -31,55 +30,46 @@ __device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
+// Eight consecutive elements as they lie in memory.  ONCE: they are read once
+// and need no place in the caches.
+template <bool ONCE = false>
+__device__ __forceinline__ u32x4v load8_raw(const uint16_t* p) {
+    if constexpr (ONCE)
+        return __builtin_nontemporal_load((const TIDE_GLOBAL_AS u32x4_any*)p);
+    else
+        return *(const TIDE_GLOBAL_AS u32x4_any*)p;
+}
+__device__ __forceinline__ void widen(u32x4v w, float (&v)[8]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        v[2 * k] = bf16_lo(w[k]);
+        v[2 * k + 1] = bf16_hi(w[k]);
+    }
+}
+
 // Eight consecutive elements of a row, of which the first n are there.
 __device__ __forceinline__ void load8(const uint16_t* p, int64_t n, float (&v)[8]) {
     if (n >= 8) {
-        const u32x4v w = *(const TIDE_GLOBAL_AS u32x4_any*)p;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[2 * k] = bf16_lo(w[k]);
-            v[2 * k + 1] = bf16_hi(w[k]);
-        }
+        widen(load8_raw(p), v);
         return;
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = k < n ? bf16_at(p + k) : 0.0f;
 }
 
+template <bool ONCE = false>
 __device__ __forceinline__ void store8(uint16_t* p, int64_t n, const float (&v)[8]) {
     if (n >= 8) {
         const u32x4v w = {to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[4], v[5]),
                           to_bf16x2(v[6], v[7])};
-        *(TIDE_GLOBAL_AS u32x4_any*)p = w;
+        if constexpr (ONCE)
+            __builtin_nontemporal_store(w, (TIDE_GLOBAL_AS u32x4_any*)p);
+        else
+            *(TIDE_GLOBAL_AS u32x4_any*)p = w;
         return;
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-        if (k < n) *(TIDE_GLOBAL_AS uint16_t*)(p + k) = to_bf16(v[k]);
-}
-
-// Four consecutive elements of a row, of which the first n are there.
-__device__ __forceinline__ void load4(const uint16_t* p, int64_t n, float (&v)[4]) {
-    if (n >= 4) {
-        const u32x2 w = *(const TIDE_GLOBAL_AS u32x2_any*)p;
-        v[0] = bf16_lo(w.x);
-        v[1] = bf16_hi(w.x);
-        v[2] = bf16_lo(w.y);
-        v[3] = bf16_hi(w.y);
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = k < n ? bf16_at(p + k) : 0.0f;
-}
-
-__device__ __forceinline__ void store4(uint16_t* p, int64_t n, const float (&v)[4]) {
-    if (n >= 4) {
-        const u32x2 w = {to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3])};
-        *(TIDE_GLOBAL_AS u32x2_any*)p = w;
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
         if (k < n) *(TIDE_GLOBAL_AS uint16_t*)(p + k) = to_bf16(v[k]);
 }
 

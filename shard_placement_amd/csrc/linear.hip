@@ -295,18 +295,6 @@ struct Gemv {
 constexpr int kGemvRows = 8;
 constexpr int kGemvThreads = 256;
 
-__device__ __forceinline__ u32x4v load_once(const uint16_t* p) {
-    return __builtin_nontemporal_load((const TIDE_GLOBAL_AS u32x4_any*)p);
-}
-
-__device__ __forceinline__ void widen(u32x4v w, float (&v)[8]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        v[2 * k] = bf16_lo(w[k]);
-        v[2 * k + 1] = bf16_hi(w[k]);
-    }
-}
-
 template <int T>
 __global__ __launch_bounds__(kGemvThreads, 4) void gemv_kernel(Gemv p) {
     __shared__ float part[kGemvThreads / 64][T][kGemvRows];
@@ -324,9 +312,9 @@ __global__ __launch_bounds__(kGemvThreads, 4) void gemv_kernel(Gemv p) {
     auto step = [&](int64_t k, int seen) __attribute__((always_inline)) {
         u32x4v wv[kGemvRows], xv[T];
 #pragma unroll
-        for (int r = 0; r < kGemvRows; ++r) wv[r] = load_once(w[r] + k);
+        for (int r = 0; r < kGemvRows; ++r) wv[r] = load8_raw<true>(w[r] + k);
 #pragma unroll
-        for (int t = 0; t < T; ++t) xv[t] = *(const TIDE_GLOBAL_AS u32x4_any*)(x[t] + k);
+        for (int t = 0; t < T; ++t) xv[t] = load8_raw(x[t] + k);
 #pragma unroll
         for (int r = 0; r < kGemvRows; ++r) {
             float v[8];
@@ -390,7 +378,7 @@ constexpr int kFewStep = 128;
 constexpr int kFewPitch = kFewRows + 4;  // floats of a token's sums in LDS
 
 __device__ __forceinline__ bf16x8 load_frag(const uint16_t* p) {
-    return __builtin_bit_cast(bf16x8, *(const TIDE_GLOBAL_AS u32x4_any*)p);
+    return __builtin_bit_cast(bf16x8, load8_raw(p));
 }
 // The first n of 8 elements, the others 0.
 __device__ __forceinline__ bf16x8 load_frag(const uint16_t* p, int64_t n) {
@@ -522,11 +510,11 @@ __global__ __launch_bounds__(kPadThreads) void pad_kernel(const uint16_t* in, in
 
 // dz = dy act'(z) rounded to bf16, rows of `width` elements with zeros behind
 // the N-th, and the column sums of dz before the rounding over each chunk of
-// rows (one row of `sums` for each chunk).  A workgroup takes 256 columns of a
-// chunk: 32 lanes of 8 columns, 8 rows at a time, and a lane has the loads of
-// kDzRows such rows in flight.
+// rows (one row of `sums` for each chunk).  A lane keeps its 8 columns through
+// the chunk's rows, so a workgroup reads runs of up to 4 KB of each row (with
+// runs of 512 bytes 2048 x 13824 took 37 us), and has the loads of kDzRows
+// rows in flight.
 constexpr int kDzThreads = 256;
-constexpr int kDzCols = 256;
 constexpr int kDzRows = 4;
 
 struct DzArgs {
@@ -540,64 +528,67 @@ struct DzArgs {
     int32_t col_groups;
 };
 
-template <int ACT>
-__global__ __launch_bounds__(kDzThreads) void dz_kernel(DzArgs p) {
-    __shared__ float part[8][kDzCols];
-    const int64_t cg = blockIdx.x % p.col_groups, ch = blockIdx.x / p.col_groups;
-    const int lc = threadIdx.x & 31, lr = threadIdx.x >> 5;
-    const int64_t c = cg * kDzCols + lc * 8;
-    const int64_t t1 = min(p.T, (ch + 1) * p.chunk);
+// One lane's columns c .. c + 7 through a chunk; WHOLE: all of them exist.
+template <int ACT, bool WHOLE>
+__device__ __forceinline__ void dz_lane(const DzArgs& p, int64_t c, int64_t t0, int64_t t1,
+                                        float (&sum)[8]) {
     const int64_t pitch = act8_pitch(p.N);
-    float sum[8] = {};
-    if (c < p.N) {
-        for (int64_t t0 = ch * p.chunk + lr; t0 < t1; t0 += 8 * kDzRows) {
-            float v[kDzRows][8];
-            u32x2 q[kDzRows];
-            uint32_t s[kDzRows];
+    const uint8_t* scales = p.z + p.T * pitch;
+    for (; t0 < t1; t0 += kDzRows) {
+        u32x4v y[kDzRows];
+        float v[kDzRows][8];
+        u32x2 q[kDzRows];
+        uint32_t s[kDzRows];
 #pragma unroll
-            for (int u = 0; u < kDzRows; ++u) {
-                const int64_t t = t0 + 8 * u;
-                load8(p.dy + t * p.ld + c, t < t1 ? p.N - c : 0, v[u]);
-                if constexpr (ACT != TIDE_ACT_NONE) {
-                    q[u] = 0;
-                    s[u] = 0;
-                    if (t < t1) {
-                        q[u] = *(const TIDE_GLOBAL_AS u32x2*)(p.z + t * pitch + c);
-                        s[u] = *(const TIDE_GLOBAL_AS uint8_t*)(p.z + p.T * pitch +
-                                                               (t * pitch + c) / kActBlock);
-                    }
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kDzRows; ++u) {
-                const int64_t t = t0 + 8 * u;
-                if (t >= t1) break;
-                if constexpr (ACT != TIDE_ACT_NONE) {
-                    float z[8];
-                    act8_unpack8(q[u], act8_scale(s[u]), z);
-                    apply_slope<ACT>(z, v[u]);
-                }
-                if (c + 8 > p.N) {
-#pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        if (c + r >= p.N) v[u][r] = 0.0f;
-                }
-#pragma unroll
-                for (int r = 0; r < 8; ++r) sum[r] += v[u][r];
-                if (p.dz) store8(p.dz + t * p.width + c, 8, v[u]);
+        for (int u = 0; u < kDzRows; ++u) {
+            const int64_t t = min(t0 + u, t1 - 1);
+            const uint16_t* from = p.dy + t * p.ld + c;
+            if constexpr (WHOLE)
+                y[u] = load8_raw(from);
+            else
+                load8(from, p.N - c, v[u]);
+            if constexpr (ACT != TIDE_ACT_NONE) {
+                q[u] = *(const TIDE_GLOBAL_AS u32x2*)(p.z + t * pitch + c);
+                s[u] = *(const TIDE_GLOBAL_AS uint8_t*)(scales + (t * pitch + c) / kActBlock);
             }
         }
+#pragma unroll
+        for (int u = 0; u < kDzRows; ++u) {
+            const int64_t t = t0 + u;
+            if (t >= t1) break;
+            if constexpr (WHOLE) widen(y[u], v[u]);
+            if constexpr (ACT != TIDE_ACT_NONE) {
+                float z[8];
+                act8_unpack8(q[u], act8_scale(s[u]), z);
+                apply_slope<ACT>(z, v[u]);
+            }
+            if constexpr (!WHOLE) {
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (c + r >= p.N) v[u][r] = 0.0f;
+            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r) sum[r] += v[u][r];
+            if (p.dz) store8(p.dz + t * p.width + c, 8, v[u]);
+        }
     }
+}
+
+template <int ACT>
+__global__ __launch_bounds__(kDzThreads) void dz_kernel(DzArgs p) {
+    const int64_t cg = blockIdx.x % p.col_groups, ch = blockIdx.x / p.col_groups;
+    const int64_t c = (cg * blockDim.x + threadIdx.x) * 8;
+    if (c >= p.N) return;
+    const int64_t t0 = ch * p.chunk, t1 = min(p.T, t0 + p.chunk);
+    float sum[8] = {};
+    if (c + 8 <= p.N)
+        dz_lane<ACT, true>(p, c, t0, t1, sum);
+    else
+        dz_lane<ACT, false>(p, c, t0, t1, sum);
     if (!p.sums) return;
 #pragma unroll
-    for (int r = 0; r < 8; ++r) part[lr][lc * 8 + r] = sum[r];
-    __syncthreads();
-    const int64_t col = cg * kDzCols + threadIdx.x;
-    if (col >= p.N) return;
-    float s = part[0][threadIdx.x];
-#pragma unroll
-    for (int r = 1; r < 8; ++r) s += part[r][threadIdx.x];
-    p.sums[ch * p.N + col] = s;
+    for (int r = 0; r < 8; ++r)
+        if (c + r < p.N) p.sums[ch * p.N + c + r] = sum[r];
 }
 
 // dbias from the chunks' sums: a wave's lane takes a column, the workgroup's
@@ -978,7 +969,8 @@ namespace {
 struct BackwardPlan {
     bool make_dz;       // dz is written (to the workspace), not dy itself
     int64_t width;      // of dz's rows there
-    int64_t chunk, chunks;
+    int dz_threads;
+    int64_t dz_groups, chunk, chunks;
     Source w;
     uint16_t* dz = nullptr;
     float* sums = nullptr;
@@ -1026,10 +1018,12 @@ BackwardPlan plan_backward(const tide_linear_backward_args& a, void* ws) {
     b.make_dz = products && T && N && (a.act != TIDE_ACT_NONE || !direct(a.dy, a.lddy, T, N));
     b.width = round_up(N, 8);
     if (b.make_dz) b.dz = c.take<uint16_t>(T * b.width);
-    // Chunks of rows for the column sums: enough workgroups to fill the chip,
-    // at most 256 chunks for the second pass to add up.
-    const int64_t groups = ceil_div(std::max<int64_t>(N, 1), kDzCols);
-    b.chunk = std::max<int64_t>(8, round_up(ceil_div(T, std::min<int64_t>(256, std::max<int64_t>(1, 2048 / groups))), 8));
+    // Chunks of rows: about 1024 workgroups, but where the column sums are
+    // wanted at least 32 rows, so that the partial sums stay few
+    b.dz_threads = (int)std::min<int64_t>(kDzThreads, round_up(ceil_div(std::max<int64_t>(N, 1), 8), 64));
+    b.dz_groups = ceil_div(std::max<int64_t>(N, 1), 8 * b.dz_threads);
+    b.chunk = std::max<int64_t>(a.dbias ? 32 : kDzRows,
+                                ceil_div(T, std::max<int64_t>(1, 1024 / b.dz_groups)));
     b.chunks = ceil_div(T, b.chunk);
     if (a.dbias) b.sums = c.take<float>(b.chunks * N);
     b.w = {a.weight, K, a.dx && T ? N : 0, K};
@@ -1086,8 +1080,8 @@ extern "C" tide_status tide_linear_backward(const tide_linear_backward_args* arg
         d.T = T;
         d.N = N;
         d.chunk = b.chunk;
-        d.col_groups = (int32_t)ceil_div(N, kDzCols);
-        TIDE_TRY(launch(dz_kernel_of(a.act), d.col_groups * b.chunks, kDzThreads, stream, d));
+        d.col_groups = (int32_t)b.dz_groups;
+        TIDE_TRY(launch(dz_kernel_of(a.act), b.dz_groups * b.chunks, b.dz_threads, stream, d));
     }
     if (a.dbias && N)
         TIDE_TRY(launch(dbias_kernel, ceil_div(N, 64), 64 * kDbWaves, stream,
