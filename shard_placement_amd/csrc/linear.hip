@@ -41,10 +41,30 @@ __device__ __forceinline__ float sigmoid(float u) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2E * u));
 }
 
+// exp(-z^2 / 2) and the normal distribution's Phi(z): erfc(x) = P(t) exp(-x^2),
+// t = 1 / (1 + p x), x = |z| / sqrt(2), by formula 7.1.26 of Abramowitz and
+// Stegun's handbook, off by at most 1.5e-7 (tests/test_linear_gpu.py bounds
+// what bf16 leaves of that).  The library's erff took 55 us where this takes
+// 38, in the gradient of 2048 x 13824 elements, which reads and writes 141 MB.
+__device__ __forceinline__ float normal_cdf(float z, float* bell) {
+    const float g = __builtin_amdgcn_exp2f(-0.5f * kLog2E * (z * z));
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f * kSqrtHalf, fabsf(z), 1.0f));
+    float poly = __builtin_fmaf(1.061405429f, t, -1.453152027f);
+    poly = __builtin_fmaf(poly, t, 1.421413741f);
+    poly = __builtin_fmaf(poly, t, -0.284496736f);
+    poly = __builtin_fmaf(poly, t, 0.254829592f);
+    const float tail = 0.5f * poly * t * g;
+    *bell = g;
+    return z < 0.0f ? tail : 1.0f - tail;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
     if constexpr (ACT == TIDE_ACT_RELU) return z > 0.0f ? z : 0.0f * z;
-    if constexpr (ACT == TIDE_ACT_GELU) return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+    if constexpr (ACT == TIDE_ACT_GELU) {
+        float bell;
+        return z * normal_cdf(z, &bell);
+    }
     if constexpr (ACT == TIDE_ACT_GELU_TANH)
         return z * sigmoid(z * __builtin_fmaf(kTanhA, z * z, kTanhC));
     if constexpr (ACT == TIDE_ACT_SILU) return z * sigmoid(z);
@@ -54,9 +74,11 @@ __device__ __forceinline__ float act_value(float z) {
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == TIDE_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f * z;
-    if constexpr (ACT == TIDE_ACT_GELU)
-        return 0.5f * (1.0f + erff(z * kSqrtHalf)) +
-               z * __builtin_amdgcn_exp2f(-0.5f * kLog2E * (z * z)) * kInvSqrt2Pi;
+    if constexpr (ACT == TIDE_ACT_GELU) {
+        float bell;
+        const float cdf = normal_cdf(z, &bell);
+        return __builtin_fmaf(z * kInvSqrt2Pi, bell, cdf);
+    }
     if constexpr (ACT == TIDE_ACT_GELU_TANH) {
         const float t = z * z;
         const float s = sigmoid(z * __builtin_fmaf(kTanhA, t, kTanhC));
@@ -356,15 +378,16 @@ __global__ __launch_bounds__(kGemvThreads, 4) void gemv_kernel(Gemv p) {
     finish(p.e, n0, threadIdx.x, threadIdx.x < p.e.J, v);
 }
 
-// ---- forward for few tokens ------------------------------------------------
+// ---- forward for few tokens, any alignment ------------------------------------------------
 
-// With at most 32 tokens the weight's bytes bound the product, and it is read
-// straight from memory into the matrix instructions' registers: a wave takes
-// 32 of W's rows, 128 contraction elements at a time, the next 128 in flight
-// while these are multiplied.  The waves of a workgroup share the 32 rows and
-// take the 128-element pieces in turn, so that they read runs of whole rows;
-// their sums meet in LDS, in the waves' order, before the epilogue.  Loads need
-// no alignment.
+// For operands that the tile kernels could only read as copies (rows that do
+// not start on 16 bytes): the weight is read once, straight from memory into
+// the matrix instructions' registers.  A wave takes 32 of W's rows, 128
+// contraction elements at a time, the next 128 in flight while these are
+// multiplied; the waves of a workgroup share the 32 rows and take the pieces
+// in turn, and their sums meet in LDS, in the waves' order, before the
+// epilogue.  (28672 x 8192 and 16 tokens: 115 us, the tile kernel on aligned
+// rows 80, so those go there.)
 struct Few {
     const uint16_t* x;
     int64_t ldx;
@@ -511,10 +534,12 @@ __global__ __launch_bounds__(kPadThreads) void pad_kernel(const uint16_t* in, in
 // dz = dy act'(z) rounded to bf16, rows of `width` elements with zeros behind
 // the N-th, and the column sums of dz before the rounding over each chunk of
 // rows (one row of `sums` for each chunk).  A lane keeps its 8 columns through
-// the chunk's rows, so a workgroup reads runs of up to 4 KB of each row (with
-// runs of 512 bytes 2048 x 13824 took 37 us), and has the loads of kDzRows
-// rows in flight.
-constexpr int kDzThreads = 256;
+// a quarter of the chunk's rows, so a workgroup reads runs of up to 4 KB of a
+// row, and has the loads of kDzRows rows in flight; the quarters' sums meet in
+// LDS.  (2048 x 13824 with relu: 29 us, 4.9 TB/s; 33 without
+// the quarters, two waves a SIMD.)
+constexpr int kDzLanes = 256;    // of 8 columns
+constexpr int kDzQuarters = 4;
 constexpr int kDzRows = 4;
 
 struct DzArgs {
@@ -575,17 +600,30 @@ __device__ __forceinline__ void dz_lane(const DzArgs& p, int64_t c, int64_t t0, 
 }
 
 template <int ACT>
-__global__ __launch_bounds__(kDzThreads) void dz_kernel(DzArgs p) {
+__global__ __launch_bounds__(kDzLanes* kDzQuarters) void dz_kernel(DzArgs p) {
+    extern __shared__ __attribute__((aligned(16))) float part[];  // [quarters - 1][lanes * 8]
+    const int lanes = blockDim.x / kDzQuarters;
+    const int quarter = threadIdx.x / lanes, lane = threadIdx.x - quarter * lanes;
     const int64_t cg = blockIdx.x % p.col_groups, ch = blockIdx.x / p.col_groups;
-    const int64_t c = (cg * blockDim.x + threadIdx.x) * 8;
-    if (c >= p.N) return;
-    const int64_t t0 = ch * p.chunk, t1 = min(p.T, t0 + p.chunk);
+    const int64_t c = (cg * lanes + lane) * 8;
+    const int64_t each = p.chunk / kDzQuarters;
+    const int64_t t0 = ch * p.chunk + quarter * each, t1 = min(p.T, t0 + each);
     float sum[8] = {};
     if (c + 8 <= p.N)
         dz_lane<ACT, true>(p, c, t0, t1, sum);
-    else
+    else if (c < p.N)
         dz_lane<ACT, false>(p, c, t0, t1, sum);
     if (!p.sums) return;
+    if (quarter) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) part[((quarter - 1) * 8 + r) * lanes + lane] = sum[r];
+    }
+    __syncthreads();
+    if (quarter) return;
+#pragma unroll
+    for (int u = 0; u < kDzQuarters - 1; ++u)
+#pragma unroll
+        for (int r = 0; r < 8; ++r) sum[r] += part[(u * 8 + r) * lanes + lane];
 #pragma unroll
     for (int r = 0; r < 8; ++r)
         if (c + r < p.N) p.sums[ch * p.N + c + r] = sum[r];
@@ -678,18 +716,21 @@ double product_us(const TileCost& c, const Shape& s, int64_t I, int64_t J) {
         const double used = (double)groups / (rounds * kCus);
         us = rounds * (steps * (c.step + c.power * used * used) + c.rest);
     }
-    // the partial sums are written and read once, at about 3.8 MB/us in all,
-    // and the join is a launch of its own
-    if (s.splits > 1) us += 3.0 + 4.0 * (double)s.splits * (double)I * (double)J / 3.8e6;
+    // partial sums: a compute unit writes 40 KB/us, the join is a launch of its
+    // own and reads 5.5 MB/us
+    if (s.splits > 1)
+        us += rounds * 4.0 * c.bi * c.bj / 40e3 +
+              3.0 + 4.0 * (double)s.splits * (double)I * (double)J / 5.5e6;
     return us;
 }
 
 // Up to 64 rows of outputs the A operand's bytes bound the product: narrow
-// tiles, and the contraction split until about 1024 workgroups keep loads in
-// flight (four on a compute unit).  A forward weight of more bytes than the
-// 256 MB cache holds is read 512 bytes of a row at a time and past the cache:
-// 91-104 us against 115-121 for 28672 x 8192 and 5 to 32 tokens; smaller
-// weights are faster from the cache (5120 x 5120: 20 us against 30).
+// tiles, and the contraction split until about two workgroups a compute unit
+// keep loads in flight (5120 x 5120 and 16 rows: 13.8 us, with one 15.6, with
+// four 16.8).  A forward weight of more bytes than the 256 MB cache holds is
+// read 512 bytes of a row at a time and past the cache, in tiles that fill
+// LDS: 80 us for 28672 x 8192 and 16 rows, 115 otherwise.  Smaller weights are
+// faster from the cache (5120 x 5120 and 24 rows: 30 us that way).
 // Otherwise the tile and split of the least estimated time.  2048 x 5120
 // outputs of depth 13824: 264 us with the 256 x 192 tiles this takes, 290 with
 // 256 x 256, 313 with 128 x 128.
@@ -700,7 +741,8 @@ Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth) {
         s.bi = 128;
         s.bj = J <= 16 ? 16 : J <= 32 ? 32 : 64;
         if (kind == kForward && s.bj <= 32 && I * depth > ((int64_t)128 << 20)) s.bk = 256;
-        set_split(&s, I, J, depth, 1024 / std::max<int64_t>(1, ceil_div(I, s.bi)));
+        const int64_t want = s.bk == 256 ? kCus : 2 * kCus;
+        set_split(&s, I, J, depth, want / std::max<int64_t>(1, ceil_div(I, s.bi)));
         return s;
     }
     double best = 0.0;
@@ -892,7 +934,7 @@ ForwardPlan plan_forward(const tide_linear_forward_args& a, void* ws) {
     ForwardPlan f;
     Carver c{static_cast<char*>(ws)};
     const int64_t T = a.tokens, N = a.out_features, K = a.in_features;
-    f.few = T <= kFewTokens;
+    f.few = T <= kFewTokens && !(direct(a.x, a.ldx, T, K) && direct(a.weight, K, N, K));
     f.bytes = 0;
     if (f.few) return f;
     f.x = {a.x, a.ldx, T, K};
@@ -969,7 +1011,7 @@ namespace {
 struct BackwardPlan {
     bool make_dz;       // dz is written (to the workspace), not dy itself
     int64_t width;      // of dz's rows there
-    int dz_threads;
+    int dz_lanes;
     int64_t dz_groups, chunk, chunks;
     Source w;
     uint16_t* dz = nullptr;
@@ -1018,12 +1060,14 @@ BackwardPlan plan_backward(const tide_linear_backward_args& a, void* ws) {
     b.make_dz = products && T && N && (a.act != TIDE_ACT_NONE || !direct(a.dy, a.lddy, T, N));
     b.width = round_up(N, 8);
     if (b.make_dz) b.dz = c.take<uint16_t>(T * b.width);
-    // Chunks of rows: about 1024 workgroups, but where the column sums are
-    // wanted at least 32 rows, so that the partial sums stay few
-    b.dz_threads = (int)std::min<int64_t>(kDzThreads, round_up(ceil_div(std::max<int64_t>(N, 1), 8), 64));
-    b.dz_groups = ceil_div(std::max<int64_t>(N, 1), 8 * b.dz_threads);
-    b.chunk = std::max<int64_t>(a.dbias ? 32 : kDzRows,
-                                ceil_div(T, std::max<int64_t>(1, 1024 / b.dz_groups)));
+    // Chunks of rows: about 512 workgroups of 16 waves, but where the column
+    // sums are wanted at least 32 rows, so that the partial sums stay few
+    const int64_t n = std::max<int64_t>(N, 1);
+    b.dz_lanes = (int)std::min<int64_t>(kDzLanes, round_up(ceil_div(n, 8), 64));
+    b.dz_groups = ceil_div(n, 8 * b.dz_lanes);
+    b.chunk = std::max<int64_t>(a.dbias ? 32 : kDzQuarters,
+                                ceil_div(T, std::max<int64_t>(1, 512 / b.dz_groups)));
+    b.chunk = round_up(b.chunk, kDzQuarters);
     b.chunks = ceil_div(T, b.chunk);
     if (a.dbias) b.sums = c.take<float>(b.chunks * N);
     b.w = {a.weight, K, a.dx && T ? N : 0, K};
@@ -1081,7 +1125,9 @@ extern "C" tide_status tide_linear_backward(const tide_linear_backward_args* arg
         d.N = N;
         d.chunk = b.chunk;
         d.col_groups = (int32_t)b.dz_groups;
-        TIDE_TRY(launch(dz_kernel_of(a.act), b.dz_groups * b.chunks, b.dz_threads, stream, d));
+        const int threads = b.dz_lanes * kDzQuarters;
+        const unsigned lds = a.dbias ? (kDzQuarters - 1) * b.dz_lanes * 8 * sizeof(float) : 0;
+        TIDE_TRY(launch_lds(dz_kernel_of(a.act), b.dz_groups * b.chunks, threads, lds, stream, d));
     }
     if (a.dbias && N)
         TIDE_TRY(launch(dbias_kernel, ceil_div(N, 64), 64 * kDbWaves, stream,
