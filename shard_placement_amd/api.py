@@ -338,10 +338,10 @@ def _index(t: torch.Tensor, what: str) -> int:
         raise TypeError("%s must be a torch.Tensor" % what)
     if t.dtype != torch.bfloat16:
         raise TideError(-6, "%s has dtype %s, expected %s" % (what, t.dtype, torch.bfloat16))
-    if not t.is_cuda:
-        raise TideError(-6, "%s is on %s, expected a GPU" % (what, t.device))
     if t.dim() != 2:
         raise TideError(-1, "%s has %d dimensions, expected 2" % (what, t.dim()))
+    if not t.is_cuda:
+        raise TideError(-6, "%s is on %s, expected a GPU" % (what, t.device))
     return t.get_device()
 
 
@@ -400,7 +400,9 @@ def _workspace(query, args, index):
     torch's allocator for each call: calls on different streams, or captured
     into different graphs, never share one."""
     n = ctypes.c_size_t(0)
-    check(query(ctypes.byref(args), ctypes.byref(n)), query.__name__)
+    status = query(ctypes.byref(args), ctypes.byref(n))
+    if status:
+        check(status, query.__name__)
     if not n.value:
         return None, None, 0
     t = torch.empty(n.value, dtype=torch.uint8, device=index)

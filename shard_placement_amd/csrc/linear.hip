@@ -191,9 +191,8 @@ struct Product {
 constexpr int kXcdCount = 8;
 constexpr int kBand = 4;
 
-__device__ __forceinline__ void tile_at(const Product& p, int64_t* ti, int64_t* tj, int64_t* sp) {
-    const int64_t total = gridDim.x;
-    int64_t b = blockIdx.x;
+__device__ __forceinline__ void tile_at(const Product& p, int64_t b, int64_t total, int64_t* ti,
+                                        int64_t* tj, int64_t* sp) {
     const int64_t each = total / kXcdCount, extra = total % kXcdCount;
     const int64_t x = b % kXcdCount, n = b / kXcdCount;
     b = x * each + (x < extra ? x : extra) + n;
@@ -211,29 +210,34 @@ __device__ __forceinline__ void tile_at(const Product& p, int64_t* ti, int64_t* 
 // returned before it writes again.
 __device__ __forceinline__ void wave_lds_order() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
+// LDS of a workgroup: two staged tiles, which the epilogue reuses.
+template <int BI, int BJ, int K>
+constexpr int kProductLds = 2 * (BI + BJ) * K * 2;
+
+// The tile of workgroup `block` of `blocks`.
 template <int BI, int BJ, int K, int WI, int WJ, Layout CA, Layout CB>
-__global__ __launch_bounds__(WI* WJ * 64, BI == 256 ? 2 : 1) void product_kernel(Product p) {
+__device__ __forceinline__ void product_tile(const Product& p, int64_t block, int64_t blocks,
+                                             TIDE_LDS char* lds) {
     constexpr int TI = BI / WI / 16, TJ = BJ / WJ / 16;
     static_assert(TI % 2 == 0, "a wave holds whole checkpoint blocks");
-    __shared__ __attribute__((aligned(1024))) char lds[2 * (BI + BJ) * K * 2];
     int64_t ti, tj, sp;
-    tile_at(p, &ti, &tj, &sp);
+    tile_at(p, block, blocks, &ti, &tj, &sp);
     const int64_t i0 = ti * BI, j0 = tj * BJ;
     const int64_t k0 = sp * p.split_depth;
     const int64_t k1 = min(p.depth, k0 + p.split_depth);
     f32x4v acc[TI][TJ];
-    tile_loop<BI, BJ, K, WI, WJ, CA, CB>(p.A, p.B, p.depth, k0, k1, i0, j0, (TIDE_LDS char*)lds, acc);
+    tile_loop<BI, BJ, K, WI, WJ, CA, CB>(p.A, p.B, p.depth, k0, k1, i0, j0, lds, acc);
 
     // The accumulators pass through LDS, 16 rows of a wave at a time, so that
     // each lane ends with 8 consecutive columns and a row's stores are whole
     // lines.  The row pitch's extra 4 floats keep the writes off each other's
     // banks.
     constexpr int kRow = TI * 16, kPitch = kRow + 4, kLanes = kRow / 8;
-    static_assert(WI * WJ * 16 * kPitch * 4 <= (int)sizeof(lds), "the staging fits");
+    static_assert(WI * WJ * 16 * kPitch * 4 <= kProductLds<BI, BJ, K>, "the staging fits");
     tile_barrier();
     const int lane = threadIdx.x & 63;
     const int wave = threadIdx.x >> 6;
-    TIDE_LDS float* mine = (TIDE_LDS float*)(TIDE_LDS char*)lds + wave * 16 * kPitch;
+    TIDE_LDS float* mine = (TIDE_LDS float*)lds + wave * 16 * kPitch;
     const int64_t iw = i0 + (wave / WJ) * kRow + (lane % kLanes) * 8;
     const int64_t jw = j0 + (wave % WJ) * TJ * 16 + lane / kLanes;
 #pragma unroll
@@ -260,6 +264,24 @@ __global__ __launch_bounds__(WI* WJ * 64, BI == 256 ? 2 : 1) void product_kernel
         }
         wave_lds_order();
     }
+}
+
+template <int BI, int BJ, int K, int WI, int WJ, Layout CA, Layout CB>
+__global__ __launch_bounds__(WI* WJ * 64, BI == 256 ? 2 : 1) void product_kernel(Product p) {
+    __shared__ __attribute__((aligned(1024))) char lds[kProductLds<BI, BJ, K>];
+    product_tile<BI, BJ, K, WI, WJ, CA, CB>(p, blockIdx.x, gridDim.x, (TIDE_LDS char*)lds);
+}
+
+// dx and dW in one launch, for shapes too small to fill the chip one after the
+// other: the first `n_w` workgroups take dW's tiles, the others dx's.
+template <int BJ, int WI, int WJ>
+__global__ __launch_bounds__(256) void pair_kernel(Product w, Product x, int32_t n_w) {
+    __shared__ __attribute__((aligned(1024))) char lds[kProductLds<128, 128, 64>];
+    if ((int)blockIdx.x < n_w)
+        product_tile<128, 128, 64, 2, 2, kKept, kColumns>(w, blockIdx.x, n_w, (TIDE_LDS char*)lds);
+    else
+        product_tile<128, BJ, 64, WI, WJ, kColumns, kRows>(x, blockIdx.x - n_w, gridDim.x - n_w,
+                                                           (TIDE_LDS char*)lds);
 }
 
 // The sums of a split contraction added up in the splits' order, then the
@@ -541,6 +563,7 @@ __global__ __launch_bounds__(kPadThreads) void pad_kernel(const uint16_t* in, in
 constexpr int kDzLanes = 256;    // of 8 columns
 constexpr int kDzQuarters = 4;
 constexpr int kDzRows = 4;
+constexpr int64_t kDzOneChunk = 64;
 
 struct DzArgs {
     const uint16_t* dy;
@@ -549,6 +572,7 @@ struct DzArgs {
     uint16_t* dz;      // or NULL: sums only
     int64_t width;
     float* sums;       // or NULL
+    uint16_t* dbias;   // the one chunk's sums go there, or NULL
     int64_t T, N, chunk;
     int32_t col_groups;
 };
@@ -613,7 +637,7 @@ __global__ __launch_bounds__(kDzLanes* kDzQuarters) void dz_kernel(DzArgs p) {
         dz_lane<ACT, true>(p, c, t0, t1, sum);
     else if (c < p.N)
         dz_lane<ACT, false>(p, c, t0, t1, sum);
-    if (!p.sums) return;
+    if (!p.sums && !p.dbias) return;
     if (quarter) {
 #pragma unroll
         for (int r = 0; r < 8; ++r) part[((quarter - 1) * 8 + r) * lanes + lane] = sum[r];
@@ -625,8 +649,13 @@ __global__ __launch_bounds__(kDzLanes* kDzQuarters) void dz_kernel(DzArgs p) {
 #pragma unroll
         for (int r = 0; r < 8; ++r) sum[r] += part[(u * 8 + r) * lanes + lane];
 #pragma unroll
-    for (int r = 0; r < 8; ++r)
-        if (c + r < p.N) p.sums[ch * p.N + c + r] = sum[r];
+    for (int r = 0; r < 8; ++r) {
+        if (c + r >= p.N) continue;
+        if (p.dbias)
+            *(TIDE_GLOBAL_AS uint16_t*)(p.dbias + c + r) = to_bf16(sum[r]);
+        else
+            p.sums[ch * p.N + c + r] = sum[r];
+    }
 }
 
 // dbias from the chunks' sums: a wave's lane takes a column, the workgroup's
@@ -779,15 +808,27 @@ ProductKernel of_kind(Kind k) {
     }
 }
 
+void set_shape(Product* p, const Shape& s, float* partial) {
+    p->tiles_i = s.tiles_i;
+    p->tiles_j = s.tiles_j;
+    p->splits = s.splits;
+    p->split_depth = s.split_depth;
+    p->partial = partial;
+    p->partial_pitch = round_up(p->e.I, kActBlock);
+}
+
+int64_t grid_of(const Shape& s) { return (int64_t)s.tiles_i * s.tiles_j * s.splits; }
+
+tide_status run_join(const Product& p, tide_stream_t stream) {
+    if (p.splits == 1) return TIDE_OK;
+    return launch(join_kernel, ceil_div(p.e.J * p.partial_pitch / 8, kJoinThreads), kJoinThreads,
+                  stream, p);
+}
+
 tide_status run_product(Kind kind, Product p, const Shape& s, float* partial,
                         tide_stream_t stream) {
     if (p.e.I == 0 || p.e.J == 0) return TIDE_OK;
-    p.tiles_i = s.tiles_i;
-    p.tiles_j = s.tiles_j;
-    p.splits = s.splits;
-    p.split_depth = s.split_depth;
-    p.partial = partial;
-    p.partial_pitch = round_up(p.e.I, kActBlock);
+    set_shape(&p, s, partial);
     ProductKernel k;
     int threads = 256;
     if (s.bi == 256) {
@@ -804,11 +845,8 @@ tide_status run_product(Kind kind, Product p, const Shape& s, float* partial,
     } else {
         k = s.bk == 256 ? product_kernel<128, 16, 256, 4, 1, kRows, kRows> : of_kind<128, 16, 64, 4, 1>(kind);
     }
-    const int64_t grid = (int64_t)s.tiles_i * s.tiles_j * s.splits;
-    tide_status st = launch(k, grid, threads, stream, p);
-    if (st != TIDE_OK || s.splits == 1) return st;
-    return launch(join_kernel, ceil_div(p.e.J * p.partial_pitch / 8, kJoinThreads), kJoinThreads,
-                  stream, p);
+    const tide_status st = launch(k, grid_of(s), threads, stream, p);
+    return st == TIDE_OK ? run_join(p, stream) : st;
 }
 
 // Whether the kernels can read rows of this matrix where they lie.
@@ -1010,6 +1048,7 @@ namespace {
 
 struct BackwardPlan {
     bool make_dz;       // dz is written (to the workspace), not dy itself
+    bool pair = false;  // dx and dW share a launch
     int64_t width;      // of dz's rows there
     int dz_lanes;
     int64_t dz_groups, chunk, chunks;
@@ -1068,14 +1107,23 @@ BackwardPlan plan_backward(const tide_linear_backward_args& a, void* ws) {
     b.chunk = std::max<int64_t>(a.dbias ? 32 : kDzQuarters,
                                 ceil_div(T, std::max<int64_t>(1, 512 / b.dz_groups)));
     b.chunk = round_up(b.chunk, kDzQuarters);
+    // few rows are one chunk, whose sums are dbias
+    if (a.dbias && T <= kDzOneChunk) b.chunk = round_up(std::max<int64_t>(T, 1), kDzQuarters);
     b.chunks = ceil_div(T, b.chunk);
-    if (a.dbias) b.sums = c.take<float>(b.chunks * N);
+    if (a.dbias && b.chunks != 1) b.sums = c.take<float>(b.chunks * N);
     b.w = {a.weight, K, a.dx && T ? N : 0, K};
     b.w.plan(c);
     b.w_shape = choose(kGradWeight, K, N, T);
     // the 256-wide tiles read x from here, widened (tile_product.h)
     if (a.dweight && N && b.w_shape.bi == 256) b.x = c.take<uint16_t>(T * act8_pitch(K));
     b.in_shape = choose(kGradInput, K, T, b.width);
+    // Both in one launch where together they are at most two workgroups a
+    // compute unit; then a short contraction is cheaper whole than split and
+    // joined (a join is 5 us, a step of 64 0.6)
+    b.pair = a.dx && a.dweight && T && N && K && b.in_shape.bi == 128 && b.w_shape.bi == 128 &&
+             b.w_shape.bj == 128 && b.w_shape.splits == 1 &&
+             grid_of(b.in_shape) + grid_of(b.w_shape) <= 2 * kCus;
+    if (b.pair && b.width <= 1024) set_split(&b.in_shape, K, T, b.width, 1);
     int64_t floats = 0;
     if (a.dx) floats = std::max(floats, partial_floats(b.in_shape, K, T));
     if (a.dweight) floats = std::max(floats, partial_floats(b.w_shape, K, N));
@@ -1121,6 +1169,7 @@ extern "C" tide_status tide_linear_backward(const tide_linear_backward_args* arg
         d.dz = b.make_dz ? b.dz : nullptr;
         d.width = b.width;
         d.sums = b.sums;
+        d.dbias = b.chunks == 1 ? static_cast<uint16_t*>(a.dbias) : nullptr;
         d.T = T;
         d.N = N;
         d.chunk = b.chunk;
@@ -1129,39 +1178,49 @@ extern "C" tide_status tide_linear_backward(const tide_linear_backward_args* arg
         const unsigned lds = a.dbias ? (kDzQuarters - 1) * b.dz_lanes * 8 * sizeof(float) : 0;
         TIDE_TRY(launch_lds(dz_kernel_of(a.act), b.dz_groups * b.chunks, threads, lds, stream, d));
     }
-    if (a.dbias && N)
+    if (a.dbias && N && b.chunks != 1)
         TIDE_TRY(launch(dbias_kernel, ceil_div(N, 64), 64 * kDbWaves, stream,
                         static_cast<const float*>(b.sums), b.chunks, N,
                         static_cast<uint16_t*>(a.dbias)));
     if (K == 0) return TIDE_OK;
 
     Source dz = {b.make_dz ? b.dz : a.dy, b.make_dz ? b.width : a.lddy, T, b.make_dz ? b.width : N};
+    Product x = {}, w = {};
     if (a.dx && T) {
         TIDE_TRY(b.w.fill(stream));
-        Product p = {};
-        p.A = b.w.operand(true);
-        p.B = dz.operand(false);
-        p.depth = b.width;  // dz's columns behind the N-th are 0
-        p.e.I = K;
-        p.e.J = T;
-        p.e.out = static_cast<uint16_t*>(a.dx);
-        p.e.ldo = a.lddx;
-        TIDE_TRY(run_product(kGradInput, p, b.in_shape, b.partial, stream));
+        x.A = b.w.operand(true);
+        x.B = dz.operand(false);
+        x.depth = b.width;  // dz's columns behind the N-th are 0
+        x.e.I = K;
+        x.e.J = T;
+        x.e.out = static_cast<uint16_t*>(a.dx);
+        x.e.ldo = a.lddx;
     }
     if (a.dweight && N) {
-        Product p = {};
-        p.A = {a.x_kept, act8_pitch(K), act8_pitch(K), T};
+        w.A = {a.x_kept, act8_pitch(K), act8_pitch(K), T};
         if (b.w_shape.bi == 256) {
             TIDE_TRY(tide_act8_unpack(a.x_kept, T, K, b.x, act8_pitch(K), stream));
-            p.A.p = b.x;
+            w.A.p = b.x;
         }
-        p.B = dz.operand(true);
-        p.depth = T;
-        p.e.I = K;
-        p.e.J = N;
-        p.e.out = static_cast<uint16_t*>(a.dweight);
-        p.e.ldo = K;
-        TIDE_TRY(run_product(kGradWeight, p, b.w_shape, b.partial, stream));
+        w.B = dz.operand(true);
+        w.depth = T;
+        w.e.I = K;
+        w.e.J = N;
+        w.e.out = static_cast<uint16_t*>(a.dweight);
+        w.e.ldo = K;
     }
+    if (b.pair) {
+        set_shape(&w, b.w_shape, nullptr);
+        set_shape(&x, b.in_shape, b.partial);
+        auto k = b.in_shape.bj == 128  ? pair_kernel<128, 2, 2>
+                 : b.in_shape.bj == 64 ? pair_kernel<64, 2, 2>
+                 : b.in_shape.bj == 32 ? pair_kernel<32, 4, 1>
+                                       : pair_kernel<16, 4, 1>;
+        const int64_t n_w = grid_of(b.w_shape);
+        TIDE_TRY(launch(k, n_w + grid_of(b.in_shape), 256, stream, w, x, (int32_t)n_w));
+        return run_join(x, stream);
+    }
+    if (a.dx && T) TIDE_TRY(run_product(kGradInput, x, b.in_shape, b.partial, stream));
+    if (a.dweight && N) TIDE_TRY(run_product(kGradWeight, w, b.w_shape, b.partial, stream));
     return TIDE_OK;
 }

@@ -19,15 +19,13 @@ tensors together.
 """
 from __future__ import annotations
 
-import contextlib
 from typing import Optional
 
 import torch
 
 from . import api
-from ._lib import TideError
+from ._lib import TideError, TideLinearBackwardArgs, TideLinearForwardArgs
 
-_nothing = contextlib.nullcontext()
 BLOCK = 32  # columns of a checkpoint that share a scale
 
 
@@ -50,6 +48,7 @@ class Act8:
         if flat.numel() < need:
             raise TideError(-1, "buffer holds %d bytes, need %d" % (flat.numel(), need))
         self.buffer = flat[:need]
+        self._gpu = buffer.get_device()  # -1: not a GPU
         pitch = -(-self.cols // BLOCK) * BLOCK
         values = self.rows * pitch
         self.data = self.buffer[:values].view(torch.float8_e4m3fn).view(self.rows, pitch)
@@ -60,48 +59,90 @@ class Act8:
         return api.tide_act8_bytes(rows, cols)
 
     def pack(self, x: torch.Tensor, stream=None) -> "Act8":
-        if x.shape != (self.rows, self.cols):
-            raise TideError(-1, "x is %s, expected [%d, %d]" % (list(x.shape), self.rows, self.cols))
-        api.tide_act8_pack(x, self.buffer, stream)
+        """Write the checkpoint of the bf16 matrix x."""
+        px, ldx = self._matrix(x, "x")
+        api._on_device(self._gpu, stream, api._pack_on, px, ldx, self.rows, self.cols,
+                       self.buffer.data_ptr())
         return self
 
     def unpack(self, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The bf16 matrix that the checkpoint stands for (allocated when not given)."""
         if out is None:
-            with torch.cuda.stream(stream) if stream is not None else _nothing:
-                out = torch.empty(self.rows, self.cols, dtype=torch.bfloat16,
-                                  device=self.buffer.device)
-        elif out.shape != (self.rows, self.cols):
-            raise TideError(-1, "out is %s, expected [%d, %d]"
-                            % (list(out.shape), self.rows, self.cols))
-        api.tide_act8_unpack(self.buffer, out, stream)
+            return api._on_device(self._gpu, stream, self._unpack_new)
+        px, ldx = self._matrix(out, "out")
+        api._on_device(self._gpu, stream, api._unpack_on, self.buffer.data_ptr(), self.rows,
+                       self.cols, px, ldx)
         return out
+
+    def _unpack_new(self, s):
+        out = torch.empty(self.rows, self.cols, dtype=torch.bfloat16, device=self.buffer.device)
+        api._unpack_on(s, self.buffer.data_ptr(), self.rows, self.cols, out.data_ptr(), self.cols)
+        return out
+
+    def _matrix(self, t, what):
+        if not isinstance(t, torch.Tensor) or t.shape != (self.rows, self.cols):
+            raise TideError(-1, "%s is %s, expected [%d, %d]"
+                            % (what, list(getattr(t, "shape", ())), self.rows, self.cols))
+        if api._index(t, what) != self._gpu:
+            raise TideError(-6, "%s is on %s, the checkpoint on %s"
+                            % (what, t.device, self.buffer.device))
+        return api._rows(t, what)
+
+    def _of(self, rows: int, cols: int, gpu: int, what: str) -> int:
+        """The address, as the checkpoint of a [rows, cols] matrix on this GPU."""
+        if self.rows != rows or self.cols != cols:
+            raise TideError(-1, "%s is a checkpoint of [%d, %d], expected [%d, %d]"
+                            % (what, self.rows, self.cols, rows, cols))
+        if self._gpu != gpu:
+            raise TideError(-6, "%s is on %s, expected cuda:%d" % (what, self.buffer.device, gpu))
+        return self.buffer.data_ptr()
 
 
 class Linear:
     """y = act(x weight^T + bias) + residual and its gradients.
 
-    weight [N, K], bias [N]: contiguous bf16 tensors; weight_grad and
+    weight [N, K], bias [N]: contiguous bf16 GPU tensors; weight_grad and
     bias_grad, where given, receive the gradients (overwritten by every
-    backward).  act: "none", "relu", "gelu", "gelu_tanh" or "silu"."""
+    backward).  act: "none", "relu", "gelu", "gelu_tanh" or "silu".  The four
+    tensors are checked here and kept; calls use their memory as it is then."""
 
     def __init__(self, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
                  act: str = "none", weight_grad: Optional[torch.Tensor] = None,
                  bias_grad: Optional[torch.Tensor] = None):
-        if weight.dim() != 2:
-            raise TideError(-1, "weight has %d dimensions, expected 2" % weight.dim())
-        api._act(act)
-        self.weight, self.bias, self.act = weight, bias, act
-        self.weight_grad, self.bias_grad = weight_grad, bias_grad
+        self._act = api._act(act)
+        self._gpu = api._index(weight, "weight")
+        self._shape = N, K = tuple(weight.shape)
+        for t, shape, what in ((weight, (N, K), "weight"), (bias, (N,), "bias"),
+                               (weight_grad, (N, K), "weight_grad"), (bias_grad, (N,), "bias_grad")):
+            if t is not None:
+                api._whole(t, shape, what, self._gpu)
+        self._weight, self._bias, self.act = weight, bias, act
+        self._weight_grad, self._bias_grad = weight_grad, bias_grad
+
+    weight = property(lambda self: self._weight)
+    bias = property(lambda self: self._bias)
+    weight_grad = property(lambda self: self._weight_grad)
+    bias_grad = property(lambda self: self._bias_grad)
 
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
                 out: Optional[torch.Tensor] = None, z: Optional[Act8] = None,
                 stream=None) -> torch.Tensor:
         """z: the checkpoint that receives act's argument (which backward
-        needs unless act is "none")."""
+        needs unless act is "none").  out is allocated when not given."""
+        N, K = self._shape
+        gpu = self._gpu
+        T = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() else 0
+        px, ldx = api._matrix(x, T, K, "x", gpu)
+        a = TideLinearForwardArgs(T, N, K, self._act, 0, px, ldx, self._weight.data_ptr())
+        if self._bias is not None:
+            a.bias = self._bias.data_ptr()
+        if residual is not None:
+            a.residual, a.ldr = api._matrix(residual, T, N, "residual", gpu)
+        if out is not None:
+            a.y, a.ldy = api._matrix(out, T, N, "out", gpu)
         if z is not None:
-            self._same(z, x.shape[0], self.weight.shape[0], "z")
-        return api.tide_linear_forward(x, self.weight, out, self.bias, residual, self.act,
-                                       None if z is None else z.buffer, stream)
+            a.z_kept = z._of(T, N, gpu, "z")
+        return api._on_device(gpu, stream, api._forward_on, a, out, gpu)
 
     def backward(self, dy: torch.Tensor, x: Optional[Act8] = None, z: Optional[Act8] = None,
                  dx: Optional[torch.Tensor] = None, input_grad: bool = True,
@@ -109,21 +150,28 @@ class Linear:
         """Writes weight_grad and bias_grad (where the layer has them) and
         returns dx (None with input_grad=False).  x: the checkpoint of
         forward's x, z: the one forward wrote.  The residual's gradient is dy."""
-        N, K = self.weight.shape
-        if x is not None:
-            self._same(x, dy.shape[0], K, "x")
-        if z is not None:
-            self._same(z, dy.shape[0], N, "z")
-        if not input_grad:
+        N, K = self._shape
+        gpu = self._gpu
+        T = dy.shape[0] if isinstance(dy, torch.Tensor) and dy.dim() else 0
+        pdy, lddy = api._matrix(dy, T, N, "dy", gpu)
+        a = TideLinearBackwardArgs(T, N, K, self._act, 0, pdy, lddy)
+        if self._act:
+            if z is None:
+                raise TideError(-1, "act %r needs the checkpoint of its argument" % self.act)
+            a.z_kept = z._of(T, N, gpu, "z")
+        if input_grad:
+            a.weight = self._weight.data_ptr()
+            if dx is None:
+                dx = True
+            else:
+                a.dx, a.lddx = api._matrix(dx, T, K, "dx", gpu)
+        else:
             dx = None
-        elif dx is None:
-            dx = True
-        return api.tide_linear_backward(dy, K, self.weight, None if x is None else x.buffer,
-                                        None if z is None else z.buffer, self.act, dx,
-                                        self.weight_grad, self.bias_grad, stream)
-
-    @staticmethod
-    def _same(kept: Act8, rows: int, cols: int, what: str) -> None:
-        if (kept.rows, kept.cols) != (rows, cols):
-            raise TideError(-1, "%s is a checkpoint of [%d, %d], expected [%d, %d]"
-                            % (what, kept.rows, kept.cols, rows, cols))
+        if self._weight_grad is not None:
+            if x is None:
+                raise TideError(-1, "weight_grad needs the checkpoint of x")
+            a.x_kept = x._of(T, K, gpu, "x")
+            a.dweight = self._weight_grad.data_ptr()
+        if self._bias_grad is not None:
+            a.dbias = self._bias_grad.data_ptr()
+        return api._on_device(gpu, stream, api._backward_on, a, dx, gpu)
