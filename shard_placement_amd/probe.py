@@ -6,9 +6,9 @@ reduce-scatter, and reports that TIDE lowers that interference roughly
 tenfold (Abstract of "The Endgame of
 FSDP Communication", weekinpapers.com; kongchang.com article, sections "The
 Root of FSDP2 Communication Overhead" and "Performance").  This probe times a
-bf16 GEMM (torch.matmul -> hipBLASLt) alone, then beside a train of
-reduce-scatter launches on another stream, under several ways of confining
-the reduce-scatter: all CUs with one short-lived workgroup per tile, a capped
+bf16 GEMM (torch.matmul -> hipBLASLt, or one of the layer's own products)
+alone, then beside a train of reduce-scatter launches on another stream,
+under several ways of confining the reduce-scatter: all CUs with one short-lived workgroup per tile, a capped
 grid of persistent workgroups, a CU-masked stream, and the launch size (a
 call cut into launches of about launch_mib MiB each).  The GEMM shape is
 chosen so that its grid is at most one workgroup per CU (checked with the
@@ -23,6 +23,7 @@ from typing import Dict, List, Optional, Sequence, Tuple
 import torch
 
 from . import api
+from .linear import Act8, Linear
 
 # A mode: (name, plan, max_workgroups, CU-mask width); 0 = unlimited / all.
 Mode = Tuple[str, "api.Plan", int, int]
@@ -84,22 +85,54 @@ def _new_stream():
     return torch.cuda.Stream()
 
 
-def _gemm_train(a, b, c, stream, n):
+# The GEMMs a probe can run beside the reduce-scatter: the library product, or
+# one of the layer's own (linear.Linear): the next layer's forward product, or
+# the weight gradient that a backward pass computes while the previous layer's
+# gradients are reduced.
+GEMMS = ("matmul", "forward", "weight-grad")
+
+
+def _gemm(kind: str, M: int, N: int, K: int, dev):
+    """(call, text) of a bf16 product with M x N results and K terms each;
+    the call computes it once on the current stream."""
+    if kind == "matmul":
+        a = torch.randn(M, K, device=dev, dtype=torch.bfloat16)
+        b = torch.randn(K, N, device=dev, dtype=torch.bfloat16)
+        c = torch.empty(M, N, device=dev, dtype=torch.bfloat16)
+        return (lambda: torch.matmul(a, b, out=c),
+                "bf16 [%d,%d]x[%d,%d] torch.matmul" % (M, K, K, N))
+    if kind == "forward":
+        x = torch.randn(M, K, device=dev, dtype=torch.bfloat16)
+        layer = Linear(torch.randn(N, K, device=dev, dtype=torch.bfloat16))
+        y = torch.empty(M, N, device=dev, dtype=torch.bfloat16)
+        return (lambda: layer.forward(x, out=y),
+                "bf16 forward of %d tokens through a [%d,%d] weight" % (M, N, K))
+    if kind == "weight-grad":
+        dy = torch.randn(K, M, device=dev, dtype=torch.bfloat16)
+        x8 = Act8(K, N, device=dev).pack(torch.randn(K, N, device=dev, dtype=torch.bfloat16))
+        w = torch.empty(M, N, device=dev, dtype=torch.bfloat16)
+        layer = Linear(w, weight_grad=torch.empty_like(w))
+        return (lambda: layer.backward(dy, x=x8, input_grad=False),
+                "bf16 gradient of a [%d,%d] weight from %d tokens kept in 8 bits" % (M, N, K))
+    raise ValueError("gemm must be one of %s" % ", ".join(GEMMS))
+
+
+def _gemm_train(gemm, stream, n):
     evs = [(torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True))
            for _ in range(n)]
     with torch.cuda.stream(stream):
         for e0, e1 in evs:
             e0.record(stream)
-            torch.matmul(a, b, out=c)
+            gemm()
             e1.record(stream)
     return evs
 
 
 def run(modes: Sequence[Mode], rs_bytes: int, iters: int = 40, M: int = 4096, N: int = 4096,
-        K: int = 8192, quiet_gc: bool = True) -> Dict:
-    """Time the GEMM alone, then, per mode, alone again and beside the
-    mode's reduce-scatter (the slowdown is against the mode's own alone
-    time).  The
+        K: int = 8192, quiet_gc: bool = True, gemm: str = "matmul") -> Dict:
+    """Time the GEMM (one of GEMMS) alone, then, per mode, alone again and
+    beside the mode's reduce-scatter (the slowdown is against the mode's own
+    alone time).  The
     reduce-scatter always runs on a CU-masked stream, which HIP backs with a
     hardware queue of its own (with the full mask when the mode has none):
     two streams that share a hardware queue run one after the other, which
@@ -109,25 +142,23 @@ def run(modes: Sequence[Mode], rs_bytes: int, iters: int = 40, M: int = 4096, N:
     and the garbage collector paused meanwhile (quiet_gc=False leaves both
     alone)."""
     if not quiet_gc:
-        return _run(modes, rs_bytes, iters, M, N, K)
+        return _run(modes, rs_bytes, iters, M, N, K, gemm)
     with _no_gc():
-        return _run(modes, rs_bytes, iters, M, N, K)
+        return _run(modes, rs_bytes, iters, M, N, K, gemm)
 
 
-def _run(modes, rs_bytes, iters, M, N, K) -> Dict:
+def _run(modes, rs_bytes, iters, M, N, K, kind="matmul") -> Dict:
     dev = torch.device("cuda")
     n_all = torch.cuda.get_device_properties(dev).multi_processor_count
-    a = torch.randn(M, K, device=dev, dtype=torch.bfloat16)
-    b = torch.randn(K, N, device=dev, dtype=torch.bfloat16)
-    c = torch.empty(M, N, device=dev, dtype=torch.bfloat16)
+    gemm, text = _gemm(kind, M, N, K, dev)
     gemm_stream = _new_stream()
     for _ in range(5):
-        torch.matmul(a, b, out=c)
+        gemm()
     torch.cuda.synchronize()
-    alone = _gemm_train(a, b, c, gemm_stream, iters)
+    alone = _gemm_train(gemm, gemm_stream, iters)
     torch.cuda.synchronize()
     t0 = _median([e0.elapsed_time(e1) for e0, e1 in alone])
-    out = {"gemm": "bf16 [%d,%d]x[%d,%d] torch.matmul" % (M, K, K, N),
+    out = {"gemm": text,
            "gemm_tflops_alone": round(2.0 * M * N * K / (t0 * 1e-3) / 1e12, 1),
            "t_gemm_alone_ms": round(t0, 4), "cus": n_all, "modes": []}
     for name, plan, max_wg, n_cu in modes:
@@ -143,7 +174,7 @@ def _run(modes, rs_bytes, iters, M, N, K) -> Dict:
             rs_alone = e0.elapsed_time(e1) / 3
             # the GEMM alone again, right before this mode (clocks drift
             # over a sweep; each mode is compared with its own baseline)
-            own = _gemm_train(a, b, c, gemm_stream, iters)
+            own = _gemm_train(gemm, gemm_stream, iters)
             torch.cuda.synchronize()
             t0m = _median([e0.elapsed_time(e1) for e0, e1 in own])
             # concurrent: enough reduce-scatters to cover the GEMM train twice
@@ -161,7 +192,7 @@ def _run(modes, rs_bytes, iters, M, N, K) -> Dict:
                 c1.record(rs_stream)
                 if k == 0:
                     gemm_stream.wait_event(r0)
-                    conc = _gemm_train(a, b, c, gemm_stream, iters)
+                    conc = _gemm_train(gemm, gemm_stream, iters)
             torch.cuda.synchronize()
             window = r0.elapsed_time(calls[-1][1])
             inside = [e1.elapsed_time(e2) for e1, e2 in conc
@@ -210,22 +241,20 @@ def _gemm_during(host_call, expect_ms, M, N, K) -> Dict:
     GEMM train of about half that length is queued on its own stream just
     before the call."""
     dev = torch.device("cuda")
-    a = torch.randn(M, K, device=dev, dtype=torch.bfloat16)
-    b = torch.randn(K, N, device=dev, dtype=torch.bfloat16)
-    c = torch.empty(M, N, device=dev, dtype=torch.bfloat16)
+    gemm, _ = _gemm("matmul", M, N, K, dev)
     s = _new_stream()
     for _ in range(5):
-        torch.matmul(a, b, out=c)
+        gemm()
     torch.cuda.synchronize()
-    alone = _gemm_train(a, b, c, s, 30)
+    alone = _gemm_train(gemm, s, 30)
     torch.cuda.synchronize()
     t0 = _median([e0.elapsed_time(e1) for e0, e1 in alone])
     n = max(4, min(400, int(0.5 * expect_ms / t0)))
-    conc = _gemm_train(a, b, c, s, n)
+    conc = _gemm_train(gemm, s, n)
     host_call()
     torch.cuda.synchronize()
     t1 = _median([e0.elapsed_time(e1) for e0, e1 in conc])
-    after = _gemm_train(a, b, c, s, 30)
+    after = _gemm_train(gemm, s, 30)
     torch.cuda.synchronize()
     t0 = _median([e0.elapsed_time(e1) for e0, e1 in alone + after])
     return {"gemm_alone_ms": round(t0, 4), "gemm_during_staging_ms": round(t1, 4),
@@ -241,20 +270,18 @@ def gemm_after_idle(idle_ms: Sequence[float] = (0, 2, 10, 30, 100, 300), n: int 
     import time
 
     dev = torch.device("cuda")
-    a = torch.randn(M, K, device=dev, dtype=torch.bfloat16)
-    b = torch.randn(K, N, device=dev, dtype=torch.bfloat16)
-    c = torch.empty(M, N, device=dev, dtype=torch.bfloat16)
+    gemm, _ = _gemm("matmul", M, N, K, dev)
     s = _new_stream()
     out = []
     with _no_gc():
         for _ in range(2):
-            _gemm_train(a, b, c, s, n)
+            _gemm_train(gemm, s, n)
             torch.cuda.synchronize()
         for _ in range(rounds):
             for idle in idle_ms:
                 torch.cuda.synchronize()
                 time.sleep(idle / 1e3)
-                evs = _gemm_train(a, b, c, s, n)
+                evs = _gemm_train(gemm, s, n)
                 torch.cuda.synchronize()
                 t = [1e3 * e0.elapsed_time(e1) for e0, e1 in evs]
                 out.append({"idle_ms": idle, "median_us": round(_median(t), 1),
@@ -278,6 +305,9 @@ def main(argv=None) -> int:
     ap.add_argument("--workload", default="5", help="workload key or name")
     ap.add_argument("--reps", type=int, default=3)
     ap.add_argument("--iters", type=int, default=40)
+    ap.add_argument("--gemm", default="matmul", choices=GEMMS,
+                    help="the product beside the reduce-scatter: the library's, or the layer's own "
+                         "forward product or weight gradient")
     ap.add_argument("--side", default="none",
                     choices=("none", "collect", "collect-frozen", "trim", "hold-lock"),
                     help="a side thread acting every 20 ms during the probe: a full garbage "
@@ -299,7 +329,7 @@ def main(argv=None) -> int:
     res = None
     for _ in range(a.reps):
         r = run([("default launches", st.plan, 0, 0)], harness.rs_bytes(w), iters=a.iters,
-                 quiet_gc=a.side == "none")
+                 quiet_gc=a.side == "none", gemm=a.gemm)
         if res is None:
             res = r
         else:
