@@ -234,7 +234,7 @@ __device__ __forceinline__ void product_tile(const Product& p, int64_t block, in
     // banks.
     constexpr int kRow = TI * 16, kPitch = kRow + 4, kLanes = kRow / 8;
     static_assert(WI * WJ * 16 * kPitch * 4 <= kProductLds<BI, BJ, K>, "the staging fits");
-    tile_barrier();
+    tile_barrier(lds, lds);
     const int lane = threadIdx.x & 63;
     const int wave = threadIdx.x >> 6;
     TIDE_LDS float* mine = (TIDE_LDS float*)lds + wave * 16 * kPitch;

@@ -253,8 +253,10 @@ struct Reader {
 
 // Every load into LDS has landed and every LDS read has returned, in every
 // wave: the staged tile can be read and the other one overwritten.
-__device__ __forceinline__ void tile_barrier() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+// The two tiles' addresses are operands so that, __restrict__ or not, the
+// compiler takes it to use that memory and moves no access across.
+__device__ __forceinline__ void tile_barrier(const TIDE_LDS char* a, const TIDE_LDS char* b) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::"s"(a), "s"(b) : "memory");
 }
 
 // The S-th 32 contraction elements of a staged tile of K: their reads, and
@@ -316,7 +318,7 @@ __device__ __forceinline__ void deep_step(TIDE_LDS char* __restrict__ next,
     multiply_part<TI, TJ>(a0, b0, acc);
     interleave<kReads>();
     __builtin_amdgcn_sched_barrier(0);
-    tile_barrier();
+    tile_barrier(now, next);
     __builtin_amdgcn_sched_barrier(0);
     if (more) read_part<BI, BJ, K, TI, TJ, CA, CB, 0>(next, next + SA::kBytes, wi, wj, lane, a0, b0);
     if (more2) {
@@ -324,6 +326,11 @@ __device__ __forceinline__ void deep_step(TIDE_LDS char* __restrict__ next,
         sb.stage(now + SA::kBytes, valid);
     }
     multiply_part<TI, TJ>(a1, b1, acc);
+    if constexpr (CB != kRows) {
+        // many short reads: the loads are issued before them
+        __builtin_amdgcn_sched_group_barrier(0x020, SA::kMine + SB::kMine, 0);
+        interleave<kReads>();
+    }
     __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -391,7 +398,7 @@ __device__ __forceinline__ void tile_loop(const Operand& A, const Operand& B, in
     sa.stage(lds, valid);
     sb.stage(lds + SA::kBytes, valid);
     if constexpr (kWaves == 8) {
-        tile_barrier();
+        tile_barrier(lds, lds + kTile);
         valid -= K;
         if (steps > 1) {
             sa.stage(lds + kTile, valid);
@@ -411,7 +418,7 @@ __device__ __forceinline__ void tile_loop(const Operand& A, const Operand& B, in
         step(false, false);
     } else {
         for (int s = 0; s < steps; ++s) {
-            tile_barrier();
+            tile_barrier(lds + at, lds + (at ^ kTile));
             valid -= K;
             plain_step<BI, BJ, K, TI, TJ, CA, CB>(lds + (at ^ kTile), lds + at, s + 1 < steps, sa, sb,
                                                valid, wi, wj, lane, acc);
