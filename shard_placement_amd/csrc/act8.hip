@@ -68,6 +68,8 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const uint16_t* x, int64
     }
 }
 
+// ONCE: x is not read again soon.
+template <bool ONCE>
 __global__ __launch_bounds__(kThreads) void unpack_kernel(const uint8_t* in, int64_t rows,
                                                           int64_t cols, uint32_t per_row,
                                                           uint16_t* x, int64_t ldx) {
@@ -94,7 +96,7 @@ __global__ __launch_bounds__(kThreads) void unpack_kernel(const uint8_t* in, int
         const int64_t c = (int64_t)at[k].unit * 8;
         float v[8];
         act8_unpack8(q[k], act8_scale(s[k]), v);
-        store8<true>(x + at[k].row * ldx + c, cols - c, v);
+        store8<ONCE>(x + at[k].row * ldx + c, cols - c, v);
     }
 }
 
@@ -145,12 +147,18 @@ extern "C" tide_status tide_act8_pack(const void* x, int64_t ldx, int64_t rows, 
                   static_cast<uint8_t*>(kept));
 }
 
+tide_status tide::act8_unpack_into(const void* kept, int64_t rows, int64_t cols, void* x,
+                                   int64_t ldx, bool once, tide_stream_t stream) {
+    if (rows == 0 || cols == 0) return TIDE_OK;
+    const int64_t per_row = act8_pitch(cols) / 8;
+    return launch(once ? unpack_kernel<true> : unpack_kernel<false>,
+                  (rows * per_row + kUnitsPerGroup - 1) / kUnitsPerGroup, kThreads, stream,
+                  static_cast<const uint8_t*>(kept), rows, cols, (uint32_t)per_row,
+                  static_cast<uint16_t*>(x), ldx);
+}
+
 extern "C" tide_status tide_act8_unpack(const void* kept, int64_t rows, int64_t cols, void* x,
                                         int64_t ldx, tide_stream_t stream) {
     const tide_status st = check_call(x, ldx, kept, rows, cols, stream);
-    if (st != TIDE_OK || rows == 0 || cols == 0) return st;
-    const int64_t per_row = act8_pitch(cols) / 8;
-    return launch(unpack_kernel, (rows * per_row + kUnitsPerGroup - 1) / kUnitsPerGroup, kThreads,
-                  stream, static_cast<const uint8_t*>(kept), rows, cols, (uint32_t)per_row,
-                  static_cast<uint16_t*>(x), ldx);
+    return st == TIDE_OK ? act8_unpack_into(kept, rows, cols, x, ldx, true, stream) : st;
 }

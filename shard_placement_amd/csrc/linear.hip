@@ -1199,7 +1199,7 @@ extern "C" tide_status tide_linear_backward(const tide_linear_backward_args* arg
     if (a.dweight && N) {
         w.A = {a.x_kept, act8_pitch(K), act8_pitch(K), T};
         if (b.w_shape.bi == 256) {
-            TIDE_TRY(tide_act8_unpack(a.x_kept, T, K, b.x, act8_pitch(K), stream));
+            TIDE_TRY(act8_unpack_into(a.x_kept, T, K, b.x, act8_pitch(K), false, stream));
             w.A.p = b.x;
         }
         w.B = dz.operand(true);

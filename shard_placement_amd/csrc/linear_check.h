@@ -87,4 +87,9 @@ tide_status launch(void (*kernel)(P...), int64_t grid, int threads, tide_stream_
     return launch_lds(kernel, grid, threads, 0, stream, a...);
 }
 
+// tide_act8_unpack without its checks; once: x is not read again soon, so it
+// needs no place in the caches.
+tide_status act8_unpack_into(const void* kept, int64_t rows, int64_t cols, void* x, int64_t ldx,
+                             bool once, tide_stream_t stream);
+
 }  // namespace tide
