@@ -522,8 +522,8 @@ tide_status tide_act8_unpack(const void *kept, int64_t rows, int64_t cols, void 
  * are multiples of 8 save a copy of the operand into the workspace).  Outputs may
  * overlap no input and no other output (TIDE_EOVERLAP), but y may be the
  * residual itself (same address and ldy = ldr).  T < 2^31; N, K and every
- * ld at most 2^22 (TIDE_EUNSUPPORTED).  T, N or K may be 0: an empty sum is 0,
- * and outputs without elements are not touched.
+ * ld at most 2^22; T N, T K and N K at most 2^33 (TIDE_EUNSUPPORTED).  T, N or
+ * K may be 0: an empty sum is 0, and outputs without elements are not touched.
  *
  * The workspace (16-byte aligned device memory of at least the bytes that
  * the _workspace call gives for the same arguments, TIDE_ENOSPACE otherwise;

@@ -400,145 +400,13 @@ __global__ __launch_bounds__(kGemvThreads, 4) void gemv_kernel(Gemv p) {
     finish(p.e, n0, threadIdx.x, threadIdx.x < p.e.J, v);
 }
 
-// ---- forward for few tokens, any alignment ------------------------------------------------
-
-// For operands that the tile kernels could only read as copies (rows that do
-// not start on 16 bytes): the weight is read once, straight from memory into
-// the matrix instructions' registers.  A wave takes 32 of W's rows, 128
-// contraction elements at a time, the next 128 in flight while these are
-// multiplied; the waves of a workgroup share the 32 rows and take the pieces
-// in turn, and their sums meet in LDS, in the waves' order, before the
-// epilogue.  (28672 x 8192 and 16 tokens: 115 us, the tile kernel on aligned
-// rows 80, so those go there.)
-struct Few {
-    const uint16_t* x;
-    int64_t ldx;
-    const uint16_t* w;
-    int64_t K;
-    Epilogue e;  // I = N, J = T
-};
-
-constexpr int kFewRows = 32;
-constexpr int kFewStep = 128;
-constexpr int kFewPitch = kFewRows + 4;  // floats of a token's sums in LDS
-
-__device__ __forceinline__ bf16x8 load_frag(const uint16_t* p) {
-    return __builtin_bit_cast(bf16x8, load8_raw(p));
-}
-// The first n of 8 elements, the others 0.
-__device__ __forceinline__ bf16x8 load_frag(const uint16_t* p, int64_t n) {
-    if (n >= 8) return load_frag(p);
-    s16x8 v;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        v[k] = k < n ? (short)*(const TIDE_GLOBAL_AS uint16_t*)(p + k) : (short)0;
-    return __builtin_bit_cast(bf16x8, v);
-}
-
-template <int TJ>
-__global__ __launch_bounds__(512) void few_kernel(Few p) {
-    extern __shared__ __attribute__((aligned(16))) float sums[];  // [waves][16 TJ][kFewPitch]
-    constexpr int kSteps = kFewStep / 32;
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = blockDim.x >> 6;
-    const int r = lane & 15, g = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * kFewRows;
-    // rows and tokens past the last one repeat it; their sums are not stored
-    const uint16_t* w[2];
-    const uint16_t* x[TJ];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) w[h] = p.w + min(n0 + 16 * h + r, p.e.I - 1) * p.K + g * 8;
-#pragma unroll
-    for (int y = 0; y < TJ; ++y) x[y] = p.x + min((int64_t)(16 * y + r), p.e.J - 1) * p.ldx + g * 8;
-
-    struct Piece {
-        bf16x8 w[2][kSteps], x[TJ][kSteps];
-    };
-    f32x4v acc[2][TJ];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int y = 0; y < TJ; ++y) acc[h][y] = 0;
-    auto load = [&](Piece& f, int64_t k) __attribute__((always_inline)) {
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) f.w[h][s] = load_frag(w[h] + k + 32 * s);
-#pragma unroll
-            for (int y = 0; y < TJ; ++y) f.x[y][s] = load_frag(x[y] + k + 32 * s);
-        }
-    };
-    auto multiply = [&](const Piece& f) __attribute__((always_inline)) {
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int y = 0; y < TJ; ++y)
-                    acc[h][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.w[h][s], f.x[y][s],
-                                                                        acc[h][y], 0, 0, 0);
-    };
-    const int64_t whole = p.K / kFewStep;
-    const int64_t stride = (int64_t)waves * kFewStep, end = whole * kFewStep;
-    int64_t k = (int64_t)wave * kFewStep;
-    Piece a, b;
-    if (k < end) load(a, k);
-    while (k < end) {
-        k += stride;
-        if (k < end) load(b, k);
-        multiply(a);
-        if (k >= end) break;
-        k += stride;
-        if (k < end) load(a, k);
-        multiply(b);
-    }
-    if (p.K > end && wave == whole % waves) {
-#pragma unroll 1
-        for (int64_t t = end; t < p.K; t += 32) {
-            const int64_t n = p.K - t - g * 8;
-            bf16x8 fw[2], fx[TJ];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) fw[h] = load_frag(w[h] + t, n);
-#pragma unroll
-            for (int y = 0; y < TJ; ++y) fx[y] = load_frag(x[y] + t, n);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int y = 0; y < TJ; ++y)
-                    acc[h][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[h], fx[y], acc[h][y], 0,
-                                                                        0, 0);
-        }
-    }
-    TIDE_LDS float* mine = (TIDE_LDS float*)sums + (wave * 16 * TJ + r) * kFewPitch + g * 4;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int y = 0; y < TJ; ++y)
-            *(TIDE_LDS f32x4v*)(mine + 16 * y * kFewPitch + 16 * h) = acc[h][y];
-    __syncthreads();
-    // 4 lanes of 8 columns for each token: the first TJ waves
-    if (wave >= TJ) return;
-    const int64_t j = threadIdx.x >> 2;
-    const int c = (threadIdx.x & 3) * 8;
-    float v[8] = {};
-    for (int u = 0; u < waves; ++u) {
-        const TIDE_LDS float* from = (TIDE_LDS float*)sums + (u * 16 * TJ + j) * kFewPitch + c;
-        const f32x4v lo = *(const TIDE_LDS f32x4v*)from, hi = *(const TIDE_LDS f32x4v*)(from + 4);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            v[q] += lo[q];
-            v[q + 4] += hi[q];
-        }
-    }
-    finish(p.e, n0 + c, j, j < p.e.J && n0 + c < p.e.I, v);
-}
-
 // ---- operand preparation -------------------------------------------------
 
 // Rows of `cols` elements copied to rows of `width` (a multiple of 8), the
 // rest 0: operands whose rows do not start on 16 bytes, or whose length is
-// not a multiple of 8.
+// not a multiple of 8.  (Reading such a weight straight into the matrix
+// instructions' registers, without the copy, took 58 us against 22 for 24
+// tokens and 1001 x 5121, 401 against 293 for 32 and 28672 x 8191.)
 constexpr int kPadThreads = 256;
 
 __global__ __launch_bounds__(kPadThreads) void pad_kernel(const uint16_t* in, int64_t ld,
@@ -890,6 +758,9 @@ tide_status check_dims(int64_t T, int64_t N, int64_t K, int32_t act, int32_t res
     if (T < 0 || N < 0 || K < 0 || act < TIDE_ACT_NONE || act > TIDE_ACT_SILU || reserved != 0)
         return TIDE_EINVAL;
     if (T > kMaxTokens || N > kMaxWidth || K > kMaxWidth) return TIDE_EUNSUPPORTED;
+    // every launch's grid, a lane for 8 elements at least, stays below kMaxGrid
+    if (T * N > kMaxElements || T * K > kMaxElements || N * K > kMaxElements)
+        return TIDE_EUNSUPPORTED;
     return TIDE_OK;
 }
 
@@ -929,14 +800,8 @@ tide_status check_workspace(void* ws, size_t have, int64_t need, const Extent* o
 // ---- forward -------------------------------------------------------------
 
 constexpr int64_t kGemvTokens = 4;
-constexpr int64_t kFewTokens = 32;
-
-// Waves of a workgroup of few_kernel: 8 where 4 would give the chip less than
-// 16 waves a compute unit.
-int few_waves(int64_t N) { return ceil_div(N, kFewRows) * 4 < 4096 ? 8 : 4; }
-
 struct ForwardPlan {
-    bool few;
+    bool gemv;
     Source x, w;
     Shape shape;
     float* partial;
@@ -972,9 +837,10 @@ ForwardPlan plan_forward(const tide_linear_forward_args& a, void* ws) {
     ForwardPlan f;
     Carver c{static_cast<char*>(ws)};
     const int64_t T = a.tokens, N = a.out_features, K = a.in_features;
-    f.few = T <= kFewTokens && !(direct(a.x, a.ldx, T, K) && direct(a.weight, K, N, K));
+    // any alignment, but whole checkpoint blocks need the tiles' epilogue
+    f.gemv = T <= kGemvTokens && K >= 8 && !a.z_kept;
     f.bytes = 0;
-    if (f.few) return f;
+    if (f.gemv) return f;
     f.x = {a.x, a.ldx, T, K};
     f.w = {a.weight, K, N, K};
     f.x.plan(c);
@@ -1018,19 +884,11 @@ extern "C" tide_status tide_linear_forward(const tide_linear_forward_args* args,
     e.ldr = a.ldr;
     e.kept = static_cast<uint8_t*>(a.z_kept);
     e.act = a.act;
-    if (T <= kGemvTokens && K >= 8 && !a.z_kept) {
+    if (f.gemv) {
         const Gemv gemv = {static_cast<const uint16_t*>(a.x), T > 1 ? a.ldx : K,
                            static_cast<const uint16_t*>(a.weight), K, e};
         return launch(T == 1 ? gemv_kernel<1> : T == 2 ? gemv_kernel<2> : gemv_kernel<4>,
                       ceil_div(N, kGemvRows), kGemvThreads, stream, gemv);
-    }
-    if (f.few) {
-        const Few few = {static_cast<const uint16_t*>(a.x), T > 1 ? a.ldx : K,
-                         static_cast<const uint16_t*>(a.weight), K, e};
-        const int waves = few_waves(N), tj = T <= 16 ? 1 : 2;
-        return launch_lds(tj == 1 ? few_kernel<1> : few_kernel<2>, ceil_div(N, kFewRows),
-                          64 * waves, (unsigned)(waves * 16 * tj * kFewPitch * sizeof(float)),
-                          stream, few);
     }
     TIDE_TRY(f.x.fill(stream));
     TIDE_TRY(f.w.fill(stream));

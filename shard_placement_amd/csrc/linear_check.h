@@ -11,10 +11,11 @@ namespace tide {
 
 // Limits of the kernels' 32-bit arithmetic: a workgroup addresses at most 256
 // rows from a 64-bit base, so 256 rows of bf16 have to stay within 2^31
-// bytes; tokens are counted in 31 bits; a grid's threads in 32.
+// bytes; tokens are counted in 31 bits, a grid's threads in 32.
 constexpr int64_t kMaxTokens = INT32_MAX;
 constexpr int64_t kMaxWidth = (int64_t)1 << 22;
 constexpr int64_t kMaxGrid = ((int64_t)1 << 23) - 1;
+constexpr int64_t kMaxElements = (int64_t)1 << 33;  // of a product's matrices
 
 // The bytes of a matrix: rows of `width` bytes, `pitch` apart.
 struct Extent {

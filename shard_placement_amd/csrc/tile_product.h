@@ -69,9 +69,8 @@ constexpr uint32_t kNowhere = 0xf0000000u;  // an offset past every descriptor's
 
 // The swizzles: a "rows" tile's chunk c of row r lies at c ^ row_swizzle(r), a
 // "columns" tile's 32-byte pair p of row k at p ^ column_swizzle(k).
-template <int K>
 __device__ __forceinline__ constexpr int row_swizzle(int r) {
-    return r & (K == 128 ? 15 : 7);
+    return r & 7;
 }
 template <int N>
 __device__ __forceinline__ constexpr int column_swizzle(int k) {
@@ -92,7 +91,7 @@ struct Stager {
 
     // a lane's chunk is the same in all its loads: they are a multiple of the
     // swizzle's period of rows apart
-    static_assert(COLUMNS || kMine == 1 || WAVES * 64 / kRowChunks % (K == 128 ? 16 : 8) == 0, "");
+    static_assert(COLUMNS || kMine == 1 || WAVES * 64 / kRowChunks % 8 == 0, "");
 
     const char* base;
     int64_t step;        // bytes from one k tile to the next
@@ -122,7 +121,7 @@ struct Stager {
             if constexpr (COLUMNS) {
                 c = at ^ (column_swizzle<N>(row) << 1);
             } else {
-                c = at ^ row_swizzle<K>(row);
+                c = at ^ row_swizzle(row);
                 chunk_k = c * 8;
             }
             offset[q] = (uint32_t)((int64_t)row * o.ld * 2 + c * 16);
@@ -245,7 +244,7 @@ struct Reader {
             return __builtin_bit_cast(bf16x8, v);
         } else {
             const int row = m0 + (lane & 15);
-            const int c = (4 * S + (lane >> 4)) ^ row_swizzle<K>(lane & 15);
+            const int c = (4 * S + (lane >> 4)) ^ row_swizzle(lane & 15);
             return *(const TIDE_LDS bf16x8*)(lds + row * (2 * K) + c * 16);
         }
     }
@@ -334,6 +333,11 @@ __device__ __forceinline__ void deep_step(TIDE_LDS char* __restrict__ next,
     __builtin_amdgcn_sched_barrier(0);
 }
 
+template <int S>
+struct Part {
+    static constexpr int value = S;
+};
+
 // One k tile, plainly: the next tile's loads, this tile's reads and matrix
 // instructions half by half.  For the smaller tiles, of which a compute unit
 // holds several: other workgroups fill the gaps, and fewer registers let more
@@ -349,21 +353,20 @@ __device__ __forceinline__ void plain_step(TIDE_LDS char* __restrict__ next,
         sb.stage(next + SA::kBytes, valid);
     }
     bf16x8 a[TI], b[TJ];
-    auto part = [&]<int S>() __attribute__((always_inline)) {
-        read_part<BI, BJ, K, TI, TJ, CA, CB, S>(now, now + SA::kBytes, wi, wj, lane, a, b);
+    auto part = [&](auto s) __attribute__((always_inline)) {
+        read_part<BI, BJ, K, TI, TJ, CA, CB, decltype(s)::value>(now, now + SA::kBytes, wi, wj, lane,
+                                                                a, b);
         multiply_part<TI, TJ>(a, b, acc);
     };
-    part.template operator()<0>();
-    part.template operator()<1>();
-    if constexpr (K >= 128) {
-        part.template operator()<2>();
-        part.template operator()<3>();
-    }
-    if constexpr (K >= 256) {
-        part.template operator()<4>();
-        part.template operator()<5>();
-        part.template operator()<6>();
-        part.template operator()<7>();
+    part(Part<0>());
+    part(Part<1>());
+    if constexpr (K == 256) {
+        part(Part<2>());
+        part(Part<3>());
+        part(Part<4>());
+        part(Part<5>());
+        part(Part<6>());
+        part(Part<7>());
     }
 }
 

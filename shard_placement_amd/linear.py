@@ -67,6 +67,8 @@ class Act8:
 
     def unpack(self, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """The bf16 matrix that the checkpoint stands for (allocated when not given)."""
+        if self._gpu < 0:
+            raise TideError(-6, "the checkpoint is on %s, expected a GPU" % self.buffer.device)
         if out is None:
             return api._on_device(self._gpu, stream, self._unpack_new)
         px, ldx = self._matrix(out, "out")

@@ -91,6 +91,12 @@ def test_forward_refusals():
     for bad in (dict(tokens=1 << 31), dict(out_features=(1 << 22) + 1, ldy=1 << 23),
                 dict(in_features=(1 << 22) + 1, ldx=1 << 23), dict(ldx=(1 << 22) + 1)):
         assert call(fwd(**bad)) == EUNSUPPORTED, bad
+    # grids that a later launch could not have are refused before the first
+    for T, N, K in ((1 << 30, 64, 96), (2049, 1 << 22, 96), (40, 1 << 22, 2049)):
+        a = fwd(tokens=T, out_features=N, in_features=K, ldx=1 << 22, ldy=1 << 22)
+        assert call(a) == EUNSUPPORTED, (T, N, K)
+        b = bwd(tokens=T, out_features=N, in_features=K, lddy=1 << 22, lddx=1 << 22)
+        assert L.tide_linear_backward(ctypes.byref(b), None, 0, None) == EUNSUPPORTED
     for bad in (dict(x=AT + 1), dict(weight=2 * AT + 1), dict(y=3 * AT + 1), dict(bias=5 * AT + 1),
                 dict(residual=6 * AT + 1), dict(z_kept=7 * AT + 8)):
         assert call(fwd(**bad)) == EALIGN, bad
@@ -171,6 +177,12 @@ def test_python_refusals():
     assert kept.data.shape == (4, 64) and kept.scales.shape == (4, 2)
     with pytest.raises(_lib.TideError, match="expected .4, 33."):
         kept.pack(x)
+    with pytest.raises(_lib.TideError, match="expected a GPU"):
+        kept.unpack()
+    with pytest.raises(_lib.TideError, match="expected a GPU"):
+        kept.unpack(torch.zeros(4, 33, dtype=torch.bfloat16))
+    with pytest.raises(TypeError):
+        linear.Linear(None)
 
 
 def test_reference_rounds_like_torch():
