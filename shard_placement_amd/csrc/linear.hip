@@ -273,7 +273,8 @@ __global__ __launch_bounds__(WI* WJ * 64, BI == 256 ? 2 : 1) void product_kernel
 }
 
 // dx and dW in one launch, for shapes too small to fill the chip one after the
-// other: the first `n_w` workgroups take dW's tiles, the others dx's.
+// other (77 x 768 x 2048: 13.2 us for both, 7.6, 3.0 and 8.0 for dx, its join
+// and dW): the first `n_w` workgroups take dW's tiles, the others dx's.
 template <int BJ, int WI, int WJ>
 __global__ __launch_bounds__(256) void pair_kernel(Product w, Product x, int32_t n_w) {
     __shared__ __attribute__((aligned(1024))) char lds[kProductLds<128, 128, 64>];
@@ -285,7 +286,8 @@ __global__ __launch_bounds__(256) void pair_kernel(Product w, Product x, int32_t
 }
 
 // The sums of a split contraction added up in the splits' order, then the
-// epilogue.
+// epilogue.  Bound by the partial sums' bytes and a launch: 3 splits of 2048 x
+// 5120 sums (126 MB) 23 us, 12 of 24 x 5120 (6 MB) 4.2.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinAhead = 8;  // splits whose loads are in flight together
 
@@ -327,7 +329,9 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(Product p) {
 // row 5.3, in runs of 4 KB 6.6 (nontemporal; plain loads 0.5 less).  So a
 // workgroup takes 8 rows, its 4 waves side by side 4 KB of each at a time; a
 // lane multiplies its 8 elements of every row by its 8 elements of each
-// token in binary32 and the lanes' sums are added at the end.
+// token in binary32 and the lanes' sums are added at the end.  28672 x 8192:
+// 72 us for one token (6.5 TB/s), 74 for two, 85 for four.  Rows may start
+// anywhere.
 struct Gemv {
     const uint16_t* x;
     int64_t ldx;
