@@ -642,7 +642,8 @@ Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth) {
         s.bi = 128;
         s.bj = J <= 16 ? 16 : J <= 32 ? 32 : 64;
         if (kind == kForward && s.bj <= 32 && I * depth > ((int64_t)128 << 20)) s.bk = 256;
-        const int64_t want = s.bk == 256 ? kCus : 2 * kCus;
+        // a contraction of up to 1024 is over before a join would be
+        const int64_t want = depth <= 1024 ? 1 : s.bk == 256 ? kCus : 2 * kCus;
         set_split(&s, I, J, depth, want / std::max<int64_t>(1, ceil_div(I, s.bi)));
         return s;
     }
