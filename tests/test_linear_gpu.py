@@ -343,6 +343,33 @@ def test_gradients_against_differences(act):
     within(layer.weight_grad, dw, ref.BF16 * (dw.abs() + 1.01 * (want.abs().T @ x.abs())) + 1e-5, "dw")
 
 
+# ---- every tile, whole and split ---------------------------------------------------------------
+
+# Shapes that between them take each form of the three products: 256 x 256, 256 x
+# 192, 256 x 128 and 128 x 128 tiles and the narrow ones, each with a whole and a
+# split contraction, and dx and dW in one launch with each tile of dx.
+TILES = [(2500, 1550, 260), (1300, 1000, 4001), (5001, 1551, 24), (130, 8201, 2508), (8200, 1303, 25),
+         (2500, 1032, 5000), (24, 1032, 5001), (1550, 260, 2500), (1300, 4000, 1000), (1550, 24, 5000),
+         (8208, 2501, 130), (8200, 24, 1301), (2501, 5001, 1032), (260, 777, 5000), (4000, 1301, 1001),
+         (24, 5003, 1551), (2500, 130, 8200), (24, 8203, 1303), (5000, 2500, 1032), (12, 1040, 200),
+         (24, 1035, 24), (40, 1032, 25), (70, 1032, 25), (513, 518, 27), (40, 2051, 2508), (10, 24, 2000),
+         (25, 24, 1040), (40, 24, 1040), (1032, 40, 24), (1035, 24, 24), (1030, 12, 40), (4, 40, 5000)]
+
+
+@pytest.mark.parametrize("T,N,K", TILES)
+def test_every_tile(T, N, K):
+    test_forward(T, N, K, "silu", True, True, True)
+    test_backward(T, N, K, "gelu_tanh", True)
+    test_backward(T, N, K, "none", False)
+
+
+@pytest.mark.parametrize("T", [5, 12, 16, 30])
+def test_forward_of_a_weight_past_the_cache(T):
+    """Few tokens through a weight of more than 256 MB: deep tiles, split and,
+    with an odd number of rows and a ragged contraction, to its last element."""
+    test_forward(T, 16403, 8216, "gelu", True, True, T != 12)
+
+
 # ---- streams, graphs, repeats, memory ----------------------------------------------------------
 
 def step(layer, x, r, dy, x8, z8):
@@ -391,6 +418,37 @@ def test_streams_side_by_side():
     torch.cuda.synchronize()
     got = [bits(y1, dx1, one[0].weight_grad, one[0].bias_grad),
            bits(y2, dx2, two[0].weight_grad, two[0].bias_grad)]
+    for a, b in zip(want, got):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_two_host_threads():
+    """Two threads' steps, each on its own stream with its own layer."""
+    import threading
+
+    ms = [make(11, 300, 520, 333), make(12, 40, 1032, 200, act="silu")]
+    want = [bits(*step(*m), m[0].weight_grad, m[0].bias_grad, m[4].buffer) for m in ms]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def work(k):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    out = step(*ms[k])
+                s.synchronize()
+                got[k] = bits(*out, ms[k][0].weight_grad, ms[k][0].bias_grad, ms[k][4].buffer)
+                s.synchronize()
+        except Exception as e:  # shown by the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not errors and not any(t.is_alive() for t in threads)
     for a, b in zip(want, got):
         assert all(torch.equal(p, q) for p, q in zip(a, b))
 
