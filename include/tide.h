@@ -515,14 +515,15 @@ tide_status tide_act8_unpack(const void *kept, int64_t rows, int64_t cols, void 
  *           dy itself.
  *
  * A z that is not finite was kept as NaN and makes its gradients NaN.  The
- * gradient of relu at 0 is 0.
+ * gradient of relu at 0 is 0.  relu of minus infinity is 0; gelu, gelu_tanh
+ * and silu of it are NaN (minus infinity times 0).
  *
  * Rows of x, residual, y, dy and dx lie ld* elements apart (>= the row's
  * length; any 2-byte alignment; rows that start on 16 bytes with widths that
  * are multiples of 8 save a copy of the operand into the workspace).  Outputs may
  * overlap no input and no other output (TIDE_EOVERLAP), but y may be the
- * residual itself (same address and ldy = ldr).  T < 2^31; N, K and every
- * ld at most 2^22; T N, T K and N K at most 2^33 (TIDE_EUNSUPPORTED).  T, N or
+ * residual itself (same address and ldy = ldr).  T at most 2^30; N, K and
+ * every ld at most 2^22; T N, T K and N K at most 2^33 (TIDE_EUNSUPPORTED).  T, N or
  * K may be 0: an empty sum is 0, and outputs without elements are not touched.
  *
  * The workspace (16-byte aligned device memory of at least the bytes that

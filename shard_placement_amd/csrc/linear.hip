@@ -60,7 +60,7 @@ __device__ __forceinline__ float normal_cdf(float z, float* bell) {
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
-    if constexpr (ACT == TIDE_ACT_RELU) return z > 0.0f ? z : 0.0f * z;
+    if constexpr (ACT == TIDE_ACT_RELU) return z < 0.0f ? 0.0f : z;  // NaN stays NaN
     if constexpr (ACT == TIDE_ACT_GELU) {
         float bell;
         return z * normal_cdf(z, &bell);

@@ -249,6 +249,22 @@ def test_rows_of_nan_stay_alone():
     assert torch.equal(~dw.isfinite(), bad)
 
 
+@pytest.mark.parametrize("T,N,K", [(1, 40, 64), (3, 70, 65), (24, 40, 2048), (150, 300, 200)])
+def test_act_of_infinities(T, N, K):
+    """relu of minus infinity is 0, so what masks a column out adds nothing; plus
+    infinity stays, and the other activations of minus infinity are NaN."""
+    g = gen(T + N)
+    x, w, r = normal(g, T, K), normal(g, N, K), normal(g, T, N)
+    b = torch.zeros(N, dtype=BF, device=DEV)
+    b[3], b[N - 1], b[7], b[9] = -math.inf, -math.inf, math.inf, math.nan
+    for act in ("relu", "gelu", "gelu_tanh", "silu"):
+        y = Linear(w, bias=b, act=act).forward(x, residual=r)
+        for c in (3, N - 1):
+            assert torch.equal(y[:, c], r[:, c]) if act == "relu" else y[:, c].isnan().all()
+        assert (y[:, 7] == math.inf).all() and y[:, 9].isnan().all()
+        assert y[:, [0, 1, 2, 4, 5, 6, 8]].isfinite().all()
+
+
 # ---- the gradients -----------------------------------------------------------------------------
 
 @pytest.mark.parametrize("T,N,K", PRODUCTS)
