@@ -487,7 +487,8 @@ tide_status tide_rs_two_phase_noalloc(const void *h_plan, const void *d_plan,
  *
  * tide_act8_bytes: the checkpoint's size.  x: bf16, element (t, c) at
  * t * ldx + c, 2-byte aligned, ldx >= cols.  x and the checkpoint may not
- * overlap.  rows < 2^31, cols and ldx <= 2^22 (TIDE_EUNSUPPORTED).
+ * overlap.  rows < 2^31, cols and ldx <= 2^22, rows * pitch at most 2^36
+ * (TIDE_EUNSUPPORTED).
  * Asynchronous on `stream`, which belongs to the current device
  * (TIDE_EINVAL otherwise); allocates nothing. */
 tide_status tide_act8_bytes(int64_t rows, int64_t cols, size_t *bytes);

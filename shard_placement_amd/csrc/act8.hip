@@ -101,10 +101,12 @@ __global__ __launch_bounds__(kThreads) void unpack_kernel(const uint8_t* in, int
 }
 
 // Rows and columns of a checkpoint that the kernels can address: a row's
-// units and a workgroup's units together stay below 2^31.
+// units and a workgroup's units together stay below 2^31, a grid's threads
+// below 2^32.
 tide_status check_shape(int64_t rows, int64_t cols) {
     if (rows < 0 || cols < 0) return TIDE_EINVAL;
-    if (rows > kMaxTokens || cols > kMaxWidth) return TIDE_EUNSUPPORTED;
+    if (rows > kMaxRows || cols > kMaxWidth) return TIDE_EUNSUPPORTED;
+    if (rows * act8_pitch(cols) > kMaxKept) return TIDE_EUNSUPPORTED;
     return TIDE_OK;
 }
 

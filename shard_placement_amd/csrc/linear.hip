@@ -287,7 +287,7 @@ __global__ __launch_bounds__(256) void pair_kernel(Product w, Product x, int32_t
 
 // The sums of a split contraction added up in the splits' order, then the
 // epilogue.  Bound by the partial sums' bytes and a launch: 3 splits of 2048 x
-// 5120 sums (126 MB) 23 us, 12 of 24 x 5120 (6 MB) 4.2.
+// 5120 sums (126 MB) 23 us, 10 of 24 x 5120 (5 MB) 4.2.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinAhead = 8;  // splits whose loads are in flight together
 
@@ -763,7 +763,6 @@ tide_status check_dims(int64_t T, int64_t N, int64_t K, int32_t act, int32_t res
     if (T < 0 || N < 0 || K < 0 || act < TIDE_ACT_NONE || act > TIDE_ACT_SILU || reserved != 0)
         return TIDE_EINVAL;
     if (T > kMaxTokens || N > kMaxWidth || K > kMaxWidth) return TIDE_EUNSUPPORTED;
-    // every launch's grid, a lane for 8 elements at least, stays below kMaxGrid
     if (T * N > kMaxElements || T * K > kMaxElements || N * K > kMaxElements)
         return TIDE_EUNSUPPORTED;
     return TIDE_OK;

@@ -11,10 +11,14 @@ namespace tide {
 
 // Limits of the kernels' 32-bit arithmetic: a workgroup addresses at most 256
 // rows from a 64-bit base, so 256 rows of bf16 have to stay within 2^31
-// bytes; tokens are counted in 31 bits, a grid's threads in 32.
-constexpr int64_t kMaxTokens = INT32_MAX;
+// bytes; rows are counted in 31 bits, a grid's threads in 32.  Within these
+// limits no launch of a call is refused for its grid, so that none is refused
+// after the ones before it have run.
 constexpr int64_t kMaxWidth = (int64_t)1 << 22;
-constexpr int64_t kMaxGrid = ((int64_t)1 << 23) - 1;
+constexpr int64_t kMaxThreads = UINT32_MAX;         // of a grid
+constexpr int64_t kMaxRows = INT32_MAX;             // of a checkpoint
+constexpr int64_t kMaxKept = (int64_t)1 << 36;      // its values (a lane packs 32 of them)
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;    // of a product (128 a workgroup of 256)
 constexpr int64_t kMaxElements = (int64_t)1 << 33;  // of a product's matrices
 
 // The bytes of a matrix: rows of `width` bytes, `pitch` apart.
@@ -73,7 +77,7 @@ template <typename... P, typename... A>
 tide_status launch_lds(void (*kernel)(P...), int64_t grid, int threads, unsigned lds_bytes,
                        tide_stream_t stream, A... a) {
     if (grid <= 0) return TIDE_OK;
-    if (grid > kMaxGrid) return TIDE_EUNSUPPORTED;
+    if (grid > kMaxThreads / threads) return TIDE_EUNSUPPORTED;
     void* args[] = {&a...};
     static_assert(sizeof...(P) == sizeof...(A), "one argument for each parameter");
     static_assert((__is_same(P, A) && ...), "arguments of the parameters' own types");

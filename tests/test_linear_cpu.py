@@ -219,3 +219,20 @@ def test_reference_slopes_against_differences(act):
     h = 1e-6
     want = (ref.act_ref(z + h, act) - ref.act_ref(z - h, act)) / (2 * h)
     assert (ref.slope_ref(z, act) - want).abs().max() < 1e-8
+
+
+def test_limits_of_long_narrow_matrices():
+    """At the documented limits the workspace can be asked for; past them every
+    call is refused before its first launch."""
+    L = _lib.lib()
+    n = ctypes.c_size_t(0)
+    assert api.tide_act8_bytes(1 << 14, 1 << 22) == (1 << 36) // 32 * 33
+    assert L.tide_act8_bytes((1 << 14) + 1, 1 << 22, ctypes.byref(n)) == EUNSUPPORTED
+    assert L.tide_act8_pack(AT, 1 << 22, (1 << 14) + 1, 1 << 22, 1 << 50, None) == EUNSUPPORTED
+    far = dict(out_features=1, in_features=1, weight=1 << 50)
+    for T, want in ((1 << 30, 0), ((1 << 30) + 1, EUNSUPPORTED)):
+        a = fwd(tokens=T, x=1 << 51, ldx=1, y=1 << 52, ldy=1, **far)
+        b = bwd(tokens=T, dy=1 << 51, lddy=1, dx=1 << 52, lddx=1, x_kept=1 << 53, z_kept=1 << 54,
+                dweight=1 << 55, dbias=1 << 56, **far)
+        assert query("tide_linear_forward_workspace", a)[0] == want
+        assert query("tide_linear_backward_workspace", b)[0] == want

@@ -600,3 +600,26 @@ def test_offsets_past_32_bits():
     assert (dx[70000:70010] == 0).all()
     out = k.unpack(x)
     assert torch.equal(out[rows].double(), ref.unpack_ref(codes, scales, K))
+
+
+@pytest.mark.big
+def test_most_tokens():
+    """2^30 tokens of one feature, the most there may be: every product is
+    exact (a weight of 2, one non-zero dy), so every element is compared."""
+    T = 1 << 30
+    x = torch.randint(-64, 65, (T, 1), generator=gen(3), device=DEV, dtype=torch.int8).to(BF)
+    w = torch.full((1, 1), 2.0, dtype=BF, device=DEV)
+    assert torch.equal(Linear(w).forward(x), x + x)
+    last = x[T - 1].item()
+    k = Act8(T, 1, device=DEV).pack(x)
+    assert torch.equal(k.unpack(), x.clamp(-64, 64).to(torch.float8_e4m3fn).to(BF))
+    kept = k.unpack()[T - 1].item()
+    assert abs(kept - last) <= abs(last) / 16
+    x.zero_()
+    x[T - 1] = 3.0
+    b = torch.zeros(1, dtype=BF, device=DEV)
+    layer = Linear(w, bias=b, weight_grad=torch.empty_like(w), bias_grad=torch.empty_like(b))
+    dx = layer.backward(x, x=k)
+    assert torch.equal(dx, x + x)
+    assert layer.bias_grad.item() == 3.0
+    assert layer.weight_grad.item() == torch.tensor(3 * kept).to(BF).item()
