@@ -191,19 +191,21 @@ struct Product {
 constexpr int kXcdCount = 8;
 constexpr int kBand = 4;
 
-__device__ __forceinline__ void tile_at(const Product& p, int64_t b, int64_t total, int64_t* ti,
-                                        int64_t* tj, int64_t* sp) {
-    const int64_t each = total / kXcdCount, extra = total % kXcdCount;
-    const int64_t x = b % kXcdCount, n = b / kXcdCount;
-    b = x * each + (x < extra ? x : extra) + n;
-    const int64_t tiles = (int64_t)p.tiles_i * p.tiles_j;
-    *sp = b / tiles;
-    b -= *sp * tiles;
-    const int64_t band = b / ((int64_t)kBand * p.tiles_i);
-    const int64_t width = min((int64_t)kBand, p.tiles_j - band * kBand);
+__device__ __forceinline__ void tile_at(const Product& p, uint32_t b, uint32_t total, int* ti,
+                                        int* tj, int* sp) {
+    const uint32_t each = total / kXcdCount, extra = total % kXcdCount;
+    const uint32_t x = b % kXcdCount, n = b / kXcdCount;
+    b = x * each + min(x, extra) + n;
+    const uint32_t tiles = (uint32_t)p.tiles_i * (uint32_t)p.tiles_j;
+    const uint32_t s = b / tiles;
+    b -= s * tiles;
+    const uint32_t band = b / (uint32_t)(kBand * p.tiles_i);
+    const uint32_t width = min((uint32_t)kBand, p.tiles_j - band * kBand);
     b -= band * kBand * p.tiles_i;
-    *ti = b / width;
-    *tj = band * kBand + b % width;
+    // the same in all lanes: scalar registers, of which the tile loop needs fewer
+    *sp = __builtin_amdgcn_readfirstlane(s);
+    *ti = __builtin_amdgcn_readfirstlane(b / width);
+    *tj = __builtin_amdgcn_readfirstlane(band * kBand + b % width);
 }
 
 // A wave's LDS writes have arrived before its reads, and its reads have
@@ -216,13 +218,13 @@ constexpr int kProductLds = 2 * (BI + BJ) * K * 2;
 
 // The tile of workgroup `block` of `blocks`.
 template <int BI, int BJ, int K, int WI, int WJ, Layout CA, Layout CB>
-__device__ __forceinline__ void product_tile(const Product& p, int64_t block, int64_t blocks,
+__device__ __forceinline__ void product_tile(const Product& p, uint32_t block, uint32_t blocks,
                                              TIDE_LDS char* lds) {
     constexpr int TI = BI / WI / 16, TJ = BJ / WJ / 16;
     static_assert(TI % 2 == 0, "a wave holds whole checkpoint blocks");
-    int64_t ti, tj, sp;
+    int ti, tj, sp;
     tile_at(p, block, blocks, &ti, &tj, &sp);
-    const int64_t i0 = ti * BI, j0 = tj * BJ;
+    const int64_t i0 = (int64_t)ti * BI, j0 = (int64_t)tj * BJ;
     const int64_t k0 = sp * p.split_depth;
     const int64_t k1 = min(p.depth, k0 + p.split_depth);
     f32x4v acc[TI][TJ];
@@ -235,8 +237,11 @@ __device__ __forceinline__ void product_tile(const Product& p, int64_t block, in
     constexpr int kRow = TI * 16, kPitch = kRow + 4, kLanes = kRow / 8;
     static_assert(WI * WJ * 16 * kPitch * 4 <= kProductLds<BI, BJ, K>, "the staging fits");
     tile_barrier(lds, lds);
-    const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
+    // (what follows from the thread is worked out here, not kept in registers
+    // through the loop)
+    int thread = threadIdx.x;
+    asm volatile("" : "+v"(thread));
+    const int lane = thread & 63, wave = thread >> 6;
     TIDE_LDS float* mine = (TIDE_LDS float*)lds + wave * 16 * kPitch;
     const int64_t iw = i0 + (wave / WJ) * kRow + (lane % kLanes) * 8;
     const int64_t jw = j0 + (wave % WJ) * TJ * 16 + lane / kLanes;
@@ -283,6 +288,26 @@ __global__ __launch_bounds__(256) void pair_kernel(Product w, Product x, int32_t
     else
         product_tile<128, BJ, 64, WI, WJ, kColumns, kRows>(x, blockIdx.x - n_w, gridDim.x - n_w,
                                                            (TIDE_LDS char*)lds);
+}
+
+// The same with 256-wide tiles, one workgroup a compute unit, the product of the
+// longer tiles first: where its tiles do not fill whole rounds of the chip the
+// other's fill the gaps (2048 x 13824 x 5120: 160 tiles of dx of 342 us and 1080 of
+// dW of 57 on 256 compute units, 445 us for both, 570 one after the other).
+template <int BJW, int BJX>
+__global__ __launch_bounds__(512, 2) void wide_pair_kernel(Product w, Product x, int32_t first_w,
+                                                           int32_t first_x) {
+    constexpr int kBj = BJW > BJX ? BJW : BJX;
+    __shared__ __attribute__((aligned(1024))) char lds[kProductLds<256, kBj, 64>];
+    const int block = blockIdx.x, blocks = gridDim.x;
+    // one of the two starts at 0, the other where that one ends
+    const bool of_x = first_x ? block >= first_x : block < first_w;
+    if (of_x)
+        product_tile<256, BJX, 64, 2, 4, kColumns, kRows>(
+            x, block - first_x, first_x ? blocks - first_x : first_w, (TIDE_LDS char*)lds);
+    else
+        product_tile<256, BJW, 64, 2, 4, kColumns, kColumns>(
+            w, block - first_w, first_w ? blocks - first_w : first_x, (TIDE_LDS char*)lds);
 }
 
 // The sums of a split contraction added up in the splits' order, then the
@@ -605,6 +630,11 @@ constexpr TileCost kTiles[] = {{256, 256, 1.25, 0.30, 7.0},
 constexpr double kPairStep = 0.95;
 constexpr int kCus = 256;
 
+// A tile of 256 rows, with `used` of the compute units at work.
+double wide_tile_us(const TileCost& c, const Shape& s, double used) {
+    return (double)(s.split_depth / 64) * (c.step + c.power * used * used) + c.rest;
+}
+
 double product_us(const TileCost& c, const Shape& s, int64_t I, int64_t J) {
     const int64_t groups = (int64_t)s.tiles_i * s.tiles_j * s.splits;
     const double rounds = (double)ceil_div(groups, kCus);
@@ -614,8 +644,7 @@ double product_us(const TileCost& c, const Shape& s, int64_t I, int64_t J) {
         const double pairs = (double)(int64_t)(rounds / 2), single = rounds - 2 * pairs;
         us = pairs * (steps * kPairStep + c.rest) + single * (steps * c.step + c.rest);
     } else {
-        const double used = (double)groups / (rounds * kCus);
-        us = rounds * (steps * (c.step + c.power * used * used) + c.rest);
+        us = rounds * wide_tile_us(c, s, (double)groups / (rounds * kCus));
     }
     // partial sums: a compute unit writes 40 KB/us, the join is a launch of its
     // own and reads 5.5 MB/us
@@ -635,7 +664,7 @@ double product_us(const TileCost& c, const Shape& s, int64_t I, int64_t J) {
 // Otherwise the tile and split of the least estimated time.  2048 x 5120
 // outputs of depth 13824: 264 us with the 256 x 192 tiles this takes, 290 with
 // 256 x 256, 313 with 128 x 128.
-Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth) {
+Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth, double* estimate = nullptr) {
     Shape s = {};
     s.bk = 64;
     if (J <= 64) {
@@ -663,7 +692,49 @@ Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth) {
             if ((int64_t)t.tiles_i * t.tiles_j >= 4 * kCus) break;  // enough without
         }
     }
+    if (estimate) *estimate = best;
     return s;
+}
+
+// dx [T, K] and dW [N, K] in one launch of 256-wide tiles, the longer ones
+// first: the pair of tiles of the least estimated time, or none if that is not
+// 3% less than `best`, that of the two products one after the other.
+// (Measured, both gradients with dz, against two launches: 2048 x 13824 x 5120
+// 496 us, 600; 8192 x 8192 x 1024 272, 331; 3000 x 1280 x 8192 129, 141; and 748
+// against 729 for 700 x 28672 x 8192, whose estimates were 0.7% apart.)
+bool choose_pair(int64_t T, int64_t N, int64_t K, double best, Shape* in, Shape* weight) {
+    constexpr int kWide = 2;  // 256 x 256 and 256 x 192
+    bool found = false;
+    best *= 0.97;
+    for (int a = 0; a < kWide; ++a) {
+        for (int b = 0; b < kWide; ++b) {
+            const TileCost &cx = kTiles[a], &cw = kTiles[b];
+            Shape x = {cx.bi, cx.bj, 64}, w = {cw.bi, cw.bj, 64};
+            set_split(&x, K, T, N, 1);
+            set_split(&w, K, N, T, 1);
+            const int64_t nx = (int64_t)x.tiles_i * x.tiles_j, nw = (int64_t)w.tiles_i * w.tiles_j;
+            const double tx = wide_tile_us(cx, x, 1.0), tw = wide_tile_us(cw, w, 1.0);
+            const double longer = std::max(tx, tw), shorter = std::min(tx, tw);
+            const int64_t n_long = tx >= tw ? nx : nw;
+            int64_t n_short = nx + nw - n_long;
+            // whole rounds of the longer; then the shorter beside the rest of
+            // them, and on the whole chip behind them
+            double us = (double)(n_long / kCus) * longer;
+            const int64_t rest = n_long % kCus;
+            if (rest) {
+                us += longer;
+                n_short -= (kCus - rest) * (int64_t)(longer / shorter);
+            }
+            if (n_short > 0) us += (double)ceil_div(n_short, kCus) * shorter;
+            if (us < best) {
+                best = us;
+                *in = x;
+                *weight = w;
+                found = true;
+            }
+        }
+    }
+    return found;
 }
 
 int64_t partial_floats(const Shape& s, int64_t I, int64_t J) {
@@ -975,17 +1046,20 @@ BackwardPlan plan_backward(const tide_linear_backward_args& a, void* ws) {
     if (a.dbias && b.chunks != 1) b.sums = c.take<float>(b.chunks * N);
     b.w = {a.weight, K, a.dx && T ? N : 0, K};
     b.w.plan(c);
-    b.w_shape = choose(kGradWeight, K, N, T);
-    // the 256-wide tiles read x from here, widened (tile_product.h)
-    if (a.dweight && N && b.w_shape.bi == 256) b.x = c.take<uint16_t>(T * act8_pitch(K));
-    b.in_shape = choose(kGradInput, K, T, b.width);
+    double in_us = 0.0, w_us = 0.0;
+    b.w_shape = choose(kGradWeight, K, N, T, &w_us);
+    b.in_shape = choose(kGradInput, K, T, b.width, &in_us);
+    const bool both = a.dx && a.dweight && T && N && K;
     // Both in one launch where together they are at most two workgroups a
     // compute unit; then a short contraction is cheaper whole than split and
     // joined (a join is 5 us, a step of 64 0.6)
-    b.pair = a.dx && a.dweight && T && N && K && b.in_shape.bi == 128 && b.w_shape.bi == 128 &&
-             b.w_shape.bj == 128 && b.w_shape.splits == 1 &&
-             grid_of(b.in_shape) + grid_of(b.w_shape) <= 2 * kCus;
+    b.pair = both && b.in_shape.bi == 128 && b.w_shape.bi == 128 && b.w_shape.bj == 128 &&
+             b.w_shape.splits == 1 && grid_of(b.in_shape) + grid_of(b.w_shape) <= 2 * kCus;
     if (b.pair && b.width <= 1024) set_split(&b.in_shape, K, T, b.width, 1);
+    if (both && !b.pair && in_us > 0.0 && w_us > 0.0)
+        b.pair = choose_pair(T, b.width, K, in_us + w_us, &b.in_shape, &b.w_shape);
+    // the 256-wide tiles read x from here, widened (tile_product.h)
+    if (a.dweight && N && b.w_shape.bi == 256) b.x = c.take<uint16_t>(T * act8_pitch(K));
     int64_t floats = 0;
     if (a.dx) floats = std::max(floats, partial_floats(b.in_shape, K, T));
     if (a.dweight) floats = std::max(floats, partial_floats(b.w_shape, K, N));
@@ -1074,12 +1148,20 @@ extern "C" tide_status tide_linear_backward(const tide_linear_backward_args* arg
     if (b.pair) {
         set_shape(&w, b.w_shape, nullptr);
         set_shape(&x, b.in_shape, b.partial);
+        const int64_t n_w = grid_of(b.w_shape), n_x = grid_of(b.in_shape);
+        if (b.w_shape.bi == 256) {
+            const bool x_first = b.in_shape.split_depth >= b.w_shape.split_depth;
+            auto wide = b.w_shape.bj == 256
+                            ? b.in_shape.bj == 256 ? wide_pair_kernel<256, 256> : wide_pair_kernel<256, 192>
+                            : b.in_shape.bj == 256 ? wide_pair_kernel<192, 256> : wide_pair_kernel<192, 192>;
+            return launch(wide, n_w + n_x, 512, stream, w, x, (int32_t)(x_first ? n_x : 0),
+                          (int32_t)(x_first ? 0 : n_w));
+        }
         auto k = b.in_shape.bj == 128  ? pair_kernel<128, 2, 2>
                  : b.in_shape.bj == 64 ? pair_kernel<64, 2, 2>
                  : b.in_shape.bj == 32 ? pair_kernel<32, 4, 1>
                                        : pair_kernel<16, 4, 1>;
-        const int64_t n_w = grid_of(b.w_shape);
-        TIDE_TRY(launch(k, n_w + grid_of(b.in_shape), 256, stream, w, x, (int32_t)n_w));
+        TIDE_TRY(launch(k, n_w + n_x, 256, stream, w, x, (int32_t)n_w));
         return run_join(x, stream);
     }
     if (a.dx && T) TIDE_TRY(run_product(kGradInput, x, b.in_shape, b.partial, stream));

@@ -379,6 +379,31 @@ def test_every_tile(T, N, K):
     test_backward(T, N, K, "none", False)
 
 
+# dx and dW in one launch of 256-wide tiles: every combination of 256 and 192
+# columns, with the tiles of either product first.
+PAIRS = [(657, 560, 5536), (771, 969, 6265), (869, 1038, 6478), (785, 660, 7642), (1014, 809, 6607),
+         (1489, 528, 7182), (1163, 579, 7954), (1605, 1288, 2524)]
+
+
+@pytest.mark.parametrize("T,N,K", PAIRS)
+def test_both_gradients_in_one_launch(T, N, K):
+    test_backward(T, N, K, "silu", True)
+    test_backward(T, N, K, "none", False)
+
+
+@pytest.mark.parametrize("T,N,K", TILES + PAIRS)
+def test_each_gradient_alone(T, N, K):
+    """dx without dW and dW without dx: each product's own form."""
+    g = gen(T + 3 * N + K)
+    w, dy = normal(g, N, K, scale=1 / math.sqrt(K)), normal(g, T, N, scale=1e-3)
+    x8, x = kept_of(torch.randn(T, K, generator=g, device=DEV))
+    want = ref.backward_ref(dy, w, x, None, "none")
+    within(Linear(w).backward(dy), *want["dx"], "dx")
+    layer = Linear(w, weight_grad=torch.full_like(w, 9))
+    assert layer.backward(dy, x=x8, input_grad=False) is None
+    within(layer.weight_grad, *want["dw"], "dw")
+
+
 @pytest.mark.parametrize("T", [5, 12, 16, 30])
 def test_forward_of_a_weight_past_the_cache(T):
     """Few tokens through a weight of more than 256 MB: deep tiles, split and,
