@@ -13,6 +13,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 
 #include "act8.h"
 #include "bf16_io.h"
@@ -216,8 +217,10 @@ __device__ __forceinline__ void wave_lds_order() { asm volatile("s_waitcnt lgkmc
 template <int BI, int BJ, int K>
 constexpr int kProductLds = 2 * (BI + BJ) * K * 2;
 
-// The tile of workgroup `block` of `blocks`.
-template <int BI, int BJ, int K, int WI, int WJ, Layout CA, Layout CB>
+// The tile of workgroup `block` of `blocks`.  H = 2: the contraction in two
+// halves, each by WI * WJ waves with tiles in LDS of their own, whose sums are
+// added in LDS; each set of waves then finishes half of the tile.
+template <int BI, int BJ, int K, int WI, int WJ, Layout CA, Layout CB, int H = 1>
 __device__ __forceinline__ void product_tile(const Product& p, uint32_t block, uint32_t blocks,
                                              TIDE_LDS char* lds) {
     constexpr int TI = BI / WI / 16, TJ = BJ / WJ / 16;
@@ -225,28 +228,69 @@ __device__ __forceinline__ void product_tile(const Product& p, uint32_t block, u
     int ti, tj, sp;
     tile_at(p, block, blocks, &ti, &tj, &sp);
     const int64_t i0 = (int64_t)ti * BI, j0 = (int64_t)tj * BJ;
-    const int64_t k0 = sp * p.split_depth;
-    const int64_t k1 = min(p.depth, k0 + p.split_depth);
     f32x4v acc[TI][TJ];
-    tile_loop<BI, BJ, K, WI, WJ, CA, CB>(p.A, p.B, p.depth, k0, k1, i0, j0, lds, acc);
+#ifdef __HIP_DEVICE_COMPILE__  // the host's pass fails to instantiate it twice
+    tile_loop<BI, BJ, K, WI, WJ, CA, CB, H>(p.A, p.B, p.depth, sp * p.split_depth,
+                                            min(p.depth, (sp + 1) * p.split_depth), i0, j0, lds, acc);
+#endif
 
     // The accumulators pass through LDS, 16 rows of a wave at a time, so that
     // each lane ends with 8 consecutive columns and a row's stores are whole
     // lines.  The row pitch's extra 4 floats keep the writes off each other's
     // banks.
     constexpr int kRow = TI * 16, kPitch = kRow + 4, kLanes = kRow / 8;
-    static_assert(WI * WJ * 16 * kPitch * 4 <= kProductLds<BI, BJ, K>, "the staging fits");
+    constexpr int kStaging = WI * WJ * H * 16 * kPitch * 4;
+    constexpr int kDone = H == 2 && TJ > 1 ? TJ / 2 : TJ;  // 16-row pieces that a wave finishes
+    static_assert(H == 1 || TJ == 1 || TJ % 2 == 0, "the halves share the tile");
+    static_assert(kStaging <= kProductLds<BI, BJ, K> * H, "the staging fits");
     tile_barrier(lds, lds);
     // (what follows from the thread is worked out here, not kept in registers
     // through the loop)
     int thread = threadIdx.x;
     asm volatile("" : "+v"(thread));
-    const int lane = thread & 63, wave = thread >> 6;
-    TIDE_LDS float* mine = (TIDE_LDS float*)lds + wave * 16 * kPitch;
-    const int64_t iw = i0 + (wave / WJ) * kRow + (lane % kLanes) * 8;
-    const int64_t jw = j0 + (wave % WJ) * TJ * 16 + lane / kLanes;
+    const int half = H == 2 ? __builtin_amdgcn_readfirstlane(thread >> 6) / (WI * WJ) : 0;
+    const int lane = thread & 63, wave = (thread >> 6) - half * WI * WJ;
+    if constexpr (H == 2) {
+        // what the other half's wave finishes goes to it; staging lies behind
+        constexpr int kPiece = 64 * 16, kWave = TI * kDone * kPiece;
+        static_assert(kStaging + 2 * WI * WJ * kWave <= 2 * kProductLds<BI, BJ, K>, "both fit");
+        TIDE_LDS char* box = lds + kStaging + wave * kWave + lane * 16;
+        constexpr int kOther = WI * WJ * kWave;
+        if (half) {
 #pragma unroll
-    for (int y = 0; y < TJ; ++y) {
+            for (int x = 0; x < TI; ++x)
+#pragma unroll
+                for (int y = 0; y < kDone; ++y)
+                    *(TIDE_LDS f32x4v*)(box + (x * kDone + y) * kPiece) = acc[x][y];
+        } else if (TJ > 1) {
+#pragma unroll
+            for (int x = 0; x < TI; ++x)
+#pragma unroll
+                for (int y = 0; y < kDone; ++y)
+                    *(TIDE_LDS f32x4v*)(box + kOther + (x * kDone + y) * kPiece) = acc[x][TJ - kDone + y];
+        }
+        tile_barrier(lds, lds);
+        if (half && TJ == 1) return;
+        if (half) {
+#pragma unroll
+            for (int x = 0; x < TI; ++x)
+#pragma unroll
+                for (int y = 0; y < kDone; ++y)
+                    acc[x][y] = acc[x][TJ - kDone + y] +
+                                *(const TIDE_LDS f32x4v*)(box + kOther + (x * kDone + y) * kPiece);
+        } else {
+#pragma unroll
+            for (int x = 0; x < TI; ++x)
+#pragma unroll
+                for (int y = 0; y < kDone; ++y)
+                    acc[x][y] += *(const TIDE_LDS f32x4v*)(box + (x * kDone + y) * kPiece);
+        }
+    }
+    TIDE_LDS float* mine = (TIDE_LDS float*)lds + (thread >> 6) * 16 * kPitch;
+    const int64_t iw = i0 + (wave / WJ) * kRow + (lane % kLanes) * 8;
+    const int64_t jw = j0 + ((wave % WJ) * TJ + half * kDone) * 16 + lane / kLanes;
+#pragma unroll
+    for (int y = 0; y < kDone; ++y) {
 #pragma unroll
         for (int x = 0; x < TI; ++x)
             *(TIDE_LDS f32x4v*)(mine + (lane & 15) * kPitch + x * 16 + (lane >> 4) * 4) = acc[x][y];
@@ -271,23 +315,26 @@ __device__ __forceinline__ void product_tile(const Product& p, uint32_t block, u
     }
 }
 
-template <int BI, int BJ, int K, int WI, int WJ, Layout CA, Layout CB>
-__global__ __launch_bounds__(WI* WJ * 64, BI == 256 ? 2 : 1) void product_kernel(Product p) {
-    __shared__ __attribute__((aligned(1024))) char lds[kProductLds<BI, BJ, K>];
-    product_tile<BI, BJ, K, WI, WJ, CA, CB>(p, blockIdx.x, gridDim.x, (TIDE_LDS char*)lds);
+template <int BI, int BJ, int K, int WI, int WJ, Layout CA, Layout CB, int H = 1>
+__global__ __launch_bounds__(WI* WJ * 64 * H, BI == 256 ? 2 : 1) void product_kernel(Product p) {
+    __shared__ __attribute__((aligned(1024))) char lds[kProductLds<BI, BJ, K> * H];
+    product_tile<BI, BJ, K, WI, WJ, CA, CB, H>(p, blockIdx.x, gridDim.x, (TIDE_LDS char*)lds);
 }
 
 // dx and dW in one launch, for shapes too small to fill the chip one after the
 // other (77 x 768 x 2048: 13.2 us for both, 7.6, 3.0 and 8.0 for dx, its join
-// and dW): the first `n_w` workgroups take dW's tiles, the others dx's.
-template <int BJ, int WI, int WJ>
-__global__ __launch_bounds__(256) void pair_kernel(Product w, Product x, int32_t n_w) {
-    __shared__ __attribute__((aligned(1024))) char lds[kProductLds<128, 128, 64>];
+// and dW): the first `n_w` workgroups take dW's tiles, the others dx's.  H = 2
+// where each has a compute unit to itself (the same call 14.7 us with dz's
+// launch, 16.0 with one set of waves; 300 x 1024 x 1024 16.3, 18.5).
+template <int BJ, int WI, int WJ, int H>
+__global__ __launch_bounds__(256 * H) void pair_kernel(Product w, Product x, int32_t n_w) {
+    __shared__ __attribute__((aligned(1024))) char lds[kProductLds<128, 128, 64> * H];
     if ((int)blockIdx.x < n_w)
-        product_tile<128, 128, 64, 2, 2, kKept, kColumns>(w, blockIdx.x, n_w, (TIDE_LDS char*)lds);
+        product_tile<128, 128, 64, 2, 2, kKept, kColumns, H>(w, blockIdx.x, n_w,
+                                                             (TIDE_LDS char*)lds);
     else
-        product_tile<128, BJ, 64, WI, WJ, kColumns, kRows>(x, blockIdx.x - n_w, gridDim.x - n_w,
-                                                           (TIDE_LDS char*)lds);
+        product_tile<128, BJ, 64, WI, WJ, kColumns, kRows, H>(x, blockIdx.x - n_w, gridDim.x - n_w,
+                                                              (TIDE_LDS char*)lds);
 }
 
 // The same with 256-wide tiles, one workgroup a compute unit, the product of the
@@ -601,6 +648,7 @@ enum Kind { kForward, kGradInput, kGradWeight };
 // Tile and split for a product of I x J outputs.
 struct Shape {
     int bi, bj, bk;
+    int halves;  // of the contraction inside a workgroup
     int32_t tiles_i, tiles_j, splits;
     int64_t split_depth;
 };
@@ -617,15 +665,17 @@ void set_split(Shape* s, int64_t I, int64_t J, int64_t depth, int64_t splits) {
 // What a tile costs, in microseconds, measured at K = 8192: a step of 64
 // contraction elements when a quarter of the compute units have one (`step`)
 // and what it takes longer when all have (`power`: the clock falls), and the
-// rest of a tile's life (first loads, epilogue).
+// rest of a tile's life (first loads, epilogue).  Of the last, two sets of
+// waves take a step each in that time.
 struct TileCost {
-    int bi, bj;
+    int bi, bj, halves;
     double step, power, rest;
 };
-constexpr TileCost kTiles[] = {{256, 256, 1.25, 0.30, 7.0},
-                               {256, 192, 0.95, 0.36, 6.0},
-                               {256, 128, 0.72, 0.33, 5.0},
-                               {128, 128, 0.60, 0.00, 4.0}};
+constexpr TileCost kTiles[] = {{256, 256, 1, 1.25, 0.30, 7.0},
+                               {256, 192, 1, 0.95, 0.36, 6.0},
+                               {256, 128, 1, 0.72, 0.33, 5.0},
+                               {128, 128, 1, 0.60, 0.00, 4.0},
+                               {128, 128, 2, 1.10, 0.00, 4.3}};
 // Two 128 x 128 tiles on a compute unit take a step each in this time.
 constexpr double kPairStep = 0.95;
 constexpr int kCus = 256;
@@ -640,7 +690,9 @@ double product_us(const TileCost& c, const Shape& s, int64_t I, int64_t J) {
     const double rounds = (double)ceil_div(groups, kCus);
     const double steps = (double)(s.split_depth / 64);
     double us;
-    if (c.bi == 128) {
+    if (c.halves == 2) {
+        us = rounds * (std::ceil(steps / 2) * c.step + c.rest);
+    } else if (c.bi == 128) {
         const double pairs = (double)(int64_t)(rounds / 2), single = rounds - 2 * pairs;
         us = pairs * (steps * kPairStep + c.rest) + single * (steps * c.step + c.rest);
     } else {
@@ -663,10 +715,15 @@ double product_us(const TileCost& c, const Shape& s, int64_t I, int64_t J) {
 // faster from the cache (5120 x 5120 and 24 rows: 30 us that way).
 // Otherwise the tile and split of the least estimated time.  2048 x 5120
 // outputs of depth 13824: 264 us with the 256 x 192 tiles this takes, 290 with
-// 256 x 256, 313 with 128 x 128.
+// 256 x 256, 313 with 128 x 128.  A 128 x 128 tile that has a compute unit to
+// itself is worked on by two sets of waves, half the contraction each, which
+// keeps twice the loads in flight: forward of 1024 x 1024 x 1024 12.5 us, with
+// one set 15.2; 2048 x 2048 x 5120 50, 60; 1500 x 1500 x 3000 takes one set and
+// three splits, two workgroups a compute unit, 32 (with two sets 39).
 Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth, double* estimate = nullptr) {
     Shape s = {};
     s.bk = 64;
+    s.halves = 1;
     if (J <= 64) {
         s.bi = 128;
         s.bj = J <= 16 ? 16 : J <= 32 ? 32 : 64;
@@ -682,6 +739,7 @@ Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth, double* estimate = 
             Shape t = s;
             t.bi = c.bi;
             t.bj = c.bj;
+            t.halves = c.halves;
             set_split(&t, I, J, depth, splits);
             if (t.splits < splits) break;  // the contraction has no more units
             const double us = product_us(c, t, I, J);
@@ -709,7 +767,7 @@ bool choose_pair(int64_t T, int64_t N, int64_t K, double best, Shape* in, Shape*
     for (int a = 0; a < kWide; ++a) {
         for (int b = 0; b < kWide; ++b) {
             const TileCost &cx = kTiles[a], &cw = kTiles[b];
-            Shape x = {cx.bi, cx.bj, 64}, w = {cw.bi, cw.bj, 64};
+            Shape x = {cx.bi, cx.bj, 64, 1}, w = {cw.bi, cw.bj, 64, 1};
             set_split(&x, K, T, N, 1);
             set_split(&w, K, N, T, 1);
             const int64_t nx = (int64_t)x.tiles_i * x.tiles_j, nw = (int64_t)w.tiles_i * w.tiles_j;
@@ -743,12 +801,12 @@ int64_t partial_floats(const Shape& s, int64_t I, int64_t J) {
 
 using ProductKernel = void (*)(Product);
 
-template <int BI, int BJ, int K, int WI, int WJ>
+template <int BI, int BJ, int K, int WI, int WJ, int H = 1>
 ProductKernel of_kind(Kind k) {
     switch (k) {
-        case kForward: return product_kernel<BI, BJ, K, WI, WJ, kRows, kRows>;
-        case kGradInput: return product_kernel<BI, BJ, K, WI, WJ, kColumns, kRows>;
-        default: return product_kernel<BI, BJ, K, WI, WJ, BI == 256 ? kColumns : kKept, kColumns>;
+        case kForward: return product_kernel<BI, BJ, K, WI, WJ, kRows, kRows, H>;
+        case kGradInput: return product_kernel<BI, BJ, K, WI, WJ, kColumns, kRows, H>;
+        default: return product_kernel<BI, BJ, K, WI, WJ, BI == 256 ? kColumns : kKept, kColumns, H>;
     }
 }
 
@@ -781,7 +839,8 @@ tide_status run_product(Kind kind, Product p, const Shape& s, float* partial,
                           : of_kind<256, 128, 64, 2, 4>(kind);
         threads = 512;
     } else if (s.bj == 128) {
-        k = of_kind<128, 128, 64, 2, 2>(kind);
+        k = s.halves == 2 ? of_kind<128, 128, 64, 2, 2, 2>(kind) : of_kind<128, 128, 64, 2, 2>(kind);
+        threads = 256 * s.halves;
     } else if (s.bj == 64) {
         k = of_kind<128, 64, 64, 2, 2>(kind);
     } else if (s.bj == 32) {
@@ -1012,6 +1071,16 @@ tide_status check_backward(const tide_linear_backward_args& a) {
     return TIDE_OK;
 }
 
+using PairKernel = void (*)(Product, Product, int32_t);
+
+template <int H>
+PairKernel pair_of(int bj) {
+    return bj == 128  ? pair_kernel<128, 2, 2, H>
+           : bj == 64 ? pair_kernel<64, 2, 2, H>
+           : bj == 32 ? pair_kernel<32, 4, 1, H>
+                      : pair_kernel<16, 4, 1, H>;
+}
+
 using DzKernel = void (*)(DzArgs);
 
 DzKernel dz_kernel_of(int32_t act) {
@@ -1157,11 +1226,9 @@ extern "C" tide_status tide_linear_backward(const tide_linear_backward_args* arg
             return launch(wide, n_w + n_x, 512, stream, w, x, (int32_t)(x_first ? n_x : 0),
                           (int32_t)(x_first ? 0 : n_w));
         }
-        auto k = b.in_shape.bj == 128  ? pair_kernel<128, 2, 2>
-                 : b.in_shape.bj == 64 ? pair_kernel<64, 2, 2>
-                 : b.in_shape.bj == 32 ? pair_kernel<32, 4, 1>
-                                       : pair_kernel<16, 4, 1>;
-        TIDE_TRY(launch(k, n_w + n_x, 256, stream, w, x, (int32_t)n_w));
+        const int halves = n_w + n_x <= kCus ? 2 : 1;
+        auto k = halves == 2 ? pair_of<2>(b.in_shape.bj) : pair_of<1>(b.in_shape.bj);
+        TIDE_TRY(launch(k, n_w + n_x, 256 * halves, stream, w, x, (int32_t)n_w));
         return run_join(x, stream);
     }
     if (a.dx && T) TIDE_TRY(run_product(kGradInput, x, b.in_shape, b.partial, stream));

@@ -372,7 +372,10 @@ __device__ __forceinline__ void plain_step(TIDE_LDS char* __restrict__ next,
 
 // The loop over the contraction elements [k0, k1) of `depth` (the longer
 // operand's) of the tile at (i0, j0), with two tiles of K of them in LDS.
-template <int BI, int BJ, int K, int WI, int WJ, Layout CA, Layout CB>
+// H = 2: the elements in two halves of as many steps, each by WI * WJ waves
+// with tiles of their own in LDS.  (Only where k1 = depth can the number of
+// steps be odd, and behind `depth` the operands read as 0.)
+template <int BI, int BJ, int K, int WI, int WJ, Layout CA, Layout CB, int H>
 __device__ __forceinline__ void tile_loop(const Operand& A, const Operand& B, int64_t depth,
                                           int64_t k0, int64_t k1, int64_t i0, int64_t j0,
                                           TIDE_LDS char* lds,
@@ -382,7 +385,15 @@ __device__ __forceinline__ void tile_loop(const Operand& A, const Operand& B, in
     using SB = typename StagerOf<BJ, K, kWaves, CB, false>::type;
     constexpr int kTile = SA::kBytes + SB::kBytes;
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int steps = (int)((k1 - k0 + K - 1) / K);
+    if constexpr (H == 2) {
+        const int half = wave / kWaves;
+        wave -= half * kWaves;
+        steps = (steps + 1) / 2;
+        k0 += (int64_t)half * steps * K;
+        lds += half * 2 * kTile;
+    }
     const int wi = (wave / WJ) * TI * 16, wj = (wave % WJ) * TJ * 16;
     SA sa;
     SB sb;
@@ -392,8 +403,7 @@ __device__ __forceinline__ void tile_loop(const Operand& A, const Operand& B, in
     for (int x = 0; x < TI; ++x)
 #pragma unroll
         for (int y = 0; y < TJ; ++y) acc[x][y] = 0;
-    if (k0 >= k1) return;
-    const int steps = (int)((k1 - k0 + K - 1) / K);
+    if (steps == 0) return;
     int64_t valid = depth - k0;
     int at = 0;
     sa.prime();

@@ -362,14 +362,19 @@ def test_gradients_against_differences(act):
 # ---- every tile, whole and split ---------------------------------------------------------------
 
 # Shapes that between them take each form of the three products: 256 x 256, 256 x
-# 192, 256 x 128 and 128 x 128 tiles and the narrow ones, each with a whole and a
-# split contraction, and dx and dW in one launch with each tile of dx.
+# 192, 256 x 128, 128 x 128 tiles (by one and by two sets of waves) and the narrow
+# ones, each with a whole and a split contraction, and dx and dW in one launch
+# with each tile of dx, by one and by two sets of waves.
 TILES = [(2500, 1550, 260), (1300, 1000, 4001), (5001, 1551, 24), (130, 8201, 2508), (8200, 1303, 25),
          (2500, 1032, 5000), (24, 1032, 5001), (1550, 260, 2500), (1300, 4000, 1000), (1550, 24, 5000),
          (8208, 2501, 130), (8200, 24, 1301), (2501, 5001, 1032), (260, 777, 5000), (4000, 1301, 1001),
          (24, 5003, 1551), (2500, 130, 8200), (24, 8203, 1303), (5000, 2500, 1032), (12, 1040, 200),
          (24, 1035, 24), (40, 1032, 25), (70, 1032, 25), (513, 518, 27), (40, 2051, 2508), (10, 24, 2000),
-         (25, 24, 1040), (40, 24, 1040), (1032, 40, 24), (1035, 24, 24), (1030, 12, 40), (4, 40, 5000)]
+         (25, 24, 1040), (40, 24, 1040), (1032, 40, 24), (1035, 24, 24), (1030, 12, 40), (4, 40, 5000),
+         (517, 2345, 3152), (5407, 153, 4043), (1343, 1450, 3975), (683, 5450, 3587), (273, 134, 6549),
+         (7, 387, 6579), (6, 5489, 390), (18, 397, 6590), (18, 5617, 396), (33, 389, 6905),
+         (33, 4375, 516), (2425, 130, 5401), (3907, 5428, 148), (4074, 1328, 1412), (3713, 645, 5490),
+         (258, 2310, 3592), (5485, 3928, 166), (1342, 3934, 1414), (1210, 4191, 3203)]
 
 
 @pytest.mark.parametrize("T,N,K", TILES)
