@@ -731,6 +731,11 @@ Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth, double* estimate = 
         // a contraction of up to 1024 is over before a join would be
         const int64_t want = depth <= 1024 ? 1 : s.bk == 256 ? kCus : 2 * kCus;
         set_split(&s, I, J, depth, want / std::max<int64_t>(1, ceil_div(I, s.bi)));
+        // 28672 x 1024: 15.1 us and 40 rows, with one set of waves 16.5; with
+        // more tiles than compute units more of the smaller workgroups fit
+        // (65536 x 1024 and 40 rows: 23.8, with two sets 29.5), and up to 16
+        // rows or 512 elements there is nothing to gain
+        if (s.bj > 16 && depth > 512 && depth <= 1024 && s.tiles_i <= kCus) s.halves = 2;
         return s;
     }
     double best = 0.0;
@@ -842,9 +847,13 @@ tide_status run_product(Kind kind, Product p, const Shape& s, float* partial,
         k = s.halves == 2 ? of_kind<128, 128, 64, 2, 2, 2>(kind) : of_kind<128, 128, 64, 2, 2>(kind);
         threads = 256 * s.halves;
     } else if (s.bj == 64) {
-        k = of_kind<128, 64, 64, 2, 2>(kind);
+        k = s.halves == 2 ? of_kind<128, 64, 64, 2, 2, 2>(kind) : of_kind<128, 64, 64, 2, 2>(kind);
+        threads = 256 * s.halves;
     } else if (s.bj == 32) {
-        k = s.bk == 256 ? product_kernel<128, 32, 256, 4, 1, kRows, kRows> : of_kind<128, 32, 64, 4, 1>(kind);
+        k = s.bk == 256     ? product_kernel<128, 32, 256, 4, 1, kRows, kRows>
+            : s.halves == 2 ? of_kind<128, 32, 64, 4, 1, 2>(kind)
+                            : of_kind<128, 32, 64, 4, 1>(kind);
+        threads = 256 * s.halves;
     } else {
         k = s.bk == 256 ? product_kernel<128, 16, 256, 4, 1, kRows, kRows> : of_kind<128, 16, 64, 4, 1>(kind);
     }

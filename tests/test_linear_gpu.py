@@ -374,7 +374,8 @@ TILES = [(2500, 1550, 260), (1300, 1000, 4001), (5001, 1551, 24), (130, 8201, 25
          (517, 2345, 3152), (5407, 153, 4043), (1343, 1450, 3975), (683, 5450, 3587), (273, 134, 6549),
          (7, 387, 6579), (6, 5489, 390), (18, 397, 6590), (18, 5617, 396), (33, 389, 6905),
          (33, 4375, 516), (2425, 130, 5401), (3907, 5428, 148), (4074, 1328, 1412), (3713, 645, 5490),
-         (258, 2310, 3592), (5485, 3928, 166), (1342, 3934, 1414), (1210, 4191, 3203)]
+         (258, 2310, 3592), (5485, 3928, 166), (1342, 3934, 1414), (1210, 4191, 3203), (24, 300, 1000),
+         (40, 520, 1001), (24, 1001, 300), (40, 777, 520), (700, 24, 300), (1000, 40, 520)]
 
 
 @pytest.mark.parametrize("T,N,K", TILES)
