@@ -1,0 +1,48 @@
+"""GPU tests of the layer products where their arithmetic is most easily lost:
+activation functions far from zero, values at the ends of the checkpoint's
+range.  Bounds and references as in tests/linear_ref.py."""
+import math
+
+import pytest
+import torch
+
+from shard_placement_amd.linear import Linear
+from tests import linear_ref as ref
+from tests.test_linear_gpu import BF, DEV, kept_of, normal, gen, within
+
+pytestmark = pytest.mark.gpu
+
+# What exp2's argument is off by: z^2 and its product with the constant, a binary32
+# step together, which the exponential multiplies by z^2 / 2.
+def _bell(z):
+    return z * z * ref.F32
+
+
+@pytest.mark.parametrize("lo,hi", [(-13.0, -8.0), (-8.0, -4.0), (-4.0, 0.0), (0.0, 6.0)])
+def test_gelu_relative(lo, hi):
+    """gelu is z Phi(z) to a bf16 rounding relative to itself, in its negative
+    tail too: a fit within 6 binary32 steps, 10 operations, and the exponential's
+    argument."""
+    z = torch.linspace(lo, hi, 1500, dtype=torch.float64, device=DEV).to(BF)
+    w = torch.zeros(z.numel(), 8, dtype=BF, device=DEV)
+    x = torch.zeros(6, 8, dtype=BF, device=DEV)  # z = bias
+    want = ref.act_ref(z.double(), "gelu").expand(6, -1)
+    off = 16 * ref.F32 + _bell(z.double())
+    within(Linear(w, bias=z, act="gelu").forward(x), want, want.abs() * (ref.BF16 * (1 + off) + off), "y")
+
+
+def test_gelu_slope_relative():
+    """The slope Phi(z) + z exp(-z^2 / 2) / sqrt(2 pi), relative to its two terms."""
+    grid = ref.e4m3_grid().to(DEV)
+    z = torch.cat([-grid[(grid >= 2.0 ** -4) & (grid <= 13.0)], grid[(grid >= 2.0 ** -4) & (grid <= 13.0)]])
+    z = torch.cat([z, z.new_zeros(-z.numel() % 32)])
+    N = z.numel()
+    z8, zv = kept_of(z.expand(5, N).contiguous())
+    assert torch.equal(zv, z.expand(5, N))
+    dy = normal(gen(4), 5, N)
+    w = torch.eye(N, dtype=BF, device=DEV)  # dx = dz
+    dx = Linear(w, act="gelu").backward(dy, z=z8)
+    terms = torch.special.erfc(-z / math.sqrt(2)) / 2 + z.abs() * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    want = dy.double() * ref.slope_ref(z, "gelu")
+    e = dy.double().abs() * terms * (24 * ref.F32 + _bell(z))
+    within(dx, want, 2 * ref.BF16 * (want.abs() + e) + e, "dx")
