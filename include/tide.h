@@ -515,7 +515,8 @@ tide_status tide_act8_unpack(const void *kept, int64_t rows, int64_t cols, void 
  *           products (dbias sums it unrounded).  The residual's gradient is
  *           dy itself.
  *
- * A z that is not finite was kept as NaN and makes its gradients NaN.  The
+ * A z that is not finite was kept as NaN and makes its gradients NaN; a
+ * finite one that reads back as infinity has the slope there, 1 or 0.  The
  * gradient of relu at 0 is 0.  relu of minus infinity is 0; gelu, gelu_tanh
  * and silu of it are NaN (minus infinity times 0).
  *

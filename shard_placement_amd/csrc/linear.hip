@@ -49,7 +49,7 @@ __device__ __forceinline__ float sigmoid(float u) {
 // gelu is a bf16 rounding off in its far negative tail too, where a formula of
 // small absolute error is percents off.  A library erff took 55 us in the
 // gradient of 2048 x 13824 elements, which reads and writes 141 MB, where this
-// takes 39; a forward of 4096 x 16384 x 1024 with gelu takes 157 us, 154 with
+// takes 40; a forward of 4096 x 16384 x 1024 with gelu takes 157 us, 154 with
 // a shorter polynomial of small absolute error, 2% off at z = -10.
 __device__ __forceinline__ float normal_cdf(float z, float* bell) {
     const float g = __builtin_amdgcn_exp2f(-0.5f * kLog2E * (z * z));
@@ -78,13 +78,19 @@ __device__ __forceinline__ float act_value(float z) {
     return z;
 }
 
+// z may be infinite where a finite one was kept (act8.h: values that round up
+// to 2^128), and infinity times the 0 that bounds it would be NaN: a factor z is
+// held within what changes nothing, the other factor being 0 outside.  (NaN
+// reaches the result through the other terms.)
+__device__ __forceinline__ float within(float z) { return __builtin_amdgcn_fmed3f(z, -256.0f, 256.0f); }
+
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
-    if constexpr (ACT == TIDE_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f * z;
+    if constexpr (ACT == TIDE_ACT_RELU) return z > 0.0f ? 1.0f : z < 0.0f ? 0.0f : 0.0f * z;
     if constexpr (ACT == TIDE_ACT_GELU) {
         float bell;
         const float cdf = normal_cdf(z, &bell);
-        return __builtin_fmaf(z * kInvSqrt2Pi, bell, cdf);
+        return __builtin_fmaf(within(z) * kInvSqrt2Pi, bell, cdf);
     }
     if constexpr (ACT == TIDE_ACT_GELU_TANH) {
         const float t = z * z;
@@ -95,7 +101,7 @@ __device__ __forceinline__ float act_slope(float z) {
     }
     if constexpr (ACT == TIDE_ACT_SILU) {
         const float s = sigmoid(z);
-        return s * __builtin_fmaf(z, 1.0f - s, 1.0f);
+        return s * __builtin_fmaf(within(z), 1.0f - s, 1.0f);
     }
     return 1.0f;
 }

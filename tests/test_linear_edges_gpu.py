@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from shard_placement_amd.linear import Linear
+from shard_placement_amd.linear import Act8, Linear
 from tests import linear_ref as ref
 from tests.test_linear_gpu import BF, DEV, kept_of, normal, gen, within
 
@@ -46,3 +46,27 @@ def test_gelu_slope_relative():
     want = dy.double() * ref.slope_ref(z, "gelu")
     e = dy.double().abs() * terms * (24 * ref.F32 + _bell(z))
     within(dx, want, 2 * ref.BF16 * (want.abs() + e) + e, "dx")
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("T", [3, 70])
+def test_slope_of_a_value_that_reads_back_as_infinity(act, T):
+    """The largest bf16 numbers round up to 2^128 in a checkpoint; their slope is
+    1 or 0, and only a z that was not finite makes NaN."""
+    N = 64
+    z = torch.full((T, N), 0.5, dtype=BF, device=DEV)
+    top = torch.finfo(BF).max
+    z[1, 4], z[1, 40], z[2, 7], z[2, 8] = top, -top, math.inf, math.nan
+    z8 = Act8(T, N, device=DEV).pack(z)
+    back = z8.unpack()
+    assert back[1, 4] == math.inf and back[1, 40] == -math.inf
+    assert back[2, 7].isnan() and back[2, 8].isnan()
+    dy = torch.full((T, N), 3.0, dtype=BF, device=DEV)
+    db = torch.empty(N, dtype=BF, device=DEV)
+    dx = Linear(torch.eye(N, dtype=BF, device=DEV), act=act, bias_grad=db).backward(dy, z=z8)
+    # a NaN of dz reaches its token's whole row of dx, and its column's dbias
+    assert dx[2].isnan().all() and db[7].isnan() and db[8].isnan()
+    assert dx[1, 4] == 3.0 and dx[1, 40] == 0.0
+    keep = torch.ones(T, N, dtype=torch.bool, device=DEV)
+    keep[2] = False
+    assert dx[keep].isfinite().all() and db[[4, 40]].isfinite().all()
