@@ -307,7 +307,7 @@ def test_backward_strides(T, N, K, lds, shifts, act):
     assert torch.equal(buf.view(torch.int16), before.view(torch.int16))
 
 
-def test_each_gradient_alone():
+def test_each_gradient_alone_and_what_it_needs():
     g = gen(77)
     T, N, K = 90, 136, 200
     w, dy = normal(g, N, K), normal(g, T, N)
