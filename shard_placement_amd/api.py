@@ -325,6 +325,10 @@ def _on_device(index: int, stream, call, *args):
     (default: the device's current stream) the one that allocations belong to."""
     if stream is None and index == _current_device():
         return call(_raw_stream(index), *args)
+    if stream is not None and stream.device_index != index:
+        # entering it would make its device current, and the kernels run there
+        raise TideError(-1, "stream belongs to cuda:%d, the tensors to cuda:%d"
+                        % (stream.device_index, index))
     with torch.cuda.device(index):
         if stream is None:
             return call(_raw_stream(index), *args)
