@@ -41,7 +41,7 @@ class Act8:
         self.rows, self.cols = int(rows), int(cols)
         need = self.bytes(self.rows, self.cols)
         if buffer is None:
-            buffer = torch.empty(need, dtype=torch.uint8, device=device or "cuda")
+            buffer = torch.empty(need, dtype=torch.uint8, device="cuda" if device is None else device)
         if not buffer.is_contiguous():
             raise TideError(-6, "buffer is not contiguous")
         flat = buffer.view(-1).view(torch.uint8)

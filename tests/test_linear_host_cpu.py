@@ -50,3 +50,17 @@ def test_stream_of_another_device_is_refused(no_gpu, handle):
             api._on_device(index, stream(other, handle), ran.append)
         assert e.value.status == -1
     assert not ran and not no_gpu
+
+
+@pytest.mark.parametrize("device", [0, 1, "cuda:1", torch.device("cuda", 0), None])
+def test_device_of_a_new_checkpoint(monkeypatch, device):
+    """Device 0 by its index is device 0, not the current one."""
+    asked, empty = [], torch.empty
+
+    def record(*shape, device=None, **kw):
+        asked.append(device)
+        return empty(*shape, **kw)
+
+    monkeypatch.setattr(torch, "empty", record)
+    linear.Act8(3, 40, device=device)
+    assert asked == ["cuda" if device is None else device]
