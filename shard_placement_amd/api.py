@@ -363,12 +363,21 @@ def _rows(t: torch.Tensor, what: str):
     return t.data_ptr(), ld
 
 
+def _no_graph(t: torch.Tensor, what: str) -> None:
+    """The layer calls are not recorded by autograd: a tensor whose gradient it
+    would follow through them is refused, not detached without a word."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise TideError(-6, "%s requires a gradient that autograd would not see: detach it, or call "
+                        "under torch.no_grad()" % what)
+
+
 def _matrix(t: torch.Tensor, rows: int, cols: int, what: str, index: int):
     """The same of a bf16 [rows, cols] matrix on GPU ``index``."""
     if _index(t, what) != index:
         raise TideError(-6, "%s is on %s, expected cuda:%d" % (what, t.device, index))
     if t.shape != (rows, cols):
         raise TideError(-1, "%s is %s, expected [%d, %d]" % (what, list(t.shape), rows, cols))
+    _no_graph(t, what)
     return _rows(t, what)
 
 
@@ -460,8 +469,10 @@ def tide_linear_forward(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor =
                         residual=None, act: str = "none", z_kept=None, stream=None) -> torch.Tensor:
     """y = act(x weight^T + bias) + residual; z_kept (uint8), where given,
     receives the checkpoint of act's argument.  Returns y (allocated when not
-    given)."""
+    given).  Nothing is recorded by autograd (tide_linear_backward is the
+    gradient): x, residual and y may not require one in grad mode."""
     index = _index(x, "x")
+    _no_graph(x, "x")
     T, K = x.shape
     if weight.dim() != 2:
         raise TideError(-1, "weight has %d dimensions, expected 2" % weight.dim())
@@ -497,6 +508,7 @@ def tide_linear_backward(dy: torch.Tensor, in_features: int, weight=None, x_kept
     the sum of dz over the tokens, dz = dy act'(z).  dx=True allocates it.
     Returns dx."""
     index = _index(dy, "dy")
+    _no_graph(dy, "dy")
     T, N = dy.shape
     K = int(in_features)
     pdy, lddy = _rows(dy, "dy")

@@ -15,7 +15,11 @@ or in the caller's, e.g. a vacated gathered buffer.
     dx = layer.backward(dy, x=x8, z=z8)     # writes grads[q][p]
 
 All work is done by the library (``include/tide.h``); this module only holds
-tensors together.
+tensors together.  Autograd records none of it: ``backward`` is the gradient, a
+weight's goes to ``weight_grad`` and never to ``weight.grad``, and activations
+that require a gradient are refused in grad mode.  In a
+``torch.autograd.Function`` grad mode is off, so its forward and backward can
+call these as they are.
 """
 from __future__ import annotations
 

@@ -64,3 +64,55 @@ def test_device_of_a_new_checkpoint(monkeypatch, device):
     monkeypatch.setattr(torch, "empty", record)
     linear.Act8(3, 40, device=device)
     assert asked == ["cuda" if device is None else device]
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """CPU tensors taken for a GPU's (index -1); the library's calls recorded."""
+    ran = []
+    monkeypatch.setattr(api, "_index", lambda t, what: -1)
+    monkeypatch.setattr(api, "_require", lambda t, dtype, what: None)
+    monkeypatch.setattr(api, "_on_device", lambda index, stream, call, *a: ran.append(call.__name__))
+    return ran
+
+
+def test_tensors_of_an_autograd_graph_are_refused(calls):
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    leaf = lambda *s: bf(*s).requires_grad_()  # noqa: E731
+    layer = linear.Linear(leaf(8, 16), bias=leaf(8))  # their gradients have places of their own
+    uses = [lambda f: layer.forward(f(4, 16)), lambda f: layer.forward(bf(4, 16), residual=f(4, 8)),
+            lambda f: layer.forward(bf(4, 16), out=f(4, 8)), lambda f: layer.backward(f(4, 8)),
+            lambda f: layer.backward(bf(4, 8), dx=f(4, 16)),
+            lambda f: api.tide_linear_forward(f(4, 16), bf(8, 16)),
+            lambda f: api.tide_linear_forward(bf(4, 16), bf(8, 16), residual=f(4, 8)),
+            lambda f: api.tide_linear_backward(f(4, 8), 16, dbias=bf(8))]
+    for use in uses:
+        with pytest.raises(TideError, match="requires a gradient") as e:
+            use(leaf)
+        assert e.value.status == -6 and not calls
+        for plain in (bf, lambda *s: leaf(*s).detach()):
+            use(plain)
+        with torch.no_grad():
+            use(leaf)
+        assert len(calls) == 3
+        calls.clear()
+
+
+def test_inside_an_autograd_function(calls):
+    """Grad mode is off in a Function's forward and backward."""
+    layer = linear.Linear(torch.zeros(8, 16, dtype=torch.bfloat16))
+
+    class Product(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            layer.forward(x)
+            return x[:, :8] * 2
+
+        @staticmethod
+        def backward(ctx, dy):
+            layer.backward(dy)
+            return torch.cat([dy, dy], 1)
+
+    x = torch.zeros(4, 16, dtype=torch.bfloat16, requires_grad=True)
+    (Product.apply(x) * 3).sum().backward()
+    assert calls == ["_forward_on", "_backward_on"]
