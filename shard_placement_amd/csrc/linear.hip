@@ -12,12 +12,11 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <climits>
-#include <cmath>
 
 #include "act8.h"
 #include "bf16_io.h"
 #include "linear_check.h"
+#include "product_shape.h"
 #include "tide.h"
 #include "tile_product.h"
 
@@ -638,9 +637,6 @@ __global__ __launch_bounds__(64 * kDbWaves) void dbias_kernel(const float* sums,
 
 // ---- host ----------------------------------------------------------------
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
-
 // The workspace's pieces, handed out in order, each on 256 bytes.
 struct Carver {
     char* base;
@@ -652,165 +648,6 @@ struct Carver {
         return p;
     }
 };
-
-constexpr int64_t kSplitUnit = 256;  // contraction elements
-
-enum Kind { kForward, kGradInput, kGradWeight };
-
-// Tile and split for a product of I x J outputs.
-struct Shape {
-    int bi, bj, bk;
-    int halves;  // of the contraction inside a workgroup
-    int32_t tiles_i, tiles_j, splits;
-    int64_t split_depth;
-};
-
-void set_split(Shape* s, int64_t I, int64_t J, int64_t depth, int64_t splits) {
-    const int64_t units = ceil_div(depth, kSplitUnit);
-    const int64_t each = std::max<int64_t>(1, ceil_div(units, std::max<int64_t>(1, splits)));
-    s->tiles_i = (int32_t)ceil_div(I, s->bi);
-    s->tiles_j = (int32_t)ceil_div(J, s->bj);
-    s->split_depth = each * kSplitUnit;
-    s->splits = (int32_t)std::max<int64_t>(1, ceil_div(units, each));
-}
-
-// What a tile costs, in microseconds, measured at K = 8192: a step of 64
-// contraction elements when a quarter of the compute units have one (`step`)
-// and what it takes longer when all have (`power`: the clock falls), and the
-// rest of a tile's life (first loads, epilogue).  Of the last, two sets of
-// waves take a step each in that time.
-struct TileCost {
-    int bi, bj, halves;
-    double step, power, rest;
-};
-constexpr TileCost kTiles[] = {{256, 256, 1, 1.25, 0.30, 7.0},
-                               {256, 192, 1, 0.95, 0.36, 6.0},
-                               {256, 128, 1, 0.72, 0.33, 5.0},
-                               {128, 128, 1, 0.60, 0.00, 4.0},
-                               {128, 128, 2, 1.10, 0.00, 4.3}};
-// Two 128 x 128 tiles on a compute unit take a step each in this time.
-constexpr double kPairStep = 0.95;
-constexpr int kCus = 256;
-
-// A tile of 256 rows, with `used` of the compute units at work.
-double wide_tile_us(const TileCost& c, const Shape& s, double used) {
-    return (double)(s.split_depth / 64) * (c.step + c.power * used * used) + c.rest;
-}
-
-double product_us(const TileCost& c, const Shape& s, int64_t I, int64_t J) {
-    const int64_t groups = (int64_t)s.tiles_i * s.tiles_j * s.splits;
-    const double rounds = (double)ceil_div(groups, kCus);
-    const double steps = (double)(s.split_depth / 64);
-    double us;
-    if (c.halves == 2) {
-        us = rounds * (std::ceil(steps / 2) * c.step + c.rest);
-    } else if (c.bi == 128) {
-        const double pairs = (double)(int64_t)(rounds / 2), single = rounds - 2 * pairs;
-        us = pairs * (steps * kPairStep + c.rest) + single * (steps * c.step + c.rest);
-    } else {
-        us = rounds * wide_tile_us(c, s, (double)groups / (rounds * kCus));
-    }
-    // partial sums: a compute unit writes 40 KB/us, the join is a launch of its
-    // own and reads 5.5 MB/us
-    if (s.splits > 1)
-        us += rounds * 4.0 * c.bi * c.bj / 40e3 +
-              3.0 + 4.0 * (double)s.splits * (double)I * (double)J / 5.5e6;
-    return us;
-}
-
-// Up to 64 rows of outputs the A operand's bytes bound the product: narrow
-// tiles, and the contraction split until about two workgroups a compute unit
-// keep loads in flight (5120 x 5120 and 16 rows: 13.8 us, with one 15.6, with
-// four 16.8).  A forward weight of more bytes than the 256 MB cache holds is
-// read 512 bytes of a row at a time and past the cache, in tiles that fill
-// LDS: 80 us for 28672 x 8192 and 16 rows, 115 otherwise.  Smaller weights are
-// faster from the cache (5120 x 5120 and 24 rows: 30 us that way).
-// Otherwise the tile and split of the least estimated time.  2048 x 5120
-// outputs of depth 13824: 264 us with the 256 x 192 tiles this takes, 290 with
-// 256 x 256, 313 with 128 x 128.  A 128 x 128 tile that has a compute unit to
-// itself is worked on by two sets of waves, half the contraction each, which
-// keeps twice the loads in flight: forward of 1024 x 1024 x 1024 12.5 us, with
-// one set 15.2; 2048 x 2048 x 5120 50, 60; 1500 x 1500 x 3000 takes one set and
-// three splits, two workgroups a compute unit, 32 (with two sets 39).
-Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth, double* estimate = nullptr) {
-    Shape s = {};
-    s.bk = 64;
-    s.halves = 1;
-    if (J <= 64) {
-        s.bi = 128;
-        s.bj = J <= 16 ? 16 : J <= 32 ? 32 : 64;
-        if (kind == kForward && s.bj <= 32 && I * depth > ((int64_t)128 << 20)) s.bk = 256;
-        // a contraction of up to 1024 is over before a join would be
-        const int64_t want = depth <= 1024 ? 1 : s.bk == 256 ? kCus : 2 * kCus;
-        set_split(&s, I, J, depth, want / std::max<int64_t>(1, ceil_div(I, s.bi)));
-        // 28672 x 1024: 15.1 us and 40 rows, with one set of waves 16.5; with
-        // more tiles than compute units more of the smaller workgroups fit
-        // (65536 x 1024 and 40 rows: 23.8, with two sets 29.5), and up to 16
-        // rows or 512 elements there is nothing to gain
-        if (s.bj > 16 && depth > 512 && depth <= 1024 && s.tiles_i <= kCus) s.halves = 2;
-        return s;
-    }
-    double best = 0.0;
-    for (const TileCost& c : kTiles) {
-        for (int64_t splits = 1; splits <= 16; ++splits) {
-            Shape t = s;
-            t.bi = c.bi;
-            t.bj = c.bj;
-            t.halves = c.halves;
-            set_split(&t, I, J, depth, splits);
-            if (t.splits < splits) break;  // the contraction has no more units
-            const double us = product_us(c, t, I, J);
-            if (best == 0.0 || us < best) {
-                best = us;
-                s = t;
-            }
-            if ((int64_t)t.tiles_i * t.tiles_j >= 4 * kCus) break;  // enough without
-        }
-    }
-    if (estimate) *estimate = best;
-    return s;
-}
-
-// dx [T, K] and dW [N, K] in one launch of 256-wide tiles, the longer ones
-// first: the pair of tiles of the least estimated time, or none if that is not
-// 3% less than `best`, that of the two products one after the other.
-// (Measured, both gradients with dz, against two launches: 2048 x 13824 x 5120
-// 496 us, 600; 8192 x 8192 x 1024 272, 331; 3000 x 1280 x 8192 129, 141; and 748
-// against 729 for 700 x 28672 x 8192, whose estimates were 0.7% apart.)
-bool choose_pair(int64_t T, int64_t N, int64_t K, double best, Shape* in, Shape* weight) {
-    constexpr int kWide = 2;  // 256 x 256 and 256 x 192
-    bool found = false;
-    best *= 0.97;
-    for (int a = 0; a < kWide; ++a) {
-        for (int b = 0; b < kWide; ++b) {
-            const TileCost &cx = kTiles[a], &cw = kTiles[b];
-            Shape x = {cx.bi, cx.bj, 64, 1}, w = {cw.bi, cw.bj, 64, 1};
-            set_split(&x, K, T, N, 1);
-            set_split(&w, K, N, T, 1);
-            const int64_t nx = (int64_t)x.tiles_i * x.tiles_j, nw = (int64_t)w.tiles_i * w.tiles_j;
-            const double tx = wide_tile_us(cx, x, 1.0), tw = wide_tile_us(cw, w, 1.0);
-            const double longer = std::max(tx, tw), shorter = std::min(tx, tw);
-            const int64_t n_long = tx >= tw ? nx : nw;
-            int64_t n_short = nx + nw - n_long;
-            // whole rounds of the longer; then the shorter beside the rest of
-            // them, and on the whole chip behind them
-            double us = (double)(n_long / kCus) * longer;
-            const int64_t rest = n_long % kCus;
-            if (rest) {
-                us += longer;
-                n_short -= (kCus - rest) * (int64_t)(longer / shorter);
-            }
-            if (n_short > 0) us += (double)ceil_div(n_short, kCus) * shorter;
-            if (us < best) {
-                best = us;
-                *in = x;
-                *weight = w;
-                found = true;
-            }
-        }
-    }
-    return found;
-}
 
 int64_t partial_floats(const Shape& s, int64_t I, int64_t J) {
     return s.splits > 1 ? s.splits * J * round_up(I, kActBlock) : 0;
@@ -835,8 +672,6 @@ void set_shape(Product* p, const Shape& s, float* partial) {
     p->partial = partial;
     p->partial_pitch = round_up(p->e.I, kActBlock);
 }
-
-int64_t grid_of(const Shape& s) { return (int64_t)s.tiles_i * s.tiles_j * s.splits; }
 
 tide_status run_join(const Product& p, tide_stream_t stream) {
     if (p.splits == 1) return TIDE_OK;
@@ -954,7 +789,6 @@ tide_status check_workspace(void* ws, size_t have, int64_t need, const Extent* o
 
 // ---- forward -------------------------------------------------------------
 
-constexpr int64_t kGemvTokens = 4;
 struct ForwardPlan {
     bool gemv;
     Source x, w;
@@ -992,8 +826,7 @@ ForwardPlan plan_forward(const tide_linear_forward_args& a, void* ws) {
     ForwardPlan f;
     Carver c{static_cast<char*>(ws)};
     const int64_t T = a.tokens, N = a.out_features, K = a.in_features;
-    // any alignment, but whole checkpoint blocks need the tiles' epilogue
-    f.gemv = T <= kGemvTokens && K >= 8 && !a.z_kept;
+    f.gemv = forward_by_rows(T, K, a.z_kept != nullptr);
     f.bytes = 0;
     if (f.gemv) return f;
     f.x = {a.x, a.ldx, T, K};
@@ -1136,18 +969,10 @@ BackwardPlan plan_backward(const tide_linear_backward_args& a, void* ws) {
     if (a.dbias && b.chunks != 1) b.sums = c.take<float>(b.chunks * N);
     b.w = {a.weight, K, a.dx && T ? N : 0, K};
     b.w.plan(c);
-    double in_us = 0.0, w_us = 0.0;
-    b.w_shape = choose(kGradWeight, K, N, T, &w_us);
-    b.in_shape = choose(kGradInput, K, T, b.width, &in_us);
-    const bool both = a.dx && a.dweight && T && N && K;
-    // Both in one launch where together they are at most two workgroups a
-    // compute unit; then a short contraction is cheaper whole than split and
-    // joined (a join is 5 us, a step of 64 0.6)
-    b.pair = both && b.in_shape.bi == 128 && b.w_shape.bi == 128 && b.w_shape.bj == 128 &&
-             b.w_shape.splits == 1 && grid_of(b.in_shape) + grid_of(b.w_shape) <= 2 * kCus;
-    if (b.pair && b.width <= 1024) set_split(&b.in_shape, K, T, b.width, 1);
-    if (both && !b.pair && in_us > 0.0 && w_us > 0.0)
-        b.pair = choose_pair(T, b.width, K, in_us + w_us, &b.in_shape, &b.w_shape);
+    const Gradients g = choose_gradients(T, N, K, a.dx && T && N && K, a.dweight && T && N && K);
+    b.in_shape = g.in;
+    b.w_shape = g.weight;
+    b.pair = g.pair;
     // the 256-wide tiles read x from here, widened (tile_product.h)
     if (a.dweight && N && b.w_shape.bi == 256) b.x = c.take<uint16_t>(T * act8_pitch(K));
     int64_t floats = 0;
