@@ -895,6 +895,7 @@ namespace {
 struct BackwardPlan {
     bool make_dz;       // dz is written (to the workspace), not dy itself
     bool pair = false;  // dx and dW share a launch
+    bool in_first = false;
     int64_t width;      // of dz's rows there
     int dz_lanes;
     int64_t dz_groups, chunk, chunks;
@@ -973,6 +974,7 @@ BackwardPlan plan_backward(const tide_linear_backward_args& a, void* ws) {
     b.in_shape = g.in;
     b.w_shape = g.weight;
     b.pair = g.pair;
+    b.in_first = g.in_first;
     // the 256-wide tiles read x from here, widened (tile_product.h)
     if (a.dweight && N && b.w_shape.bi == 256) b.x = c.take<uint16_t>(T * act8_pitch(K));
     int64_t floats = 0;
@@ -1065,7 +1067,7 @@ extern "C" tide_status tide_linear_backward(const tide_linear_backward_args* arg
         set_shape(&x, b.in_shape, b.partial);
         const int64_t n_w = grid_of(b.w_shape), n_x = grid_of(b.in_shape);
         if (b.w_shape.bi == 256) {
-            const bool x_first = b.in_shape.split_depth >= b.w_shape.split_depth;
+            const bool x_first = b.in_first;
             auto wide = b.w_shape.bj == 256
                             ? b.in_shape.bj == 256 ? wide_pair_kernel<256, 256> : wide_pair_kernel<256, 192>
                             : b.in_shape.bj == 256 ? wide_pair_kernel<192, 256> : wide_pair_kernel<192, 192>;

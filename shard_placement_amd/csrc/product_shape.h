@@ -33,11 +33,19 @@ inline void set_split(Shape* s, int64_t I, int64_t J, int64_t depth, int64_t spl
     s->splits = (int32_t)std::max<int64_t>(1, ceil_div(units, each));
 }
 
-// What a tile costs, in microseconds, measured at K = 8192: a step of 64
-// contraction elements when a quarter of the compute units have one (`step`)
-// and what it takes longer when all have (`power`: the clock falls), and the
-// rest of a tile's life (first loads, epilogue).  Of the last, two sets of
-// waves take a step each in that time.
+// The steps of 64 contraction elements that a tile runs: the split's, or the
+// contraction's where that ends first.
+inline int64_t steps_of(const Shape& s, int64_t depth) {
+    return ceil_div(std::min(depth, s.split_depth), 64);
+}
+
+// What a tile costs, in microseconds: a step when a quarter of the compute units
+// have one (`step`) and what it takes longer when all have (`power`: the clock
+// falls), measured at K = 8192; and the rest of a tile's life (first loads,
+// epilogue; of the 128-wide ones as 2 to 16 steps show it in all three layouts:
+// 300 x 1024 x 1024 forward, dx and dW 12.3, 12.3 and 8.9 us with two sets of
+// waves, 14.8, 13.9 and 9.3 with one).  Of the last tile, two sets of waves take
+// a step each in that time.
 struct TileCost {
     int bi, bj, halves;
     double step, power, rest;
@@ -45,21 +53,26 @@ struct TileCost {
 constexpr TileCost kTiles[] = {{256, 256, 1, 1.25, 0.30, 7.0},
                                {256, 192, 1, 0.95, 0.36, 6.0},
                                {256, 128, 1, 0.72, 0.33, 5.0},
-                               {128, 128, 1, 0.60, 0.00, 4.0},
-                               {128, 128, 2, 1.10, 0.00, 4.3}};
+                               {128, 128, 1, 0.60, 0.00, 4.6},
+                               {128, 128, 2, 1.10, 0.00, 4.2}};
 // Two 128 x 128 tiles on a compute unit take a step each in this time.
 constexpr double kPairStep = 0.95;
 constexpr int kCus = 256;
 
 // A tile of 256 rows, with `used` of the compute units at work.
-inline double wide_tile_us(const TileCost& c, const Shape& s, double used) {
-    return (double)(s.split_depth / 64) * (c.step + c.power * used * used) + c.rest;
+inline double wide_tile_us(const TileCost& c, double steps, double used) {
+    return steps * (c.step + c.power * used * used) + c.rest;
 }
 
-inline double product_us(const TileCost& c, const Shape& s, int64_t I, int64_t J) {
+// 256-wide tiles of dW read x widened to bf16, which is a launch of its own
+// before them: 3 bytes an element at 5.5 MB/us.
+inline double widen_us(int64_t T, int64_t K) { return 4.0 + 3.0 * (double)T * (double)K / 5.5e6; }
+
+inline double product_us(Kind kind, const TileCost& c, const Shape& s, int64_t I, int64_t J,
+                         int64_t depth) {
     const int64_t groups = (int64_t)s.tiles_i * s.tiles_j * s.splits;
     const double rounds = (double)ceil_div(groups, kCus);
-    const double steps = (double)(s.split_depth / 64);
+    const double steps = (double)steps_of(s, depth);
     double us;
     if (c.halves == 2) {
         us = rounds * (std::ceil(steps / 2) * c.step + c.rest);
@@ -67,7 +80,8 @@ inline double product_us(const TileCost& c, const Shape& s, int64_t I, int64_t J
         const double pairs = (double)(int64_t)(rounds / 2), single = rounds - 2 * pairs;
         us = pairs * (steps * kPairStep + c.rest) + single * (steps * c.step + c.rest);
     } else {
-        us = rounds * wide_tile_us(c, s, (double)groups / (rounds * kCus));
+        us = rounds * wide_tile_us(c, steps, (double)groups / (rounds * kCus));
+        if (kind == kGradWeight) us += widen_us(depth, I);
     }
     // partial sums: a compute unit writes 40 KB/us, the join is a launch of its
     // own and reads 5.5 MB/us
@@ -118,7 +132,7 @@ inline Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth, double* esti
             t.halves = c.halves;
             set_split(&t, I, J, depth, splits);
             if (t.splits < splits) break;  // the contraction has no more units
-            const double us = product_us(c, t, I, J);
+            const double us = product_us(kind, c, t, I, J, depth);
             if (best == 0.0 || us < best) {
                 best = us;
                 s = t;
@@ -136,7 +150,8 @@ inline Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth, double* esti
 // (Measured, both gradients with dz, against two launches: 2048 x 13824 x 5120
 // 496 us, 600; 8192 x 8192 x 1024 272, 331; 3000 x 1280 x 8192 129, 141; and 748
 // against 729 for 700 x 28672 x 8192, whose estimates were 0.7% apart.)
-inline bool choose_pair(int64_t T, int64_t N, int64_t K, double best, Shape* in, Shape* weight) {
+inline bool choose_pair(int64_t T, int64_t N, int64_t K, double best, Shape* in, Shape* weight,
+                        bool* in_first) {
     constexpr int kWide = 2;  // 256 x 256 and 256 x 192
     bool found = false;
     best *= 0.97;
@@ -147,13 +162,14 @@ inline bool choose_pair(int64_t T, int64_t N, int64_t K, double best, Shape* in,
             set_split(&x, K, T, N, 1);
             set_split(&w, K, N, T, 1);
             const int64_t nx = (int64_t)x.tiles_i * x.tiles_j, nw = (int64_t)w.tiles_i * w.tiles_j;
-            const double tx = wide_tile_us(cx, x, 1.0), tw = wide_tile_us(cw, w, 1.0);
+            const double tx = wide_tile_us(cx, (double)steps_of(x, N), 1.0),
+                         tw = wide_tile_us(cw, (double)steps_of(w, T), 1.0);
             const double longer = std::max(tx, tw), shorter = std::min(tx, tw);
             const int64_t n_long = tx >= tw ? nx : nw;
             int64_t n_short = nx + nw - n_long;
             // whole rounds of the longer; then the shorter beside the rest of
             // them, and on the whole chip behind them
-            double us = (double)(n_long / kCus) * longer;
+            double us = widen_us(T, K) + (double)(n_long / kCus) * longer;
             const int64_t rest = n_long % kCus;
             if (rest) {
                 us += longer;
@@ -164,6 +180,7 @@ inline bool choose_pair(int64_t T, int64_t N, int64_t K, double best, Shape* in,
                 best = us;
                 *in = x;
                 *weight = w;
+                *in_first = tx >= tw;
                 found = true;
             }
         }
@@ -185,11 +202,12 @@ inline bool forward_by_rows(int64_t T, int64_t K, bool keep) {
 struct Gradients {
     Shape in, weight;
     bool pair;
+    bool in_first;  // of 256-wide tiles in one launch: dx's are the longer ones
 };
 
 inline Gradients choose_gradients(int64_t T, int64_t N, int64_t K, bool dx, bool dw) {
     const int64_t width = round_up(N, 8);
-    Gradients g;
+    Gradients g = {};
     double in_us = 0.0, w_us = 0.0;
     g.weight = choose(kGradWeight, K, N, T, &w_us);
     g.in = choose(kGradInput, K, T, width, &in_us);
@@ -200,7 +218,7 @@ inline Gradients choose_gradients(int64_t T, int64_t N, int64_t K, bool dx, bool
              g.weight.splits == 1 && grid_of(g.in) + grid_of(g.weight) <= 2 * kCus;
     if (g.pair && width <= 1024) set_split(&g.in, K, T, width, 1);
     if (dx && dw && !g.pair && in_us > 0.0 && w_us > 0.0)
-        g.pair = choose_pair(T, width, K, in_us + w_us, &g.in, &g.weight);
+        g.pair = choose_pair(T, width, K, in_us + w_us, &g.in, &g.weight, &g.in_first);
     return g;
 }
 

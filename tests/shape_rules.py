@@ -26,18 +26,20 @@ double choose_of(int kind, long long I, long long J, long long depth, long long*
 int by_rows(long long T, long long K, int keep) {
     return forward_by_rows(T, K, keep != 0);
 }
-int gradients_of(long long T, long long N, long long K, int dx, int dw, long long* in, long long* weight) {
+int gradients_of(long long T, long long N, long long K, int dx, int dw, long long* in, long long* weight,
+                 int* in_first) {
     const Gradients g = choose_gradients(T, N, K, dx != 0, dw != 0);
     put(g.in, in);
     put(g.weight, weight);
+    *in_first = g.in_first;
     return g.pair;
 }
 int tiles() { return (int)(sizeof(kTiles) / sizeof(kTiles[0])); }
-double estimate(int tile, long long I, long long J, long long depth, long long splits, long long* o) {
+double estimate(int kind, int tile, long long I, long long J, long long depth, long long splits, long long* o) {
     Shape s = {kTiles[tile].bi, kTiles[tile].bj, 64, kTiles[tile].halves, 0, 0, 1, 0};
     set_split(&s, I, J, depth, splits);
     put(s, o);
-    return product_us(kTiles[tile], s, I, J);
+    return product_us((Kind)kind, kTiles[tile], s, I, J, depth);
 }
 }
 """
@@ -60,8 +62,9 @@ def lib():
         ll, out = ctypes.c_longlong, ctypes.POINTER(ctypes.c_longlong)
         L.choose_of.argtypes, L.choose_of.restype = [ctypes.c_int, ll, ll, ll, out], ctypes.c_double
         L.by_rows.argtypes = [ll, ll, ctypes.c_int]
-        L.gradients_of.argtypes = [ll, ll, ll, ctypes.c_int, ctypes.c_int, out, out]
-        L.estimate.argtypes = [ctypes.c_int, ll, ll, ll, ll, out]
+        L.gradients_of.argtypes = [ll, ll, ll, ctypes.c_int, ctypes.c_int, out, out,
+                                   ctypes.POINTER(ctypes.c_int)]
+        L.estimate.argtypes = [ctypes.c_int, ctypes.c_int, ll, ll, ll, ll, out]
         L.estimate.restype = ctypes.c_double
         _lib = L
     return _lib
@@ -78,17 +81,18 @@ def choose(kind, I, J, depth):
     return Shape(*o), us
 
 
-def estimate(tile, I, J, depth, splits):
+def estimate(kind, tile, I, J, depth, splits):
     o = _out()
-    us = lib().estimate(tile, I, J, depth, splits, o)
+    us = lib().estimate(kind, tile, I, J, depth, splits, o)
     return Shape(*o), us
 
 
 def gradients(T, N, K, dx=True, dw=True):
-    """(dx's Shape, dW's, whether they share a launch)."""
-    a, b = _out(), _out()
-    pair = lib().gradients_of(T, N, K, dx, dw, a, b)
-    return Shape(*a), Shape(*b), bool(pair)
+    """(dx's Shape, dW's, whether they share a launch, whether dx's tiles come
+    first in one of 256-wide tiles)."""
+    a, b, first = _out(), _out(), ctypes.c_int(0)
+    pair = lib().gradients_of(T, N, K, dx, dw, a, b, ctypes.byref(first))
+    return Shape(*a), Shape(*b), bool(pair), bool(first.value)
 
 
 def round8(n):

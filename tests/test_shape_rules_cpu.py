@@ -39,3 +39,38 @@ def test_few_tokens_go_by_the_weights_rows():
 def test_one_gradient_alone_is_no_pair(T, N, K):
     for dx, dw in ((True, False), (False, True), (False, False)):
         assert not rules.gradients(T, N, K, dx, dw)[2]
+
+
+@pytest.mark.parametrize("tile", range(5))
+def test_estimates_count_the_steps_that_run(tile):
+    """A contraction that ends inside its split has fewer steps than the split;
+    whole splits have all of theirs."""
+    us = {d: rules.estimate(rules.GRAD_INPUT, tile, 512, 512, d, 1)[1] for d in (64, 65, 128, 129, 256, 257, 320, 512)}
+    pair = rules.estimate(rules.GRAD_INPUT, tile, 512, 512, 64, 1)[0].halves  # two sets of waves take two steps at once
+    step = (us[512] - us[256]) / 4
+    for d, v in us.items():
+        steps = -(-d // (64 * pair)) * pair
+        assert abs(v - (us[512] - (8 - steps) * step)) < 1e-9, (d, v)
+
+
+def test_the_longer_tiles_of_a_joint_launch_come_first():
+    """dx's tiles run ceil(N / 64) steps and dW's ceil(T / 64): with tiles of one
+    kind the longer contraction is first, also where both round up to the same
+    split."""
+    seen = set()
+    for T in range(1400, 2400, 47):
+        for N, K in ((T - 120, 9000), (T + 100, 9000), (T // 2, 12000)):
+            x, w, pair, first = rules.gradients(T, N, K)
+            if pair and x.bi == 256 and x.bj == w.bj:
+                assert first == (-(-N // 64) >= -(-T // 64)), (T, N, K)
+                seen.add((first, x.split_depth == w.split_depth))
+    assert len(seen) >= 2, seen
+
+
+@pytest.mark.parametrize("tile", range(5))
+def test_wide_tiles_of_dw_pay_for_widening_x(tile):
+    """Tiles of 256 columns read x widened in a launch before them; the others
+    widen it on the way."""
+    s, dx = rules.estimate(rules.GRAD_INPUT, tile, 5120, 4096, 2048, 1)
+    _, dw = rules.estimate(rules.GRAD_WEIGHT, tile, 5120, 4096, 2048, 1)
+    assert abs(dw - dx - (4 + 3 * 5120 * 2048 / 5.5e6 if s.bi == 256 else 0)) < 1e-9
