@@ -84,10 +84,11 @@ inline double product_us(Kind kind, const TileCost& c, const Shape& s, int64_t I
         if (kind == kGradWeight) us += widen_us(depth, I);
     }
     // partial sums: a compute unit writes 40 KB/us, the join is a launch of its
-    // own and reads 5.5 MB/us
+    // own and reads 5.5 MB/us (dx of 128 x 1024 x 5120 takes 15.4 us in four
+    // splits, 13.1 whole)
     if (s.splits > 1)
         us += rounds * 4.0 * c.bi * c.bj / 40e3 +
-              3.0 + 4.0 * (double)s.splits * (double)I * (double)J / 5.5e6;
+              4.0 + 4.0 * (double)s.splits * (double)I * (double)J / 5.5e6;
     return us;
 }
 
@@ -104,7 +105,9 @@ inline double product_us(Kind kind, const TileCost& c, const Shape& s, int64_t I
 // itself is worked on by two sets of waves, half the contraction each, which
 // keeps twice the loads in flight: forward of 1024 x 1024 x 1024 12.5 us, with
 // one set 15.2; 2048 x 2048 x 5120 50, 60; 1500 x 1500 x 3000 takes one set and
-// three splits, two workgroups a compute unit, 32 (with two sets 39).
+// three splits, two workgroups a compute unit, 32 (with two sets 39).  Every
+// number of splits up to 16 is looked at: 77 x 768 x 8192 forward takes 16, 13.8
+// us, with 8 15.2; 493 x 81 x 3904 16, 11.5, with 4 14.2.
 inline Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth, double* estimate = nullptr) {
     Shape s = {};
     s.bk = 64;
@@ -123,15 +126,17 @@ inline Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth, double* esti
         if (s.bj > 16 && depth > 512 && depth <= 1024 && s.tiles_i <= kCus) s.halves = 2;
         return s;
     }
+    const int64_t most = std::min<int64_t>(16, std::max<int64_t>(1, ceil_div(depth, kSplitUnit)));
     double best = 0.0;
     for (const TileCost& c : kTiles) {
-        for (int64_t splits = 1; splits <= 16; ++splits) {
+        for (int64_t splits = 1; splits <= most; ++splits) {
             Shape t = s;
             t.bi = c.bi;
             t.bj = c.bj;
             t.halves = c.halves;
             set_split(&t, I, J, depth, splits);
-            if (t.splits < splits) break;  // the contraction has no more units
+            // a split takes whole units, so fewer splits may do, which had their turn
+            if (t.splits < splits) continue;
             const double us = product_us(kind, c, t, I, J, depth);
             if (best == 0.0 || us < best) {
                 best = us;
@@ -212,11 +217,23 @@ inline Gradients choose_gradients(int64_t T, int64_t N, int64_t K, bool dx, bool
     g.weight = choose(kGradWeight, K, N, T, &w_us);
     g.in = choose(kGradInput, K, T, width, &in_us);
     // Both in one launch where together they are at most two workgroups a
-    // compute unit; then a short contraction is cheaper whole than split and
-    // joined (a join is 5 us, a step of 64 0.6)
-    g.pair = dx && dw && g.in.bi == 128 && g.weight.bi == 128 && g.weight.bj == 128 &&
-             g.weight.splits == 1 && grid_of(g.in) + grid_of(g.weight) <= 2 * kCus;
-    if (g.pair && width <= 1024) set_split(&g.in, K, T, width, 1);
+    // compute unit, dx with half as many splits if need be (94 x 2560 x 2248: 20.5
+    // us, in two launches 29.0); then a short contraction is cheaper whole than
+    // split and joined (a join is 5 us, a step of 64 0.6), and half as many splits
+    // that leave each workgroup a compute unit to itself are better than all of
+    // them (212 x 2560 x 912: 18.8 us, 21.4).
+    if (dx && dw && g.in.bi == 128 && g.weight.bi == 128 && g.weight.bj == 128 && g.weight.splits == 1) {
+        Shape in = g.in;
+        auto fit = [&](int64_t groups) {
+            const int64_t most = (groups - grid_of(g.weight)) / ((int64_t)in.tiles_i * in.tiles_j);
+            if (most < in.splits && 2 * most >= in.splits) set_split(&in, K, T, width, most);
+        };
+        fit(2 * kCus);
+        g.pair = grid_of(in) + grid_of(g.weight) <= 2 * kCus;
+        if (width <= 1024) set_split(&in, K, T, width, 1);
+        fit(kCus);
+        if (g.pair) g.in = in;
+    }
     if (dx && dw && !g.pair && in_us > 0.0 && w_us > 0.0)
         g.pair = choose_pair(T, width, K, in_us + w_us, &g.in, &g.weight, &g.in_first);
     return g;

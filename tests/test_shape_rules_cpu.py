@@ -74,3 +74,34 @@ def test_wide_tiles_of_dw_pay_for_widening_x(tile):
     s, dx = rules.estimate(rules.GRAD_INPUT, tile, 5120, 4096, 2048, 1)
     _, dw = rules.estimate(rules.GRAD_WEIGHT, tile, 5120, 4096, 2048, 1)
     assert abs(dw - dx - (4 + 3 * 5120 * 2048 / 5.5e6 if s.bi == 256 else 0)) < 1e-9
+
+
+def test_no_split_is_passed_over():
+    """The choice is the least estimate of every tile with every number of splits
+    up to 16 that the contraction divides into."""
+    off = []
+    for kind, I, J, depth in drawn(2500, 2):
+        if J <= 64:
+            continue
+        _, us = rules.choose(kind, I, J, depth)
+        for tile in range(rules.lib().tiles()):
+            for splits in range(1, 17):
+                s, est = rules.estimate(kind, tile, I, J, depth, splits)
+                if s.tiles_i * s.tiles_j >= 4 * CUS and splits > 1:
+                    break  # tiles enough without
+                if est < us * (1 - 1e-9):
+                    off.append((kind, I, J, depth, s, est, us))
+    assert not off, off[:3]
+
+
+@pytest.mark.parametrize("I,J,depth,splits", [(768, 77, 8192, 16), (1024, 128, 5120, 10), (81, 493, 3904, 16)])
+def test_few_tiles_are_split_far(I, J, depth, splits):
+    """Splits that lie behind a number that the contraction does not divide into."""
+    assert rules.choose(rules.FORWARD, I, J, rules.round8(depth))[0].splits == splits
+
+
+@pytest.mark.parametrize("T,N,K,splits", [(94, 2560, 2248, 5), (212, 2560, 912, 5), (1027, 19840, 242, 10)])
+def test_dx_gives_up_splits_for_a_joint_launch(T, N, K, splits):
+    x, w, pair, _ = rules.gradients(T, N, K)
+    assert pair and x.splits == splits and w.splits == 1
+    assert rules.choose(rules.GRAD_INPUT, K, T, rules.round8(N))[0].splits > splits
