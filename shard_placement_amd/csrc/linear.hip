@@ -826,7 +826,8 @@ ForwardPlan plan_forward(const tide_linear_forward_args& a, void* ws) {
     ForwardPlan f;
     Carver c{static_cast<char*>(ws)};
     const int64_t T = a.tokens, N = a.out_features, K = a.in_features;
-    f.gemv = forward_by_rows(T, K, a.z_kept != nullptr);
+    f.gemv = forward_by_rows(T, N, K, a.z_kept != nullptr,
+                             direct(a.x, a.ldx, T, K) && direct(a.weight, K, N, K));
     f.bytes = 0;
     if (f.gemv) return f;
     f.x = {a.x, a.ldx, T, K};

@@ -195,11 +195,23 @@ inline bool choose_pair(int64_t T, int64_t N, int64_t K, double best, Shape* in,
 
 inline int64_t grid_of(const Shape& s) { return (int64_t)s.tiles_i * s.tiles_j * s.splits; }
 
-// The forward product of up to 4 tokens whose z is not kept (whole checkpoint
-// blocks need the tiles' epilogue) goes by the weight's rows: gemv_kernel.
-constexpr int64_t kGemvTokens = 4;
-inline bool forward_by_rows(int64_t T, int64_t K, bool keep) {
-    return T <= kGemvTokens && K >= 8 && !keep;
+// Whether a forward product goes by the weight's rows (gemv_kernel) instead of
+// tiles: up to 4 tokens, z not kept (whole checkpoint blocks need the tiles'
+// epilogue).  direct: x and W can be read where they lie; otherwise tiles need a
+// copy of W (4 x 4096 x 1001: 11.7 us by rows, 21.2).  Read in place, with
+// weights that come from memory (us by rows / in tiles, N x K):
+//   1 token   512 x 512 4.1 / 4.8, 1024 x 8192 8.0 / 10.5, 28672 x 8192 73.9 / 78.3
+//   2         256 x 512 5.9 / 4.8, 256 x 1024 6.0 / 7.0, 256 x 8192 9.2 / 8.6,
+//             1024 x 8192 9.9 / 11.4, 4096 x 4096 11.0 / 12.0
+//   4         256 x 8192 13.3 / 9.2, 1024 x 8192 14.0 / 12.0, 4096 x 4096 14.5 / 12.3,
+//             28672 x 4096 52.9 / 61.5, 28672 x 28672 258 / 278
+// (rows: 32 multiply-adds for 16 bytes of W at 4 tokens, which only the largest
+// weights' bytes hide; tiles: a second launch where the contraction is split).
+inline bool forward_by_rows(int64_t T, int64_t N, int64_t K, bool keep, bool direct) {
+    if (T > 4 || K < 8 || keep) return false;
+    if (T == 1 || !direct) return true;
+    if (T == 2) return K > 512 && (K <= 1024 || N >= 512);
+    return N * K > ((int64_t)96 << 20);
 }
 
 // The gradients' products: dx [T, K] with N (rounded up to 8) terms, dW [N, K]

@@ -23,8 +23,8 @@ double choose_of(int kind, long long I, long long J, long long depth, long long*
     put(choose((Kind)kind, I, J, depth, &us), o);
     return us;
 }
-int by_rows(long long T, long long K, int keep) {
-    return forward_by_rows(T, K, keep != 0);
+int by_rows(long long T, long long N, long long K, int keep, int direct) {
+    return forward_by_rows(T, N, K, keep != 0, direct != 0);
 }
 int gradients_of(long long T, long long N, long long K, int dx, int dw, long long* in, long long* weight,
                  int* in_first) {
@@ -61,7 +61,7 @@ def lib():
             L = ctypes.CDLL(so)
         ll, out = ctypes.c_longlong, ctypes.POINTER(ctypes.c_longlong)
         L.choose_of.argtypes, L.choose_of.restype = [ctypes.c_int, ll, ll, ll, out], ctypes.c_double
-        L.by_rows.argtypes = [ll, ll, ctypes.c_int]
+        L.by_rows.argtypes = [ll, ll, ll, ctypes.c_int, ctypes.c_int]
         L.gradients_of.argtypes = [ll, ll, ll, ctypes.c_int, ctypes.c_int, out, out,
                                    ctypes.POINTER(ctypes.c_int)]
         L.estimate.argtypes = [ctypes.c_int, ctypes.c_int, ll, ll, ll, ll, out]
@@ -100,7 +100,8 @@ def round8(n):
 
 
 def forward(T, N, K, keep=False):
-    """The forward product's Shape, or None where it goes by the weight's rows."""
-    if lib().by_rows(T, K, keep):
+    """The forward product's Shape, or None where it goes by the weight's rows
+    (x and W contiguous and starting on 16 bytes)."""
+    if lib().by_rows(T, N, K, keep, K % 8 == 0):
         return None
     return choose(FORWARD, N, T, round8(K))[0]

@@ -70,3 +70,23 @@ def test_slope_of_a_value_that_reads_back_as_infinity(act, T):
     keep = torch.ones(T, N, dtype=torch.bool, device=DEV)
     keep[2] = False
     assert dx[keep].isfinite().all() and db[[4, 40]].isfinite().all()
+
+
+# Two to four tokens on both sides of the rule that sends them by the weight's
+# rows or through tiles: widths that are no multiples of 8, narrow and wide
+# weights, short and long contractions, a weight of more than 192 MB.
+@pytest.mark.parametrize("T,N,K", [(2, 33, 512), (2, 511, 2048), (2, 513, 2048), (2, 40, 1024), (2, 33, 1001),
+                                   (3, 33, 1001), (3, 300, 4096), (4, 1030, 520), (4, 256, 28672),
+                                   (4, 33, 20), (3, 12291, 8200), (4, 12291, 8200)])
+@pytest.mark.parametrize("act,bias,res", [("none", False, False), ("gelu", True, True)])
+def test_forward_of_two_to_four_tokens(T, N, K, act, bias, res):
+    g = gen(T + N + K)
+    x, w = normal(g, T, K), normal(g, N, K, scale=2 / math.sqrt(K))
+    b = normal(g, N) if bias else None
+    r = normal(g, T, N) if res else None
+    want, _, _, bound = ref.forward_ref(x, w, b, r, act)
+    within(Linear(w, bias=b, act=act).forward(x, residual=r), want, bound, "y")
+    if N < 2000:  # rows of x that start anywhere
+        xs = torch.full((T, K + 3), math.nan, dtype=BF, device=DEV)[:, 1:K + 1]
+        xs.copy_(x)
+        within(Linear(w, bias=b, act=act).forward(xs, residual=r), want, bound, "y of strided x")

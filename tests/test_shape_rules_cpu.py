@@ -29,10 +29,16 @@ def test_every_choice_covers_the_product():
 
 
 def test_few_tokens_go_by_the_weights_rows():
-    assert rules.forward(1, 28672, 8192) is None and rules.forward(4, 9, 8) is None
-    assert rules.forward(5, 28672, 8192) is not None
-    assert rules.forward(1, 28672, 8192, keep=True) is not None
-    assert rules.forward(1, 8, 7) is not None
+    """One token, weights that tiles would copy, and, up to four tokens, those
+    whose bytes hide the arithmetic; kept z and short rows go by tiles."""
+    by_rows = lambda *a, **kw: rules.forward(*a, **kw) is None  # noqa: E731
+    assert all(by_rows(1, N, K) for N in (1, 64, 28672) for K in (8, 512, 28672))
+    assert all(by_rows(T, 64, 1001) for T in (1, 2, 3, 4))
+    assert by_rows(2, 512, 8192) and by_rows(2, 64, 1024) and by_rows(4, 28672, 4096)
+    for case in ((2, 256, 512), (2, 256, 8192), (3, 1024, 8192), (4, 4096, 4096), (4, 256, 28672),
+                 (5, 28672, 8192), (5, 64, 1001), (1, 8, 7)):
+        assert not by_rows(*case), case
+    assert not by_rows(1, 28672, 8192, keep=True)
 
 
 @pytest.mark.parametrize("T,N,K", [(77, 768, 2048), (2048, 13824, 5120), (8, 5120, 5120), (300, 1024, 1024)])
