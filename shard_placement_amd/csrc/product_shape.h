@@ -116,14 +116,22 @@ inline Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth, double* esti
         s.bi = 128;
         s.bj = J <= 16 ? 16 : J <= 32 ? 32 : 64;
         if (kind == kForward && s.bj <= 32 && I * depth > ((int64_t)128 << 20)) s.bk = 256;
-        // a contraction of up to 1024 is over before a join would be
-        const int64_t want = depth <= 1024 ? 1 : s.bk == 256 ? kCus : 2 * kCus;
-        set_split(&s, I, J, depth, want / std::max<int64_t>(1, ceil_div(I, s.bi)));
-        // 28672 x 1024: 15.1 us and 40 rows, with one set of waves 16.5; with
-        // more tiles than compute units more of the smaller workgroups fit
-        // (65536 x 1024 and 40 rows: 23.8, with two sets 29.5), and up to 16
-        // rows or 512 elements there is nothing to gain
-        if (s.bj > 16 && depth > 512 && depth <= 1024 && s.tiles_i <= kCus) s.halves = 2;
+        const int64_t want = s.bk == 256 ? kCus : 2 * kCus;
+        int64_t splits = want / std::max<int64_t>(1, ceil_div(I, s.bi));
+        // a contraction of up to 1024 is over before a join would be, and up to
+        // 2048 two sets of waves do what two splits would, without one (us with two
+        // sets / in two splits for forward, dx and dW of 28672 outputs a row, 40
+        // rows: depth 1032 17.8 / 22.9, 15.8 / 20.4, 13.3 / 20.1; depth 2048 31.0 /
+        // 30.4, 29.7 / 29.4, 20.2 / 23.2; depth 4096 65.5 / 62.9, 52.9 / 50.5, 49.0 / 42.7)
+        const bool sets = s.bj > 16 && s.bk == 64;
+        if (depth <= 1024 || (sets && depth <= 2048 && splits == 2)) splits = 1;
+        set_split(&s, I, J, depth, splits);
+        // one set of waves where more of the smaller workgroups fit (65536 x 1024
+        // and 40 rows: 23.8 us, with two sets 29.5); up to 16 rows or 512 elements
+        // there is nothing to gain from two.  40 rows, depth 1024, 768 and 5120
+        // outputs a row: forward 9.1 and 9.2 (one set 10.5 and 10.6), dx 9.0 and
+        // 9.4 (9.9 and 11.2), dW 10.6 and 10.8 (12.9 and 13.0)
+        if (sets && s.splits == 1 && depth > 512 && s.tiles_i <= kCus) s.halves = 2;
         return s;
     }
     const int64_t most = std::min<int64_t>(16, std::max<int64_t>(1, ceil_div(depth, kSplitUnit)));

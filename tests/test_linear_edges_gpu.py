@@ -8,7 +8,7 @@ import torch
 
 from shard_placement_amd.linear import Act8, Linear
 from tests import linear_ref as ref
-from tests.test_linear_gpu import BF, DEV, kept_of, normal, gen, within
+from tests.test_linear_gpu import BF, DEV, gen, kept_of, normal, test_forward as check_forward, within
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,19 @@ def test_forward_of_two_to_four_tokens(T, N, K, act, bias, res):
         xs = torch.full((T, K + 3), math.nan, dtype=BF, device=DEV)[:, 1:K + 1]
         xs.copy_(x)
         within(Linear(w, bias=b, act=act).forward(xs, residual=r), want, bound, "y of strided x")
+
+
+@pytest.mark.parametrize("rows,cols,depth", [(40, 22030, 1291), (20, 28673, 2048), (64, 22000, 1030)])
+def test_narrow_tiles_by_two_sets_of_waves(rows, cols, depth):
+    """Forward, dx and dW with few rows of outputs, whole, in two halves of a
+    contraction whose steps are odd in number or end inside."""
+    check_forward(rows, cols, depth, "silu", True, True, True)
+    g = gen(rows)
+    for T, N, K in ((rows, depth, cols), (depth, rows, cols)):
+        w, dy = normal(g, N, K, scale=1 / math.sqrt(K)), normal(g, T, N, scale=1e-3)
+        x8, x = kept_of(torch.randn(T, K, generator=g, device=DEV))
+        want = ref.backward_ref(dy, w, x, None, "none")
+        within(Linear(w).backward(dy), *want["dx"], "dx")
+        layer = Linear(w, weight_grad=torch.full_like(w, 9))
+        layer.backward(dy, x=x8, input_grad=False)
+        within(layer.weight_grad, *want["dw"], "dw")

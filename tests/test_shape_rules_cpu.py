@@ -111,3 +111,17 @@ def test_dx_gives_up_splits_for_a_joint_launch(T, N, K, splits):
     x, w, pair, _ = rules.gradients(T, N, K)
     assert pair and x.splits == splits and w.splits == 1
     assert rules.choose(rules.GRAD_INPUT, K, T, rules.round8(N))[0].splits > splits
+
+
+@pytest.mark.parametrize("kind", [rules.FORWARD, rules.GRAD_INPUT, rules.GRAD_WEIGHT])
+def test_narrow_tiles_take_two_sets_of_waves_before_two_splits(kind):
+    """Up to 2048 elements of contraction where the rule would split in two; above
+    it splits, and more than two splits stay splits."""
+    for depth, splits, halves in ((512, 1, 1), (520, 1, 2), (1024, 1, 2), (1032, 1, 2), (2048, 1, 2),
+                                  (2056, 2, 1), (4096, 2, 1)):
+        for J in (17, 40, 64):
+            s, _ = rules.choose(kind, 28672, J, depth)
+            assert (s.splits, s.halves) == (splits, halves), (depth, J, s)
+    assert rules.choose(kind, 28672, 16, 1032)[0].splits == 2  # its tiles have one set
+    assert rules.choose(kind, 5120, 40, 1280)[0].splits == 5
+    assert rules.choose(kind, 65536, 40, 1024)[0].halves == 1
