@@ -105,3 +105,22 @@ def forward(T, N, K, keep=False):
     if lib().by_rows(T, N, K, keep, K % 8 == 0):
         return None
     return choose(FORWARD, N, T, round8(K))[0]
+
+
+def forms(T, N, K):
+    """The launches that a forward product (z kept or not) and both gradients
+    together and alone take: kernel form, and whether the contraction is split."""
+    name = lambda s: (s.bi, s.bj, s.bk, s.halves, s.splits > 1)  # noqa: E731
+    out = set()
+    for keep in (False, True):
+        s = forward(T, N, K, keep)
+        out.add(("forward by rows", min(T, 3)) if s is None else ("forward",) + name(s))
+    x, w, pair, first = gradients(T, N, K)
+    if pair and w.bi == 256:
+        out.add(("both, wide", x.bj, w.bj, "dx first" if first else "dW first"))
+    elif pair:
+        groups = x.tiles_i * x.tiles_j * x.splits + w.tiles_i * w.tiles_j
+        out.add(("both", x.bj, 2 if groups <= 256 else 1, x.splits > 1))
+    out.add(("dx",) + name(gradients(T, N, K, dw=False)[0]))
+    out.add(("dW",) + name(gradients(T, N, K, dx=False)[1]))
+    return out

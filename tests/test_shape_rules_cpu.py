@@ -125,3 +125,23 @@ def test_narrow_tiles_take_two_sets_of_waves_before_two_splits(kind):
     assert rules.choose(kind, 28672, 16, 1032)[0].splits == 2  # its tiles have one set
     assert rules.choose(kind, 5120, 40, 1280)[0].splits == 5
     assert rules.choose(kind, 65536, 40, 1024)[0].halves == 1
+
+
+def test_every_launch_is_tested():
+    """No launch that random sizes take is missing from the GPU tests' lists."""
+    from tests.test_linear_forms_gpu import FORMS, PAST_THE_CACHE
+    from tests.test_linear_gpu import PAIRS, PRODUCTS, TILES
+
+    covered = set().union(*(rules.forms(*s) for s in TILES + PAIRS + PRODUCTS + FORMS))
+    covered |= {f for s in PAST_THE_CACHE for f in rules.forms(*s) if f[0] == "forward"}
+    rng = random.Random(7)
+    size = lambda hi: int(round(hi ** rng.random()))  # noqa: E731
+    missing = {}
+    for _ in range(60000):
+        s = (size(16384), size(30000), size(30000))
+        for f in rules.forms(*s) - covered:
+            missing.setdefault(f, s)
+    assert not missing, missing
+    # both gradients in one launch of 256-wide tiles: each width of each, each order
+    assert {("both, wide", a, b, c) for a in (192, 256) for b in (192, 256)
+            for c in ("dx first", "dW first")} <= covered
