@@ -240,10 +240,8 @@ __device__ __forceinline__ void product_tile(const Product& p, uint32_t block, u
     tile_at(p, block, blocks, &ti, &tj, &sp);
     const int64_t i0 = (int64_t)ti * BI, j0 = (int64_t)tj * BJ;
     f32x4v acc[TI][TJ];
-#ifdef __HIP_DEVICE_COMPILE__  // the host's pass fails to instantiate it twice
     tile_loop<BI, BJ, K, WI, WJ, CA, CB, H>(p.A, p.B, p.depth, sp * p.split_depth,
                                             min(p.depth, (sp + 1) * p.split_depth), i0, j0, lds, acc);
-#endif
 
     // The accumulators pass through LDS, 16 rows of a wave at a time, so that
     // each lane ends with 8 consecutive columns and a row's stores are whole

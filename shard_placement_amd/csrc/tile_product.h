@@ -78,10 +78,20 @@ __device__ __forceinline__ constexpr int column_swizzle(int k) {
     return ((k & 3) | ((k >> 1) & 4)) & (kPairs % 8 == 0 ? 7 : kPairs % 4 == 0 ? 3 : kPairs - 1);
 }
 
+// 16 bytes a lane from memory to LDS, contiguous over the wave there.  (The
+// compiler's host pass checks the size against the host's features, not
+// gfx950's, takes 16 for an error and the functions that use it for unusable.)
+constexpr int kNonTemporal = 2;
+template <int AUX>
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, TIDE_LDS char* lds,
+                                            uint32_t offset) {
+#ifdef __HIP_DEVICE_COMPILE__
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds, 16, offset, 0, 0, AUX);
+#endif
+}
+
 // A tile of N indices and K contraction elements from `first` on, staged by
 // WAVES waves.  ONCE: no other workgroup reads the operand's elements.
-constexpr int kNonTemporal = 2;
-
 template <int N, int K, int WAVES, bool COLUMNS, bool ONCE = false>
 struct Stager {
     static constexpr int kBytes = N * K * 2;
@@ -140,8 +150,7 @@ struct Stager {
         for (int q = 0; q < kMine; ++q) {
             const int load = q * WAVES + wave;
             if (kLoads % WAVES && load >= kLoads) break;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                r, lds + load * 1024, 16, none ? kNowhere : offset[q], 0, 0, ONCE ? kNonTemporal : 0);
+            load_to_lds<ONCE ? kNonTemporal : 0>(r, lds + load * 1024, none ? kNowhere : offset[q]);
         }
         base += step;
         left -= step;
