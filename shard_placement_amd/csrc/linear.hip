@@ -513,6 +513,12 @@ __global__ __launch_bounds__(kPadThreads) void pad_kernel(const uint16_t* in, in
 // row, and has the loads of kDzRows rows in flight; the quarters' sums meet in
 // LDS.  (2048 x 13824 with relu: 29 us, 4.9 TB/s; 33 without
 // the quarters, two waves a SIMD.)
+//
+// The rounding is the matrix instructions': they take bf16.  It makes dx and dW
+// off by 2.3e-3 of themselves, root mean square, where the one rounding of their
+// own leaves 1.7e-3.  dz in two bf16 parts would keep it and double the products'
+// work (2048 x 13824 x 5120: 387 us at the least); dbias, which needs no product,
+// sums dz before it.
 constexpr int kDzLanes = 256;    // of 8 columns
 constexpr int kDzQuarters = 4;
 constexpr int kDzRows = 4;

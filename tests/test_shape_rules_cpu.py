@@ -145,3 +145,23 @@ def test_every_launch_is_tested():
     # both gradients in one launch of 256-wide tiles: each width of each, each order
     assert {("both, wide", a, b, c) for a in (192, 256) for b in (192, 256)
             for c in ("dx first", "dW first")} <= covered
+
+
+def test_grids_fit_at_the_limits():
+    """A grid's threads are counted in 32 bits: with the most tokens, features and
+    elements a product may have, every choice's grid fits."""
+    elements = 1 << 33
+    for kind in range(3):
+        for I in [1 << k for k in range(0, 23)] + [3, 100, 129, (1 << 22) - 1]:
+            for J in [1 << k for k in range(0, 31)] + [(1 << 30) - 1]:
+                if kind == rules.GRAD_WEIGHT and J > 1 << 22 or I * J > elements:
+                    continue
+                for depth in (8, 64, 4096, 1 << 22):
+                    if max(I, J) * depth > elements:
+                        continue
+                    s, _ = rules.choose(kind, I, J, depth)
+                    threads = 512 if s.bi == 256 else 256 * s.halves
+                    assert s.tiles_i * s.tiles_j * s.splits * threads < 1 << 32, (kind, I, J, depth, s)
+                    if s.splits > 1:  # the join's
+                        pitch = -(-I // 32) * 32
+                        assert J * pitch // 8 < 1 << 32, (kind, I, J, depth, s)
