@@ -349,7 +349,7 @@ __global__ __launch_bounds__(256 * H) void pair_kernel(Product w, Product x, int
 // The same with 256-wide tiles, one workgroup a compute unit, the product of the
 // longer tiles first: where its tiles do not fill whole rounds of the chip the
 // other's fill the gaps (2048 x 13824 x 5120: 160 tiles of dx of 342 us and 1080 of
-// dW of 57 on 256 compute units, 445 us for both, 570 one after the other).
+// dW of 57 on 256 compute units, 460 us for both, 570 one after the other).
 template <int BJW, int BJX>
 __global__ __launch_bounds__(512, 2) void wide_pair_kernel(Product w, Product x, int32_t first_w,
                                                            int32_t first_x) {
