@@ -48,7 +48,7 @@ __device__ __forceinline__ float sigmoid(float u) {
 // gelu is a bf16 rounding off in its far negative tail too, where a formula of
 // small absolute error is percents off.  A library erff took 55 us in the
 // gradient of 2048 x 13824 elements, which reads and writes 141 MB, where this
-// takes 40; a forward of 4096 x 16384 x 1024 with gelu takes 157 us, 154 with
+// takes 39; a forward of 4096 x 16384 x 1024 with gelu takes 157 us, 154 with
 // a shorter polynomial of small absolute error, 2% off at z = -10.
 __device__ __forceinline__ float normal_cdf(float z, float* bell) {
     const float g = __builtin_amdgcn_exp2f(-0.5f * kLog2E * (z * z));

@@ -20,6 +20,10 @@ weight's goes to ``weight_grad`` and never to ``weight.grad``, and activations
 that require a gradient are refused in grad mode.  In a
 ``torch.autograd.Function`` grad mode is off, so its forward and backward can
 call these as they are.
+
+``stream`` (default: the current one of the tensors' device) is a stream of
+that device.  What a call allocates belongs to it; the caller orders it against
+other streams and keeps the tensors alive until its work is done.
 """
 from __future__ import annotations
 
