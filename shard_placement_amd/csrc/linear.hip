@@ -641,18 +641,6 @@ __global__ __launch_bounds__(64 * kDbWaves) void dbias_kernel(const float* sums,
 
 // ---- host ----------------------------------------------------------------
 
-// The workspace's pieces, handed out in order, each on 256 bytes.
-struct Carver {
-    char* base;
-    int64_t used = 0;
-    template <typename T>
-    T* take(int64_t count) {
-        T* p = base ? reinterpret_cast<T*>(base + used) : nullptr;
-        used += round_up(count * (int64_t)sizeof(T), 256);
-        return p;
-    }
-};
-
 int64_t partial_floats(const Shape& s, int64_t I, int64_t J) {
     return s.splits > 1 ? s.splits * J * round_up(I, kActBlock) : 0;
 }
@@ -757,39 +745,6 @@ tide_status check_dims(int64_t T, int64_t N, int64_t K, int32_t act, int32_t res
         return TIDE_EUNSUPPORTED;
     return TIDE_OK;
 }
-
-tide_status check_kept(const void* p, int64_t rows, int64_t cols) {
-    if (rows == 0 || cols == 0) return TIDE_OK;
-    if (!p) return TIDE_EINVAL;
-    return reinterpret_cast<uintptr_t>(p) % 16 ? TIDE_EALIGN : TIDE_OK;
-}
-
-// No output shares a byte with an input or another output.
-tide_status check_apart(const Extent* in, int n_in, const Extent* out, int n_out) {
-    for (int a = 0; a < n_out; ++a) {
-        for (int b = 0; b < n_in; ++b)
-            if (overlaps(out[a], in[b])) return TIDE_EOVERLAP;
-        for (int b = 0; b < a; ++b)
-            if (overlaps(out[a], out[b])) return TIDE_EOVERLAP;
-    }
-    return TIDE_OK;
-}
-
-tide_status check_workspace(void* ws, size_t have, int64_t need, const Extent* other, int n) {
-    if (need == 0) return TIDE_OK;
-    if (!ws || have < (size_t)need) return TIDE_ENOSPACE;
-    if (reinterpret_cast<uintptr_t>(ws) % 16) return TIDE_EALIGN;
-    const Extent e = bytes_extent(ws, need);
-    for (int k = 0; k < n; ++k)
-        if (overlaps(e, other[k])) return TIDE_EOVERLAP;
-    return TIDE_OK;
-}
-
-#define TIDE_TRY(call)                                \
-    do {                                              \
-        const tide_status try_st = (call);            \
-        if (try_st != TIDE_OK) return try_st;         \
-    } while (0)
 
 // ---- forward -------------------------------------------------------------
 

@@ -1,10 +1,12 @@
-// linear_check.h -- argument checks and launches shared by the checkpoint
-// calls (act8.hip) and the layer products (linear.hip).  Host code only.
+// linear_check.h -- argument checks, workspaces and launches shared by the
+// checkpoint calls (act8.hip), the layer products (linear.hip) and the norms
+// (norm.hip).  Host code only.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "product_shape.h"
 #include "tide.h"
 
 namespace tide {
@@ -72,6 +74,51 @@ inline tide_status check_stream_device(tide_stream_t stream) {
         return TIDE_EHIP;
     return sdev == dev ? TIDE_OK : TIDE_EINVAL;
 }
+
+inline tide_status check_kept(const void* p, int64_t rows, int64_t cols) {
+    if (rows == 0 || cols == 0) return TIDE_OK;
+    if (!p) return TIDE_EINVAL;
+    return reinterpret_cast<uintptr_t>(p) % 16 ? TIDE_EALIGN : TIDE_OK;
+}
+
+// No output shares a byte with an input or another output.
+inline tide_status check_apart(const Extent* in, int n_in, const Extent* out, int n_out) {
+    for (int a = 0; a < n_out; ++a) {
+        for (int b = 0; b < n_in; ++b)
+            if (overlaps(out[a], in[b])) return TIDE_EOVERLAP;
+        for (int b = 0; b < a; ++b)
+            if (overlaps(out[a], out[b])) return TIDE_EOVERLAP;
+    }
+    return TIDE_OK;
+}
+
+inline tide_status check_workspace(void* ws, size_t have, int64_t need, const Extent* other, int n) {
+    if (need == 0) return TIDE_OK;
+    if (!ws || have < (size_t)need) return TIDE_ENOSPACE;
+    if (reinterpret_cast<uintptr_t>(ws) % 16) return TIDE_EALIGN;
+    const Extent e = bytes_extent(ws, need);
+    for (int k = 0; k < n; ++k)
+        if (overlaps(e, other[k])) return TIDE_EOVERLAP;
+    return TIDE_OK;
+}
+
+#define TIDE_TRY(call)                                \
+    do {                                              \
+        const tide_status try_st = (call);            \
+        if (try_st != TIDE_OK) return try_st;         \
+    } while (0)
+
+// The workspace's pieces, handed out in order, each on 256 bytes.
+struct Carver {
+    char* base;
+    int64_t used = 0;
+    template <typename T>
+    T* take(int64_t count) {
+        T* p = base ? reinterpret_cast<T*>(base + used) : nullptr;
+        used += round_up(count * (int64_t)sizeof(T), 256);
+        return p;
+    }
+};
 
 template <typename... P, typename... A>
 tide_status launch_lds(void (*kernel)(P...), int64_t grid, int threads, unsigned lds_bytes,
