@@ -578,6 +578,81 @@ tide_status tide_linear_backward_workspace(const tide_linear_backward_args *args
 tide_status tide_linear_backward(const tide_linear_backward_args *args, void *workspace,
                                  size_t workspace_bytes, tide_stream_t stream);
 
+/* The norm in front of a layer's products, and its gradients.
+ *
+ * forward:  for each row of x [T, C]: n = (x - mu) / sqrt(v + eps), y = n weight
+ *           + bias, with mu the row's mean and v the mean of (x - mu)^2
+ *           (TIDE_NORM_LAYER), or mu = 0 and v the mean of x^2
+ *           (TIDE_NORM_RMS).  x, y, weight [C] and bias [C] are bf16, the
+ *           statistics and the result are in binary32 and y is rounded once.
+ *           x_kept and y_kept, where given, receive the checkpoints of x (what
+ *           tide_act8_pack writes; the backward pass takes it) and of y (in 8
+ *           bits straight from binary32; what the next product's weight
+ *           gradient takes).
+ * backward: with c = dy weight, dx = (c - mean(c) - n mean(c n)) / sqrt(v + eps)
+ *           + add (without mean(c) for TIDE_NORM_RMS), dweight = the sum of
+ *           dy n over the rows, dbias = the sum of dy.  x comes in bf16 or as
+ *           its checkpoint stands for it (one of x and x_kept is NULL), and its
+ *           statistics are worked out again.  add (or NULL) is the gradient
+ *           that reaches x past the norm: a residual stream's.  dx [T, C],
+ *           dweight [C] and dbias [C] are bf16, rounded once from binary32;
+ *           dweight and dbias are what tide_rs_bf16_to_fp32 reads as a rank's
+ *           gradients.  Each of the three may be NULL (not computed), and so
+ *           may what only they need (weight for dx; x for dx and dweight).
+ *
+ * Squares and their sums have to stay within binary32: a row whose sum of
+ * squares does not (|x| of 10^17 and more) is divided by infinity.  A row with a
+ * NaN or, but for the finite elements of TIDE_NORM_RMS (0), an infinity is NaN.
+ * eps is finite and at least 1e-30 (TIDE_EINVAL otherwise).
+ *
+ * Rows of x, y, dy, dx and add lie ld* elements apart (>= C, any 2-byte
+ * alignment).  Outputs may overlap no input and no other output
+ * (TIDE_EOVERLAP), but dx may be add itself (same address and lddx = ldadd).
+ * T at most 2^27; C at most 32768; T C at most 2^33; every ld at most 2^22
+ * (TIDE_EUNSUPPORTED).  T or C may be 0: empty sums are 0, and outputs without
+ * elements are not touched.
+ * Workspace, stream and order of sums as for the layer products; the forward
+ * call needs no workspace. */
+#define TIDE_NORM_RMS 0
+#define TIDE_NORM_LAYER 1
+
+typedef struct tide_norm_forward_args {
+    int64_t rows, cols; /* T, C */
+    int32_t kind;       /* TIDE_NORM_* */
+    float eps;
+    const void *x;
+    int64_t ldx;
+    const void *weight;
+    const void *bias; /* or NULL */
+    void *y;
+    int64_t ldy;
+    void *x_kept; /* or NULL */
+    void *y_kept; /* or NULL */
+} tide_norm_forward_args;
+
+typedef struct tide_norm_backward_args {
+    int64_t rows, cols; /* T, C */
+    int32_t kind;       /* TIDE_NORM_* */
+    float eps;
+    const void *dy;
+    int64_t lddy;
+    const void *x; /* or NULL: x_kept */
+    int64_t ldx;
+    const void *x_kept; /* or NULL: x */
+    const void *weight;
+    const void *add; /* or NULL */
+    int64_t ldadd;
+    void *dx; /* or NULL */
+    int64_t lddx;
+    void *dweight; /* or NULL */
+    void *dbias;   /* or NULL */
+} tide_norm_backward_args;
+
+tide_status tide_norm_forward(const tide_norm_forward_args *args, tide_stream_t stream);
+tide_status tide_norm_backward_workspace(const tide_norm_backward_args *args, size_t *bytes);
+tide_status tide_norm_backward(const tide_norm_backward_args *args, void *workspace,
+                               size_t workspace_bytes, tide_stream_t stream);
+
 /* Static text for a status code. */
 const char *tide_status_str(int32_t status);
 

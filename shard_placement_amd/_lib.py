@@ -31,7 +31,8 @@ EXPORTS = ("tide_abi_version", "tide_status_str", "tide_desc_size", "tide_desc_g
            "tide_pipeline_destroy", "tide_rs_two_phase_noalloc", "tide_rs_bf16_to_fp32_trace",
            "tide_rs_bf16_to_fp32_streams", "tide_act8_bytes", "tide_act8_pack", "tide_act8_unpack",
            "tide_linear_forward_workspace", "tide_linear_forward",
-           "tide_linear_backward_workspace", "tide_linear_backward")
+           "tide_linear_backward_workspace", "tide_linear_backward", "tide_norm_forward",
+           "tide_norm_backward_workspace", "tide_norm_backward")
 
 
 class TideShape(ctypes.Structure):
@@ -70,6 +71,22 @@ class TideLinearBackwardArgs(ctypes.Structure):
                 ("weight", ctypes.c_void_p), ("x_kept", ctypes.c_void_p),
                 ("z_kept", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64),
                 ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p)]
+
+
+class TideNormForwardArgs(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("kind", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("ldy", ctypes.c_int64), ("x_kept", ctypes.c_void_p), ("y_kept", ctypes.c_void_p)]
+
+
+class TideNormBackwardArgs(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("kind", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_kept", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("add", ctypes.c_void_p), ("ldadd", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dweight", ctypes.c_void_p),
+                ("dbias", ctypes.c_void_p)]
 
 
 class TideError(RuntimeError):
@@ -147,6 +164,10 @@ def lib():
     L.tide_linear_forward.argtypes = [fwd, vp, ctypes.c_size_t, vp]
     L.tide_linear_backward_workspace.argtypes = [bwd, sizep]
     L.tide_linear_backward.argtypes = [bwd, vp, ctypes.c_size_t, vp]
+    fwd, bwd = ctypes.POINTER(TideNormForwardArgs), ctypes.POINTER(TideNormBackwardArgs)
+    L.tide_norm_forward.argtypes = [fwd, vp]
+    L.tide_norm_backward_workspace.argtypes = [bwd, sizep]
+    L.tide_norm_backward.argtypes = [bwd, vp, ctypes.c_size_t, vp]
     for name in ("tide_desc_size", "tide_desc_geometry", "tide_desc_build", "tide_plan_query",
                  "tide_rs_bf16_to_fp32", "tide_ag_place", "tide_ag_place_sdma",
                  "tide_stream_create_cu_limited", "tide_stream_destroy",
@@ -159,7 +180,8 @@ def lib():
                  "tide_rs_bf16_to_fp32_trace", "tide_rs_bf16_to_fp32_streams",
                  "tide_act8_bytes", "tide_act8_pack", "tide_act8_unpack",
                  "tide_linear_forward_workspace", "tide_linear_forward",
-                 "tide_linear_backward_workspace", "tide_linear_backward"):
+                 "tide_linear_backward_workspace", "tide_linear_backward", "tide_norm_forward",
+                 "tide_norm_backward_workspace", "tide_norm_backward"):
         getattr(L, name).restype = ctypes.c_int
     if L.tide_abi_version() != 2:
         raise RuntimeError("libtide ABI version %d, expected 2" % L.tide_abi_version())

@@ -21,11 +21,13 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._lib import (TideError, TideLinearBackwardArgs, TideLinearForwardArgs, TideOpts,
-                   TidePlanInfo, TideShape, check)
+from ._lib import (TideError, TideLinearBackwardArgs, TideLinearForwardArgs,
+                   TideNormBackwardArgs, TideNormForwardArgs, TideOpts, TidePlanInfo, TideShape,
+                   check)
 
 ORDERS = {"fixed": 0, "tree": 1}
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+NORMS = {"rms": 0, "layer": 1}
 
 
 def _shapes(shapes: Sequence[Sequence[int]]):
@@ -531,6 +533,91 @@ def tide_linear_backward(dy: torch.Tensor, in_features: int, weight=None, x_kept
     if dbias is not None:
         a.dbias = _whole(dbias, (N,), "dbias", index)
     return _on_device(index, stream, _backward_on, a, dx, index)
+
+
+def _norm_kind(kind: str) -> int:
+    if kind not in NORMS:
+        raise TideError(-1, "kind is %r, expected one of %s" % (kind, ", ".join(NORMS)))
+    return NORMS[kind]
+
+
+def _norm_forward_on(s, a, y, index):
+    if y is None:
+        y = torch.empty(a.rows, a.cols, dtype=torch.bfloat16, device=index)
+        a.y, a.ldy = y.data_ptr(), a.cols
+    check(_lib.lib().tide_norm_forward(ctypes.byref(a), s), "tide_norm_forward")
+    return y
+
+
+def tide_norm_forward(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor = None, bias=None,
+                      kind: str = "rms", eps: float = 1e-6, x_kept=None, y_kept=None,
+                      stream=None) -> torch.Tensor:
+    """y = (x - mean) / sqrt(var + eps) weight + bias for each row ("layer"), or
+    with mean 0 and the mean square ("rms"); x_kept and y_kept (uint8), where
+    given, receive the checkpoints of x and y.  Returns y (allocated when not
+    given).  Nothing is recorded by autograd (tide_norm_backward is the
+    gradient): x and y may not require one in grad mode."""
+    index = _index(x, "x")
+    _no_graph(x, "x")
+    T, C = x.shape
+    px, ldx = _rows(x, "x")
+    a = TideNormForwardArgs(T, C, _norm_kind(kind), eps, px, ldx, _whole(weight, (C,), "weight", index))
+    if bias is not None:
+        a.bias = _whole(bias, (C,), "bias", index)
+    if y is not None:
+        a.y, a.ldy = _matrix(y, T, C, "y", index)
+    if x_kept is not None:
+        a.x_kept = _kept(x_kept, T, C, "x_kept", index)
+    if y_kept is not None:
+        a.y_kept = _kept(y_kept, T, C, "y_kept", index)
+    return _on_device(index, stream, _norm_forward_on, a, y, index)
+
+
+def _norm_backward_on(s, a, dx, index):
+    if dx is True:
+        dx = torch.empty(a.rows, a.cols, dtype=torch.bfloat16, device=index)
+        a.dx, a.lddx = dx.data_ptr(), a.cols
+    L = _lib.lib()
+    ws, ptr, n = _workspace(L.tide_norm_backward_workspace, a, index)
+    check(L.tide_norm_backward(ctypes.byref(a), ptr, n, s), "tide_norm_backward")
+    return dx
+
+
+def tide_norm_backward(dy: torch.Tensor, x=None, x_kept=None, weight=None, kind: str = "rms",
+                       eps: float = 1e-6, add=None, dx=None, dweight=None, dbias=None,
+                       stream=None):
+    """The gradients that are given, from x in bf16 or its checkpoint x_kept: dx
+    (plus ``add``), dweight = the sum of dy n over the rows, n the normalised x,
+    dbias = the sum of dy.  dx=True allocates it; dx may be add itself.  Returns
+    dx."""
+    index = _index(dy, "dy")
+    _no_graph(dy, "dy")
+    T, C = dy.shape
+    pdy, lddy = _rows(dy, "dy")
+    a = TideNormBackwardArgs(T, C, _norm_kind(kind), eps, pdy, lddy)
+    if x is not None:
+        a.x, a.ldx = _matrix(x, T, C, "x", index)
+    if x_kept is not None:
+        if x is not None:
+            raise TideError(-1, "x and x_kept are given: one of them is what forward read")
+        a.x_kept = _kept(x_kept, T, C, "x_kept", index)
+    if x is None and x_kept is None and not (dx is None and dweight is None):
+        raise TideError(-1, "dx and dweight need x or its checkpoint")
+    if dx is not None:
+        if weight is None:
+            raise TideError(-1, "dx needs the weight")
+        a.weight = _whole(weight, (C,), "weight", index)
+        if add is not None:
+            a.add, a.ldadd = _matrix(add, T, C, "add", index)
+        if dx is not True:
+            a.dx, a.lddx = _matrix(dx, T, C, "dx", index)
+    elif add is not None:
+        raise TideError(-1, "add is added to dx, which is not asked for")
+    if dweight is not None:
+        a.dweight = _whole(dweight, (C,), "dweight", index)
+    if dbias is not None:
+        a.dbias = _whole(dbias, (C,), "dbias", index)
+    return _on_device(index, stream, _norm_backward_on, a, dx, index)
 
 
 class Plan:

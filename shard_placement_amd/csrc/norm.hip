@@ -1,0 +1,719 @@
+// norm.hip -- rms and layer norm of a matrix's rows, with the 8-bit checkpoints
+// of its input and output, and their gradients, for gfx950.
+//
+//   forward   n = (x - mu) r, y = n w + b; mu the row's mean (rms: 0),
+//             r = 1 / sqrt(mean of (x - mu)^2 + eps)
+//   backward  c = dy w, dx = r (c - mean(c) - n mean(c n)) + add (rms: without
+//             mean(c)); dw = the sum of dy n over the rows, db = the sum of dy
+//
+// w is a full tensor as the all-gather placement writes it, dw and db are
+// gradients as the reduce-scatter reads them.
+//
+// Memory bounds both directions: a row is read once, kept in registers as it
+// lies in memory, and its statistics and results are worked out from there.
+// The backward pass works mu and r out again from x (or from its checkpoint)
+// instead of keeping them: the row is in registers anyway.
+//
+// A row belongs to a group of L lanes: 16 or 64 lanes of a wave for narrow
+// rows, a workgroup of 256 to 1024 for wide ones; a lane owns U units of 8
+// consecutive columns, L units apart, so every access is contiguous over the
+// wave and the 4 lanes of a quad hold a checkpoint block.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "act8.h"
+#include "bf16_io.h"
+#include "linear_check.h"
+#include "tide.h"
+
+using namespace tide;
+
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) float lds_float;
+
+constexpr int kThreads = 256;  // of a workgroup whose rows take fewer lanes
+
+// ---- sums over a row's lanes -------------------------------------------------
+
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+    const int moved = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true);
+    return v + __builtin_bit_cast(float, moved);
+}
+
+// The sum over N <= 16 consecutive lanes, in all of them: pairs, pairs of pairs,
+// then the mirrored half and the mirrored whole.
+template <int N>
+__device__ __forceinline__ float sum_lanes(float v) {
+    v = add_dpp<0xB1>(v);
+    v = add_dpp<0x4E>(v);
+    if constexpr (N >= 8) v = add_dpp<0x141>(v);
+    if constexpr (N >= 16) v = add_dpp<0x140>(v);
+    return v;
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+__device__ __forceinline__ float sum64(float v) {
+    v = sum_lanes<16>(v);
+    return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
+
+// N sums over the L lanes of a row, in all of them, always added in the same
+// order.  L > 64: `box` holds N * L / 64 floats that no wave still reads.
+template <int L, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], lds_float* box) {
+    if constexpr (L == 16) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = sum_lanes<16>(v[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = sum64(v[k]);
+    }
+    if constexpr (L > 64) {
+        constexpr int kWaves = L / 64;
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) box[k * kWaves + (threadIdx.x >> 6)] = v[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            v[k] = sum_lanes<kWaves>(box[k * kWaves + (threadIdx.x & (kWaves - 1))]);
+    }
+}
+
+// ---- a lane's part of a row --------------------------------------------------
+
+// The columns of a lane's unit u of L lanes, and how many of them exist.
+template <int L>
+__device__ __forceinline__ int32_t column(int u) {
+    return (int32_t)((threadIdx.x % L + u * L) * 8);
+}
+
+// Eight elements from column c of a row of `cols`; those that do not exist are 0.
+__device__ __forceinline__ u32x4v load_unit(const uint16_t* row, int32_t c, int32_t cols) {
+    u32x4v w = 0;
+    if (c + 8 <= cols) {
+        w = load8_raw(row + c);
+    } else if (c < cols) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (c + k < cols)
+                w[k / 2] |= (uint32_t) * (const TIDE_GLOBAL_AS uint16_t*)(row + c + k) << (k % 2 * 16);
+    }
+    return w;
+}
+
+// The same of a row that is read once.
+__device__ __forceinline__ u32x4v load_unit_once(const uint16_t* row, int32_t c, int32_t cols) {
+    return c + 8 <= cols ? load8_raw<true>(row + c) : load_unit(row, c, cols);
+}
+
+// The units as they lie in memory are what stays in registers between the
+// passes over a row: without this the compiler keeps their widened elements,
+// twice the registers (one of 8 workgroups fits where two would).
+template <int U>
+__device__ __forceinline__ void forget(u32x4v (&w)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) asm volatile("" : "+v"(w[u]));
+}
+
+// v - mu where the element exists, else 0.
+__device__ __forceinline__ void centre(float (&v)[8], float mu, int32_t c, int32_t cols) {
+    if (c + 8 <= cols) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] -= mu;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = c + k < cols ? v[k] - mu : 0.0f;
+    }
+}
+
+// A mean worked out in binary32 is off by a few steps of the mean, which a row of
+// nearly equal values would see: what is left of the mean after it was taken
+// off (`off`, a sum of small numbers) is taken off as well.
+__device__ __forceinline__ float variance(float mean_square, float off) {
+    return fmaxf(__builtin_fmaf(-off, off, mean_square), 0.0f * mean_square);
+}
+
+// Within one step of 1 / sqrt(v).
+__device__ __forceinline__ float inv_sqrt(float v) { return __builtin_amdgcn_rsqf(v); }
+
+// ---- forward -------------------------------------------------------------------
+
+struct NormForward {
+    const uint16_t* x;
+    int64_t ldx, rows;
+    int32_t cols;
+    float eps, inv_cols;
+    const uint16_t *w, *b;
+    uint16_t* y;
+    int64_t ldy;
+    uint8_t *x_kept, *y_kept;
+};
+
+__device__ __forceinline__ void keep(uint8_t* kept, int64_t rows, int64_t row, int32_t c,
+                                     int64_t pitch, float (&v)[8]) {
+    u32x2 q;
+    const int e = act8_pack8(v, &q);
+    const int64_t at = row * pitch + c;
+    __builtin_nontemporal_store(q, (TIDE_GLOBAL_AS u32x2*)(kept + at));
+    if (c % kActBlock == 0)
+        *(TIDE_GLOBAL_AS uint8_t*)(kept + rows * pitch + at / kActBlock) = (uint8_t)(e + 127);
+}
+
+template <int L, int U, bool LAYER>
+__global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_forward_kernel(NormForward p) {
+    __shared__ float box[L > 64 ? 3 * (L / 64) : 1];
+    constexpr int kRows = (L > kThreads ? L : kThreads) / L;
+    const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / L;
+    if (row >= p.rows) return;  // the whole group of lanes; L > 64: never
+    const uint16_t* from = p.x + row * p.ldx;
+    u32x4v raw[U], w[U], b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u] = load_unit_once(from, column<L>(u), p.cols);
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = load_unit(p.w, column<L>(u), p.cols);
+    if (p.b) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) b[u] = load_unit(p.b, column<L>(u), p.cols);
+    }
+    float mu = 0.0f;
+    if constexpr (LAYER) {
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float v[8];
+            widen(raw[u], v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s[0] += v[k];
+        }
+        row_sums<L>(s, (lds_float*)box);
+        mu = s[0] * p.inv_cols;
+        forget(raw);
+    }
+    float s[LAYER ? 2 : 1] = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float v[8];
+        widen(raw[u], v);
+        if constexpr (LAYER) centre(v, mu, column<L>(u), p.cols);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            s[0] = __builtin_fmaf(v[k], v[k], s[0]);
+            if constexpr (LAYER) s[1] += v[k];
+        }
+    }
+    row_sums<L>(s, (lds_float*)box + (L > 64 ? L / 64 : 0));
+    forget(raw);
+    const float off = LAYER ? s[LAYER] * p.inv_cols : 0.0f;
+    const float r = inv_sqrt(variance(s[0] * p.inv_cols, off) + p.eps);
+    const int64_t pitch = act8_pitch(p.cols);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int32_t c = column<L>(u);
+        if (c >= pitch) break;  // the same in a quad, whose lanes pack together
+        float v[8], f[8], y[8];
+        widen(raw[u], v);
+        widen(w[u], f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = (LAYER ? v[k] - mu - off : v[k]) * r * f[k];
+        if (p.b) {
+            widen(b[u], f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] += f[k];
+        }
+        if (c < p.cols) store8(p.y + row * p.ldy + c, p.cols - c, y);
+        if (p.x_kept) keep(p.x_kept, p.rows, row, c, pitch, v);
+        if (p.y_kept) {
+            if (c + 8 > p.cols) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (c + k >= p.cols) y[k] = 0.0f;
+            }
+            keep(p.y_kept, p.rows, row, c, pitch, y);
+        }
+    }
+}
+
+// ---- backward ------------------------------------------------------------------
+
+struct NormBackward {
+    const uint16_t* dy;
+    int64_t lddy;
+    const uint16_t* x;
+    int64_t ldx;
+    const uint8_t* x_kept;
+    const uint16_t* w;
+    const uint16_t* add;
+    int64_t ldadd;
+    uint16_t* dx;
+    int64_t lddx;
+    float *dw_sums, *db_sums;   // [chunks][pitch], or NULL
+    uint16_t *dweight, *dbias;  // the one chunk's sums go there, or NULL
+    int64_t rows, chunk, sums_pitch;
+    int32_t cols;
+    float eps, inv_cols;
+};
+
+// What a lane reads of a row; of a kept x a unit is 8 bytes and its scale.
+template <int U>
+struct RowParts {
+    u32x4v dy[U], x[U], add[U];
+};
+
+template <int L, int U>
+__device__ __forceinline__ void load_row(const NormBackward& p, int64_t row, RowParts<U>& r) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) r.dy[u] = load_unit_once(p.dy + row * p.lddy, column<L>(u), p.cols);
+    if (p.x_kept) {
+        const int64_t pitch = act8_pitch(p.cols);
+        const uint8_t* scales = p.x_kept + p.rows * pitch;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int32_t c = column<L>(u);
+            const int64_t at = row * pitch + c;
+            r.x[u] = 0;
+            if (c < p.cols) {
+                const u32x2 q = __builtin_nontemporal_load((const TIDE_GLOBAL_AS u32x2*)(p.x_kept + at));
+                r.x[u].xy = q;
+                r.x[u].z = *(const TIDE_GLOBAL_AS uint8_t*)(scales + at / kActBlock);
+            }
+        }
+    } else if (p.x) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) r.x[u] = load_unit_once(p.x + row * p.ldx, column<L>(u), p.cols);
+    } else {  // db alone needs no x
+#pragma unroll
+        for (int u = 0; u < U; ++u) r.x[u] = 0;
+    }
+    if (p.add) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            r.add[u] = load_unit_once(p.add + row * p.ldadd, column<L>(u), p.cols);
+    }
+}
+
+__device__ __forceinline__ void x_values(u32x4v x, bool kept, float (&v)[8]) {
+    if (kept)
+        act8_unpack8(x.xy, act8_scale(x.z), v);
+    else
+        widen(x, v);
+}
+
+// A workgroup takes a chunk of rows, kRows of them at a time, and keeps its
+// columns' sums of dy n and (DB) of dy in registers; the next rows' loads are in
+// flight while these are worked on, but for rows of 1024 lanes, which have half
+// the registers (and read w again for each row).
+template <int L, int U, bool LAYER, bool DB>
+__global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_kernel(NormBackward p) {
+    constexpr int kGroup = L > kThreads ? L : kThreads, kRows = kGroup / L;
+    constexpr int kBox = L > 64 ? 4 * 3 * (L / 64) : 1;
+    constexpr int kSums = kRows > 1 ? (kRows - 1) * L * U * 8 : 1;
+    __shared__ __attribute__((aligned(16))) float lds[kBox > kSums ? kBox : kSums];
+    lds_float* box = (lds_float*)lds;
+    const bool kept = p.x_kept;
+    constexpr bool kAhead = L < 1024;
+    const int64_t end = min(p.rows, ((int64_t)blockIdx.x + 1) * p.chunk);
+    int64_t row = blockIdx.x * p.chunk + threadIdx.x / L;
+    u32x4v w[U];
+    auto load_w = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) w[u] = p.w ? load_unit(p.w, column<L>(u), p.cols) : (u32x4v)0u;
+    };
+    if (kAhead) load_w();
+    float dw[U][8] = {}, db[DB ? U : 1][8] = {};
+    RowParts<U> next;
+    if (kAhead && row < end) load_row<L, U>(p, row, next);
+    int slot = 0;
+#pragma unroll 1
+    for (; row < end; row += kRows) {
+        RowParts<U> now;
+        if constexpr (kAhead) {
+            now = next;
+            if (row + kRows < end) load_row<L, U>(p, row + kRows, next);
+        } else {
+            load_row<L, U>(p, row, now);
+            load_w();
+        }
+        // a slot is written again two rows later, with a barrier in between
+        lds_float* mine = box + (L > 64 ? slot * 6 * (L / 64) : 0);
+        slot ^= 1;
+        float mu = 0.0f, mean_c = 0.0f;
+        if constexpr (LAYER) {
+            float s[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float v[8], d[8], f[8];
+                x_values(now.x[u], kept, v);
+                widen(now.dy[u], d);
+                widen(w[u], f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    s[0] += v[k];
+                    s[1] = __builtin_fmaf(d[k], f[k], s[1]);
+                }
+            }
+            row_sums<L>(s, mine);
+            forget(now.x);
+            forget(now.dy);
+            forget(w);
+            mu = s[0] * p.inv_cols;
+            mean_c = s[1] * p.inv_cols;
+            mine += L > 64 ? 2 * (L / 64) : 0;
+        }
+        float s[LAYER ? 3 : 2] = {};
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float v[8], d[8], f[8];
+            x_values(now.x[u], kept, v);
+            if constexpr (LAYER) centre(v, mu, column<L>(u), p.cols);
+            widen(now.dy[u], d);
+            widen(w[u], f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                s[0] = __builtin_fmaf(v[k], v[k], s[0]);
+                s[1] = __builtin_fmaf(d[k] * f[k], v[k], s[1]);
+                if constexpr (LAYER) s[2] += v[k];
+            }
+        }
+        row_sums<L>(s, mine);
+        forget(now.x);
+        forget(now.dy);
+        forget(w);
+        const float off = LAYER ? s[LAYER ? 2 : 0] * p.inv_cols : 0.0f;
+        const float r = inv_sqrt(variance(s[0] * p.inv_cols, off) + p.eps);
+        // mean(c n) n = (r^2 mean(c (x - mu))) (x - mu)
+        const float along = r * (r * __builtin_fmaf(-off, mean_c, s[1] * p.inv_cols));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int32_t c = column<L>(u);
+            float v[8], d[8], f[8];
+            x_values(now.x[u], kept, v);
+            if constexpr (LAYER) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = v[k] - mu - off;
+            }
+            widen(now.dy[u], d);
+            if (p.dx && c < p.cols) {
+                float g[8];
+                widen(w[u], f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    g[k] = r * (__builtin_fmaf(-along, v[k], d[k] * f[k]) - mean_c);
+                if (p.add) {
+                    widen(now.add[u], f);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) g[k] += f[k];
+                }
+                store8(p.dx + row * p.lddx + c, p.cols - c, g);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dw[u][k] = __builtin_fmaf(d[k], v[k] * r, dw[u][k]);
+            if constexpr (DB) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) db[u][k] += d[k];
+            }
+        }
+    }
+    // the sums of the workgroup's other groups of lanes, then out
+    auto finish = [&](auto& sum, float* sums, uint16_t* out) __attribute__((always_inline)) {
+        if constexpr (kRows > 1) {
+            __syncthreads();
+            const int group = threadIdx.x / L, lane = threadIdx.x % L;
+            if (group) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        box[(((group - 1) * U + u) * 8 + k) * L + lane] = sum[u][k];
+            }
+            __syncthreads();
+            if (group) return;
+            for (int o = 0; o < kRows - 1; ++o)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) sum[u][k] += box[((o * U + u) * 8 + k) * L + lane];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int32_t c = column<L>(u);
+            if (c >= p.cols) break;
+            if (out) {
+                store8(out + c, p.cols - c, sum[u]);
+            } else {
+                float* to = sums + (int64_t)blockIdx.x * p.sums_pitch + c;
+#pragma unroll
+                for (int k = 0; k < 8; k += 4)
+                    *(TIDE_GLOBAL_AS f32x4*)(to + k) =
+                        f32x4{sum[u][k], sum[u][k + 1], sum[u][k + 2], sum[u][k + 3]};
+            }
+        }
+    };
+    if (p.dw_sums || p.dweight) finish(dw, p.dw_sums, p.dweight);
+    if constexpr (DB) finish(db, p.db_sums, p.dbias);
+}
+
+// dw and db from the chunks' sums, in the chunks' order within a wave and then
+// over the waves: a lane takes a column, the workgroup's waves every
+// kSumWaves-th chunk.
+constexpr int kSumWaves = 16;
+constexpr int kSumAhead = 8;  // chunks whose loads are in flight together
+
+__global__ __launch_bounds__(64 * kSumWaves) void norm_sums_kernel(const float* dw_sums,
+                                                                   const float* db_sums,
+                                                                   int64_t chunks, int64_t pitch,
+                                                                   int64_t cols, uint16_t* dweight,
+                                                                   uint16_t* dbias) {
+    __shared__ float part[kSumWaves][64];
+    const int64_t groups = (cols + 63) / 64;
+    const bool second = blockIdx.x >= groups || !dw_sums;
+    const float* sums = second ? db_sums : dw_sums;
+    uint16_t* out = second ? dbias : dweight;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t c = (blockIdx.x - (blockIdx.x >= groups ? groups : 0)) * 64 + lane;
+    float s = 0.0f;
+    if (c < cols) {
+        for (int64_t k = wave; k < chunks; k += kSumWaves * kSumAhead) {
+            float v[kSumAhead];
+#pragma unroll
+            for (int a = 0; a < kSumAhead; ++a) {
+                const int64_t at = k + a * kSumWaves;
+                v[a] = at < chunks ? *(const TIDE_GLOBAL_AS float*)(sums + at * pitch + c) : 0.0f;
+            }
+#pragma unroll
+            for (int a = 0; a < kSumAhead; ++a) s += v[a];
+        }
+    }
+    part[wave][lane] = s;
+    __syncthreads();
+    if (wave || c >= cols) return;
+#pragma unroll
+    for (int w = 1; w < kSumWaves; ++w) s += part[w][lane];
+    *(TIDE_GLOBAL_AS uint16_t*)(out + c) = to_bf16(s);
+}
+
+// ---- host ----------------------------------------------------------------------
+
+constexpr int64_t kMaxNormCols = 32768;  // 4096 units: 1024 lanes of 4
+constexpr int64_t kMaxNormRows = (int64_t)1 << 27;  // 16 lanes each in one grid
+constexpr float kMinEps = 1e-30f;
+
+// Lanes and units a row takes: the fewest lanes whose units hold it.
+struct RowShape {
+    int lanes, units;
+};
+
+using ForwardKernel = void (*)(NormForward);
+using BackwardKernel = void (*)(NormBackward);
+
+struct ForwardForm {
+    RowShape shape;
+    ForwardKernel rms, layer;
+};
+struct BackwardForm {
+    RowShape shape;
+    BackwardKernel rms, layer, rms_db, layer_db;
+};
+
+#define TIDE_FORWARD_FORM(L, U) \
+    {{L, U}, norm_forward_kernel<L, U, false>, norm_forward_kernel<L, U, true>}
+#define TIDE_BACKWARD_FORM(L, U)                                                    \
+    {{L, U}, norm_backward_kernel<L, U, false, false>, norm_backward_kernel<L, U, true, false>, \
+     norm_backward_kernel<L, U, false, true>, norm_backward_kernel<L, U, true, true>}
+
+const ForwardForm kForwardForms[] = {
+    TIDE_FORWARD_FORM(16, 1),  TIDE_FORWARD_FORM(64, 1),  TIDE_FORWARD_FORM(64, 2),
+    TIDE_FORWARD_FORM(256, 1), TIDE_FORWARD_FORM(256, 2), TIDE_FORWARD_FORM(256, 3),
+    TIDE_FORWARD_FORM(256, 4), TIDE_FORWARD_FORM(512, 3), TIDE_FORWARD_FORM(512, 4),
+    TIDE_FORWARD_FORM(1024, 3), TIDE_FORWARD_FORM(1024, 4)};
+const BackwardForm kBackwardForms[] = {
+    TIDE_BACKWARD_FORM(16, 1),  TIDE_BACKWARD_FORM(64, 1),  TIDE_BACKWARD_FORM(64, 2),
+    TIDE_BACKWARD_FORM(256, 1), TIDE_BACKWARD_FORM(256, 2), TIDE_BACKWARD_FORM(256, 3),
+    TIDE_BACKWARD_FORM(512, 2), TIDE_BACKWARD_FORM(512, 3), TIDE_BACKWARD_FORM(1024, 2),
+    TIDE_BACKWARD_FORM(1024, 3), TIDE_BACKWARD_FORM(1024, 4)};
+
+template <typename Form, size_t N>
+const Form& form_of(const Form (&forms)[N], int64_t cols) {
+    const int64_t units = act8_pitch(cols) / 8;
+    for (size_t k = 0; k + 1 < N; ++k)
+        if (forms[k].shape.lanes * forms[k].shape.units >= units) return forms[k];
+    return forms[N - 1];
+}
+
+int threads_of(const RowShape& s) { return s.lanes > kThreads ? s.lanes : kThreads; }
+
+tide_status check_norm(int64_t rows, int64_t cols, int32_t kind, float eps) {
+    if (rows < 0 || cols < 0 || (kind != TIDE_NORM_RMS && kind != TIDE_NORM_LAYER)) return TIDE_EINVAL;
+    if (!(eps >= kMinEps) || !std::isfinite(eps)) return TIDE_EINVAL;
+    if (rows > kMaxNormRows || cols > kMaxNormCols || rows * cols > kMaxElements)
+        return TIDE_EUNSUPPORTED;
+    return TIDE_OK;
+}
+
+}  // namespace
+
+extern "C" tide_status tide_norm_forward(const tide_norm_forward_args* args, tide_stream_t stream) {
+    if (!args) return TIDE_EINVAL;
+    const tide_norm_forward_args& a = *args;
+    const int64_t T = a.rows, C = a.cols;
+    TIDE_TRY(check_norm(T, C, a.kind, a.eps));
+    if (T == 0 || C == 0) return TIDE_OK;
+    TIDE_TRY(check_rows(a.x, a.ldx, T, C));
+    TIDE_TRY(check_rows(a.weight, C, 1, C));
+    if (a.bias) TIDE_TRY(check_rows(a.bias, C, 1, C));
+    TIDE_TRY(check_rows(a.y, a.ldy, T, C));
+    if (a.x_kept) TIDE_TRY(check_kept(a.x_kept, T, C));
+    if (a.y_kept) TIDE_TRY(check_kept(a.y_kept, T, C));
+    const Extent in[] = {rows_extent(a.x, a.ldx, T, C), rows_extent(a.weight, C, 1, C),
+                         rows_extent(a.bias, C, 1, C)};
+    const Extent out[] = {rows_extent(a.y, a.ldy, T, C), bytes_extent(a.x_kept, act8_bytes(T, C)),
+                          bytes_extent(a.y_kept, act8_bytes(T, C))};
+    TIDE_TRY(check_apart(in, 3, out, 3));
+    TIDE_TRY(check_stream_device(stream));
+    NormForward p = {};
+    p.x = static_cast<const uint16_t*>(a.x);
+    p.ldx = a.ldx;
+    p.rows = T;
+    p.cols = (int32_t)C;
+    p.eps = a.eps;
+    p.inv_cols = 1.0f / (float)C;
+    p.w = static_cast<const uint16_t*>(a.weight);
+    p.b = static_cast<const uint16_t*>(a.bias);
+    p.y = static_cast<uint16_t*>(a.y);
+    p.ldy = a.ldy;
+    p.x_kept = static_cast<uint8_t*>(a.x_kept);
+    p.y_kept = static_cast<uint8_t*>(a.y_kept);
+    const ForwardForm& f = form_of(kForwardForms, C);
+    const int threads = threads_of(f.shape);
+    return launch(a.kind == TIDE_NORM_LAYER ? f.layer : f.rms,
+                  ceil_div(T, threads / f.shape.lanes), threads, stream, p);
+}
+
+namespace {
+
+struct NormBackwardPlan {
+    const BackwardForm* form;
+    int64_t chunk, chunks, pitch;
+    float *dw = nullptr, *db = nullptr;
+    int64_t bytes;
+};
+
+tide_status check_backward(const tide_norm_backward_args& a) {
+    const int64_t T = a.rows, C = a.cols;
+    TIDE_TRY(check_norm(T, C, a.kind, a.eps));
+    if (!a.dx && !a.dweight && !a.dbias) return TIDE_OK;
+    TIDE_TRY(check_rows(a.dy, a.lddy, T, C));
+    if (a.x && a.x_kept) return TIDE_EINVAL;
+    if (a.dx || a.dweight) {
+        if (a.x)
+            TIDE_TRY(check_rows(a.x, a.ldx, T, C));
+        else
+            TIDE_TRY(check_kept(a.x_kept, T, C));
+    }
+    if (a.dx) {
+        TIDE_TRY(check_rows(a.weight, C, 1, C));
+        TIDE_TRY(check_rows(a.dx, a.lddx, T, C));
+        if (a.add) TIDE_TRY(check_rows(a.add, a.ldadd, T, C));
+    }
+    if (a.dweight) TIDE_TRY(check_rows(a.dweight, C, 1, C));
+    if (a.dbias) TIDE_TRY(check_rows(a.dbias, C, 1, C));
+    return TIDE_OK;
+}
+
+NormBackwardPlan plan_backward(const tide_norm_backward_args& a, void* ws) {
+    NormBackwardPlan b;
+    Carver c{static_cast<char*>(ws)};
+    b.form = &form_of(kBackwardForms, a.cols);
+    const int threads = threads_of(b.form->shape);
+    const int64_t at_once = threads / b.form->shape.lanes;
+    // as many workgroups as the chip holds at two (of 1024 threads) to four
+    // (of 256) a compute unit
+    const int64_t groups = 256 * std::max(1, std::min(4, 1024 / threads));
+    b.chunk = round_up(std::max<int64_t>(1, ceil_div(a.rows, groups)), at_once);
+    b.chunks = ceil_div(a.rows, b.chunk);
+    b.pitch = round_up(a.cols, 8);
+    if (b.chunks > 1) {
+        if (a.dweight) b.dw = c.take<float>(b.chunks * b.pitch);
+        if (a.dbias) b.db = c.take<float>(b.chunks * b.pitch);
+    }
+    b.bytes = c.used;
+    return b;
+}
+
+}  // namespace
+
+extern "C" tide_status tide_norm_backward_workspace(const tide_norm_backward_args* args,
+                                                    size_t* bytes) {
+    if (!args || !bytes) return TIDE_EINVAL;
+    TIDE_TRY(check_backward(*args));
+    *bytes = args->rows && args->cols ? (size_t)plan_backward(*args, nullptr).bytes : 0;
+    return TIDE_OK;
+}
+
+extern "C" tide_status tide_norm_backward(const tide_norm_backward_args* args, void* workspace,
+                                          size_t workspace_bytes, tide_stream_t stream) {
+    if (!args) return TIDE_EINVAL;
+    const tide_norm_backward_args& a = *args;
+    TIDE_TRY(check_backward(a));
+    const int64_t T = a.rows, C = a.cols;
+    if ((!a.dx && !a.dweight && !a.dbias) || C == 0) return TIDE_OK;
+    const bool in_place = a.add == a.dx && (T <= 1 || a.ldadd == a.lddx);
+    const Extent ext[] = {
+        rows_extent(a.dy, a.lddy, T, C),
+        a.dx || a.dweight ? rows_extent(a.x, a.ldx, T, C) : Extent(),
+        a.dx || a.dweight ? bytes_extent(a.x_kept, act8_bytes(T, C)) : Extent(),
+        a.dx ? rows_extent(a.weight, C, 1, C) : Extent(),
+        a.dx && !in_place ? rows_extent(a.add, a.ldadd, T, C) : Extent(),
+        rows_extent(a.dx, a.lddx, T, C),
+        rows_extent(a.dweight, C, 1, C),
+        rows_extent(a.dbias, C, 1, C)};
+    TIDE_TRY(check_apart(ext, 5, ext + 5, 3));
+    const NormBackwardPlan b = plan_backward(a, workspace);
+    TIDE_TRY(check_workspace(workspace, workspace_bytes, T ? b.bytes : 0, ext, 8));
+    TIDE_TRY(check_stream_device(stream));
+    NormBackward p = {};
+    p.dy = static_cast<const uint16_t*>(a.dy);
+    p.lddy = a.lddy;
+    const bool need_x = a.dx || a.dweight;
+    if (need_x) {
+        p.x = static_cast<const uint16_t*>(a.x);
+        p.ldx = a.ldx;
+        p.x_kept = static_cast<const uint8_t*>(a.x_kept);
+    }
+    p.dx = static_cast<uint16_t*>(a.dx);
+    p.lddx = a.lddx;
+    if (a.dx) {
+        p.w = static_cast<const uint16_t*>(a.weight);
+        p.add = static_cast<const uint16_t*>(a.add);
+        p.ldadd = a.ldadd;
+    }
+    p.dw_sums = b.dw;
+    p.db_sums = b.db;
+    if (b.chunks <= 1) {
+        p.dweight = static_cast<uint16_t*>(a.dweight);
+        p.dbias = static_cast<uint16_t*>(a.dbias);
+    }
+    p.rows = T;
+    p.chunk = b.chunk;
+    p.sums_pitch = b.pitch;
+    p.cols = (int32_t)C;
+    p.eps = a.eps;
+    p.inv_cols = 1.0f / (float)C;
+    const bool layer = a.kind == TIDE_NORM_LAYER;
+    const BackwardForm& f = *b.form;
+    auto k = layer ? a.dbias ? f.layer_db : f.layer : a.dbias ? f.rms_db : f.rms;
+    // without rows one workgroup writes the empty sums
+    const int64_t grid = T ? b.chunks : a.dweight || a.dbias ? 1 : 0;
+    TIDE_TRY(launch(k, grid, threads_of(f.shape), stream, p));
+    if (b.chunks <= 1 || !(b.dw || b.db)) return TIDE_OK;
+    return launch(norm_sums_kernel, ceil_div(C, 64) * ((b.dw ? 1 : 0) + (b.db ? 1 : 0)),
+                  64 * kSumWaves, stream, (const float*)b.dw, (const float*)b.db, b.chunks, b.pitch, C,
+                  static_cast<uint16_t*>(a.dweight), static_cast<uint16_t*>(a.dbias));
+}
