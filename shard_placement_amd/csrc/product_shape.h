@@ -161,6 +161,16 @@ inline Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth, double* esti
     return s;
 }
 
+// The same for a product with the rows of two matrices in turn (I: both), whose
+// waves hold whole checkpoint blocks of the output: 16 rows are always two sets
+// of waves, and reading 512 bytes of a row at a time takes tiles of 32.
+inline Shape choose_gated(int64_t I, int64_t J, int64_t depth) {
+    Shape s = choose(kForward, I, J, depth);
+    if (s.bk == 256) s.bj = 32;
+    else if (s.bj == 16) s.halves = 2;
+    return s;
+}
+
 // dx [T, K] and dW [N, K] in one launch of 256-wide tiles, the longer ones
 // first: the pair of tiles of the least estimated time, or none if that is not
 // 3% less than `best`, that of the two products one after the other.

@@ -50,13 +50,30 @@ typedef float f32x4v __attribute__((ext_vector_type(4)));
 //
 // A "kept" operand is the columns of a checkpoint (act8.h): `depth` rows of
 // `count` = ld = its pitch.
-enum Layout { kRows, kColumns, kKept };
+//
+// Two matrices of one shape are one operand A in two ways.  "Pair rows": rows,
+// 16 of the first and the same 16 of the second in turn, so that a lane ends
+// with the same element of both products.  "Pair columns": columns, the
+// contraction going through the first and then, from element `turn` (a multiple
+// of 64, `depth` or more; what lies between reads as 0) on, through the second.
+enum Layout { kRows, kColumns, kKept, kPairRows, kPairColumns };
+
+// The contraction index runs across memory.
+constexpr bool across(Layout l) { return l != kRows && l != kPairRows; }
 
 struct Operand {
     const void* p;
     int64_t ld;
     int64_t count;
     int64_t depth;
+};
+
+struct PairOperand {
+    const void *p, *p2;
+    int64_t ld;
+    int64_t count;  // of one matrix
+    int64_t depth;  // of one matrix
+    int64_t turn;   // pair columns
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* base, int64_t bytes) {
@@ -226,6 +243,87 @@ struct KeptStager {
     }
 };
 
+// "Pair rows": tile row r is row r / 32 * 16 + r % 16 of matrix r / 16 % 2.
+template <int N, int K, int WAVES, bool ONCE>
+struct PairRowsStager {
+    static constexpr int kBytes = N * K * 2;
+    static constexpr int kLoads = kBytes / 1024;
+    static constexpr int kMine = kLoads / WAVES;
+    static constexpr int kRowChunks = K / 8;
+    static constexpr int kLoadRows = 64 / kRowChunks;  // of a wave's load
+    static_assert(kMine * WAVES == kLoads && WAVES * kLoadRows % 8 == 0, "");
+    // a wave's loads are of one matrix, or of both in the same order in every wave
+    static constexpr bool kOne = WAVES * kLoadRows % 32 == 0;
+    static_assert(kOne || WAVES * kLoadRows <= 16, "");
+
+    const char *base, *base2;  // kOne: the wave's matrix, in `base`
+    int64_t left;
+    uint32_t offset[kMine];
+    int wave;
+    int chunk_k;
+
+    __device__ __forceinline__ void init(const PairOperand& o, int64_t first, int64_t k0, int lane,
+                                         int wave_) {
+        wave = wave_;
+        const int64_t at = 2 * (first / 2 * o.ld + k0);
+        const bool second = kOne && wave * kLoadRows / 16 % 2;
+        base = static_cast<const char*>(second ? o.p2 : o.p) + at;
+        base2 = static_cast<const char*>(o.p2) + at;
+        left = 2 * ((o.count - first / 2 - 1) * o.ld + o.depth - k0);
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) {
+            const int place = (q * WAVES + wave) * 64 + lane;
+            const int row = place / kRowChunks, c = place % kRowChunks ^ row_swizzle(row);
+            chunk_k = c * 8;
+            offset[q] = (uint32_t)((int64_t)(row / 32 * 16 + row % 16) * o.ld * 2 + c * 16);
+        }
+    }
+
+    __device__ __forceinline__ void prime() {}
+
+    __device__ __forceinline__ void stage(TIDE_LDS char* lds, int64_t valid) {
+        const __amdgpu_buffer_rsrc_t r = resource(base, left), r2 = resource(base2, left);
+        const bool none = valid < K && chunk_k >= valid;
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) {
+            const bool second = !kOne && q * WAVES * kLoadRows / 16 % 2;
+            load_to_lds<ONCE ? kNonTemporal : 0>(second ? r2 : r, lds + (q * WAVES + wave) * 1024,
+                                                 none ? kNowhere : offset[q]);
+        }
+        base += 2 * K;
+        base2 += 2 * K;
+        left -= 2 * K;
+    }
+};
+
+// "Pair columns": a "columns" tile that goes on in the second matrix.
+template <int N, int K, int WAVES>
+struct PairColumnsStager : Stager<N, K, WAVES, true> {
+    using Base = Stager<N, K, WAVES, true>;
+    const char* base2;  // the second matrix's first tile
+    int64_t left2;
+    int64_t until;      // contraction elements up to it
+
+    __device__ __forceinline__ void init(const PairOperand& o, int64_t first, int64_t k0, int lane,
+                                         int wave) {
+        const bool second = k0 >= o.turn;
+        Base::init(Operand{second ? o.p2 : o.p, o.ld, o.count, o.depth}, first,
+                   second ? k0 - o.turn : k0, lane, wave);
+        base2 = static_cast<const char*>(o.p2) + 2 * first;
+        left2 = 2 * ((o.depth - 1) * o.ld + o.count - first);
+        until = o.turn - k0;  // none left of it where the second is under way
+    }
+
+    __device__ __forceinline__ void stage(TIDE_LDS char* lds, int64_t valid) {
+        Base::stage(lds, valid);
+        until -= K;
+        if (until == 0) {
+            this->base = base2;
+            this->left = left2;
+        }
+    }
+};
+
 template <int N, int K, int WAVES, Layout L, bool ONCE>
 struct StagerOf {
     using type = Stager<N, K, WAVES, L == kColumns, ONCE>;
@@ -234,6 +332,14 @@ template <int N, int K, int WAVES, bool ONCE>
 struct StagerOf<N, K, WAVES, kKept, ONCE> {
     using type = KeptStager<N, K, WAVES>;
 };
+template <int N, int K, int WAVES, bool ONCE>
+struct StagerOf<N, K, WAVES, kPairRows, ONCE> {
+    using type = PairRowsStager<N, K, WAVES, ONCE>;
+};
+template <int N, int K, int WAVES, bool ONCE>
+struct StagerOf<N, K, WAVES, kPairColumns, ONCE> {
+    using type = PairColumnsStager<N, K, WAVES>;
+};
 
 // The 16 x 32 piece of a staged tile that a matrix instruction takes: index
 // m0 + (lane & 15), contraction k = 32 * s + 8 * (lane >> 4) .. + 7.
@@ -241,7 +347,7 @@ template <int N, int K, Layout L>
 struct Reader {
     template <int S>
     __device__ __forceinline__ static bf16x8 read(const TIDE_LDS char* lds, int m0, int lane) {
-        if constexpr (L != kRows) {
+        if constexpr (across(L)) {
             constexpr int kRow = 2 * N;
             const int g = lane >> 4, i = lane & 15;
             const int k = 32 * S + 8 * g + (i >> 2);
@@ -320,7 +426,7 @@ __device__ __forceinline__ void deep_step(TIDE_LDS char* __restrict__ next,
                                           SA& sa, SB& sb, int64_t valid, int wi, int wj, int lane,
                                           bf16x8 (&a0)[TI], bf16x8 (&b0)[TJ],
                                           f32x4v (&acc)[TI][TJ]) {
-    constexpr int kReads = TI * (CA == kRows ? 1 : 2) + TJ * (CB == kRows ? 1 : 2);
+    constexpr int kReads = TI * (across(CA) ? 2 : 1) + TJ * (across(CB) ? 2 : 1);
     bf16x8 a1[TI], b1[TJ];
     read_part<BI, BJ, K, TI, TJ, CA, CB, 1>(now, now + SA::kBytes, wi, wj, lane, a1, b1);
     multiply_part<TI, TJ>(a0, b0, acc);
@@ -334,7 +440,7 @@ __device__ __forceinline__ void deep_step(TIDE_LDS char* __restrict__ next,
         sb.stage(now + SA::kBytes, valid);
     }
     multiply_part<TI, TJ>(a1, b1, acc);
-    if constexpr (CB != kRows) {
+    if constexpr (across(CB)) {
         // many short reads: the loads are issued before them
         __builtin_amdgcn_sched_group_barrier(0x020, SA::kMine + SB::kMine, 0);
         interleave<kReads>();
@@ -384,8 +490,8 @@ __device__ __forceinline__ void plain_step(TIDE_LDS char* __restrict__ next,
 // H = 2: the elements in two halves of as many steps, each by WI * WJ waves
 // with tiles of their own in LDS.  (Only where k1 = depth can the number of
 // steps be odd, and behind `depth` the operands read as 0.)
-template <int BI, int BJ, int K, int WI, int WJ, Layout CA, Layout CB, int H>
-__device__ __forceinline__ void tile_loop(const Operand& A, const Operand& B, int64_t depth,
+template <int BI, int BJ, int K, int WI, int WJ, Layout CA, Layout CB, int H, typename OA>
+__device__ __forceinline__ void tile_loop(const OA& A, const Operand& B, int64_t depth,
                                           int64_t k0, int64_t k1, int64_t i0, int64_t j0,
                                           TIDE_LDS char* lds,
                                           f32x4v (&acc)[BI / WI / 16][BJ / WJ / 16]) {
