@@ -653,6 +653,71 @@ tide_status tide_norm_backward_workspace(const tide_norm_backward_args *args, si
 tide_status tide_norm_backward(const tide_norm_backward_args *args, void *workspace,
                                size_t workspace_bytes, tide_stream_t stream);
 
+/* The gated block in front of a layer's last product, and its gradients.
+ *
+ * forward:  g = x Wg^T + bg, u = x Wu^T + bu, h = act(g) u, with T tokens, x
+ *           [T, K], Wg (gate) and Wu (up) [N, K], bg and bu [N], h [T, N], all
+ *           bf16; sums, biases, act and the product are in binary32 and h is
+ *           rounded once.  g_kept, u_kept and h_kept, where given, receive the
+ *           checkpoints of g, u (which the gradients need) and h (which the
+ *           next product's weight gradient needs), in 8 bits straight from
+ *           binary32.
+ * backward: dg = dh u act'(g), du = dh act(g), dx = dg Wg + du Wu, dWg = dg^T x,
+ *           dWu = du^T x, dbg and dbu the sums of dg and du over the tokens,
+ *           with x, g and u as their checkpoints stand for them.  dx, dWg and dWu
+ *           [N, K] (contiguous), dbg and dbu [N] are bf16, rounded once.  Any of
+ *           them may be NULL (not computed; dWg and dWu together), and so may
+ *           what only it needs (gate and up for dx, x_kept for dWg and dWu).  dg
+ *           and du are rounded to bf16 once before the products (the biases'
+ *           gradients sum them unrounded).
+ *
+ * act as for the layer products, and so are the limits, with 2 N in the place
+ * of N, the checks of overlap, empty sizes, workspaces and streams.  act of a g
+ * that is minus infinity is NaN forward, but for relu (0); a finite g that
+ * reads back as infinity has the value and slope of its limit. */
+typedef struct tide_gated_forward_args {
+    int64_t tokens, out_features, in_features; /* T, N, K */
+    int32_t act;                               /* TIDE_ACT_* */
+    int32_t reserved;                          /* 0 */
+    const void *x;
+    int64_t ldx;
+    const void *gate;
+    const void *up;
+    const void *gate_bias; /* or NULL */
+    const void *up_bias;   /* or NULL */
+    void *h;
+    int64_t ldh;
+    void *g_kept; /* or NULL */
+    void *u_kept; /* or NULL */
+    void *h_kept; /* or NULL */
+} tide_gated_forward_args;
+
+typedef struct tide_gated_backward_args {
+    int64_t tokens, out_features, in_features; /* T, N, K */
+    int32_t act;                               /* TIDE_ACT_* */
+    int32_t reserved;                          /* 0 */
+    const void *dh;
+    int64_t lddh;
+    const void *gate;
+    const void *up;
+    const void *x_kept;
+    const void *g_kept;
+    const void *u_kept;
+    void *dx; /* or NULL */
+    int64_t lddx;
+    void *dgate;      /* or NULL */
+    void *dup;        /* NULL where dgate is */
+    void *dgate_bias; /* or NULL */
+    void *dup_bias;   /* or NULL */
+} tide_gated_backward_args;
+
+tide_status tide_gated_forward_workspace(const tide_gated_forward_args *args, size_t *bytes);
+tide_status tide_gated_forward(const tide_gated_forward_args *args, void *workspace,
+                               size_t workspace_bytes, tide_stream_t stream);
+tide_status tide_gated_backward_workspace(const tide_gated_backward_args *args, size_t *bytes);
+tide_status tide_gated_backward(const tide_gated_backward_args *args, void *workspace,
+                                size_t workspace_bytes, tide_stream_t stream);
+
 /* Static text for a status code. */
 const char *tide_status_str(int32_t status);
 

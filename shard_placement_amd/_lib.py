@@ -32,7 +32,8 @@ EXPORTS = ("tide_abi_version", "tide_status_str", "tide_desc_size", "tide_desc_g
            "tide_rs_bf16_to_fp32_streams", "tide_act8_bytes", "tide_act8_pack", "tide_act8_unpack",
            "tide_linear_forward_workspace", "tide_linear_forward",
            "tide_linear_backward_workspace", "tide_linear_backward", "tide_norm_forward",
-           "tide_norm_backward_workspace", "tide_norm_backward")
+           "tide_norm_backward_workspace", "tide_norm_backward", "tide_gated_forward_workspace",
+           "tide_gated_forward", "tide_gated_backward_workspace", "tide_gated_backward")
 
 
 class TideShape(ctypes.Structure):
@@ -87,6 +88,26 @@ class TideNormBackwardArgs(ctypes.Structure):
                 ("weight", ctypes.c_void_p), ("add", ctypes.c_void_p), ("ldadd", ctypes.c_int64),
                 ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dweight", ctypes.c_void_p),
                 ("dbias", ctypes.c_void_p)]
+
+
+class TideGatedForwardArgs(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("out_features", ctypes.c_int64),
+                ("in_features", ctypes.c_int64), ("act", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("gate", ctypes.c_void_p), ("up", ctypes.c_void_p),
+                ("gate_bias", ctypes.c_void_p), ("up_bias", ctypes.c_void_p),
+                ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("g_kept", ctypes.c_void_p),
+                ("u_kept", ctypes.c_void_p), ("h_kept", ctypes.c_void_p)]
+
+
+class TideGatedBackwardArgs(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("out_features", ctypes.c_int64),
+                ("in_features", ctypes.c_int64), ("act", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+                ("gate", ctypes.c_void_p), ("up", ctypes.c_void_p), ("x_kept", ctypes.c_void_p),
+                ("g_kept", ctypes.c_void_p), ("u_kept", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+                ("lddx", ctypes.c_int64), ("dgate", ctypes.c_void_p), ("dup", ctypes.c_void_p),
+                ("dgate_bias", ctypes.c_void_p), ("dup_bias", ctypes.c_void_p)]
 
 
 class TideError(RuntimeError):
@@ -168,6 +189,11 @@ def lib():
     L.tide_norm_forward.argtypes = [fwd, vp]
     L.tide_norm_backward_workspace.argtypes = [bwd, sizep]
     L.tide_norm_backward.argtypes = [bwd, vp, ctypes.c_size_t, vp]
+    fwd, bwd = ctypes.POINTER(TideGatedForwardArgs), ctypes.POINTER(TideGatedBackwardArgs)
+    L.tide_gated_forward_workspace.argtypes = [fwd, sizep]
+    L.tide_gated_forward.argtypes = [fwd, vp, ctypes.c_size_t, vp]
+    L.tide_gated_backward_workspace.argtypes = [bwd, sizep]
+    L.tide_gated_backward.argtypes = [bwd, vp, ctypes.c_size_t, vp]
     for name in ("tide_desc_size", "tide_desc_geometry", "tide_desc_build", "tide_plan_query",
                  "tide_rs_bf16_to_fp32", "tide_ag_place", "tide_ag_place_sdma",
                  "tide_stream_create_cu_limited", "tide_stream_destroy",
@@ -181,7 +207,9 @@ def lib():
                  "tide_act8_bytes", "tide_act8_pack", "tide_act8_unpack",
                  "tide_linear_forward_workspace", "tide_linear_forward",
                  "tide_linear_backward_workspace", "tide_linear_backward", "tide_norm_forward",
-                 "tide_norm_backward_workspace", "tide_norm_backward"):
+                 "tide_norm_backward_workspace", "tide_norm_backward",
+                 "tide_gated_forward_workspace", "tide_gated_forward",
+                 "tide_gated_backward_workspace", "tide_gated_backward"):
         getattr(L, name).restype = ctypes.c_int
     if L.tide_abi_version() != 2:
         raise RuntimeError("libtide ABI version %d, expected 2" % L.tide_abi_version())

@@ -21,9 +21,9 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._lib import (TideError, TideLinearBackwardArgs, TideLinearForwardArgs,
-                   TideNormBackwardArgs, TideNormForwardArgs, TideOpts, TidePlanInfo, TideShape,
-                   check)
+from ._lib import (TideError, TideGatedBackwardArgs, TideGatedForwardArgs,
+                   TideLinearBackwardArgs, TideLinearForwardArgs, TideNormBackwardArgs,
+                   TideNormForwardArgs, TideOpts, TidePlanInfo, TideShape, check)
 
 ORDERS = {"fixed": 0, "tree": 1}
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
@@ -618,6 +618,90 @@ def tide_norm_backward(dy: torch.Tensor, x=None, x_kept=None, weight=None, kind:
     if dbias is not None:
         a.dbias = _whole(dbias, (C,), "dbias", index)
     return _on_device(index, stream, _norm_backward_on, a, dx, index)
+
+
+def _gated_forward_on(s, a, h, index):
+    if h is None:
+        h = torch.empty(a.tokens, a.out_features, dtype=torch.bfloat16, device=index)
+        a.h, a.ldh = h.data_ptr(), a.out_features
+    L = _lib.lib()
+    ws, ptr, n = _workspace(L.tide_gated_forward_workspace, a, index)
+    check(L.tide_gated_forward(ctypes.byref(a), ptr, n, s), "tide_gated_forward")
+    return h
+
+
+def tide_gated_forward(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
+                       h: torch.Tensor = None, gate_bias=None, up_bias=None, act: str = "silu",
+                       g_kept=None, u_kept=None, h_kept=None, stream=None) -> torch.Tensor:
+    """h = act(g) u, g = x gate^T + gate_bias, u = x up^T + up_bias; g_kept,
+    u_kept and h_kept (uint8), where given, receive their checkpoints.  Returns
+    h (allocated when not given).  Nothing is recorded by autograd
+    (tide_gated_backward is the gradient): x and h may not require one in grad
+    mode."""
+    index = _index(x, "x")
+    _no_graph(x, "x")
+    T, K = x.shape
+    if gate.dim() != 2:
+        raise TideError(-1, "gate has %d dimensions, expected 2" % gate.dim())
+    N = gate.shape[0]
+    px, ldx = _rows(x, "x")
+    a = TideGatedForwardArgs(T, N, K, _act(act), 0, px, ldx, _whole(gate, (N, K), "gate", index),
+                             _whole(up, (N, K), "up", index))
+    if gate_bias is not None:
+        a.gate_bias = _whole(gate_bias, (N,), "gate_bias", index)
+    if up_bias is not None:
+        a.up_bias = _whole(up_bias, (N,), "up_bias", index)
+    if h is not None:
+        a.h, a.ldh = _matrix(h, T, N, "h", index)
+    for name, kept in (("g_kept", g_kept), ("u_kept", u_kept), ("h_kept", h_kept)):
+        if kept is not None:
+            setattr(a, name, _kept(kept, T, N, name, index))
+    return _on_device(index, stream, _gated_forward_on, a, h, index)
+
+
+def _gated_backward_on(s, a, dx, index):
+    if dx is True:
+        dx = torch.empty(a.tokens, a.in_features, dtype=torch.bfloat16, device=index)
+        a.dx, a.lddx = dx.data_ptr(), a.in_features
+    L = _lib.lib()
+    ws, ptr, n = _workspace(L.tide_gated_backward_workspace, a, index)
+    check(L.tide_gated_backward(ctypes.byref(a), ptr, n, s), "tide_gated_backward")
+    return dx
+
+
+def tide_gated_backward(dh: torch.Tensor, in_features: int, g_kept: torch.Tensor,
+                        u_kept: torch.Tensor, gate=None, up=None, x_kept=None, act: str = "silu",
+                        dx=None, dgate=None, dup=None, dgate_bias=None, dup_bias=None, stream=None):
+    """The gradients that are given, with dg = dh u act'(g) and du = dh act(g):
+    dx = dg gate + du up, dgate = dg^T x and dup = du^T x (both or neither),
+    dgate_bias and dup_bias = the sums of dg and du over the tokens.  dx=True
+    allocates it.  Returns dx."""
+    index = _index(dh, "dh")
+    _no_graph(dh, "dh")
+    T, N = dh.shape
+    K = int(in_features)
+    pdh, lddh = _rows(dh, "dh")
+    a = TideGatedBackwardArgs(T, N, K, _act(act), 0, pdh, lddh)
+    a.g_kept = _kept(g_kept, T, N, "g_kept", index)
+    a.u_kept = _kept(u_kept, T, N, "u_kept", index)
+    if dx is not None:
+        if gate is None or up is None:
+            raise TideError(-1, "dx needs gate and up")
+        a.gate, a.up = _whole(gate, (N, K), "gate", index), _whole(up, (N, K), "up", index)
+        if dx is not True:
+            a.dx, a.lddx = _matrix(dx, T, K, "dx", index)
+    if (dgate is None) != (dup is None):
+        raise TideError(-1, "dgate and dup are computed together")
+    if dgate is not None:
+        if x_kept is None:
+            raise TideError(-1, "dgate and dup need the checkpoint of x")
+        a.x_kept = _kept(x_kept, T, K, "x_kept", index)
+        a.dgate, a.dup = _whole(dgate, (N, K), "dgate", index), _whole(dup, (N, K), "dup", index)
+    if dgate_bias is not None:
+        a.dgate_bias = _whole(dgate_bias, (N,), "dgate_bias", index)
+    if dup_bias is not None:
+        a.dup_bias = _whole(dup_bias, (N,), "dup_bias", index)
+    return _on_device(index, stream, _gated_backward_on, a, dx, index)
 
 
 class Plan:
