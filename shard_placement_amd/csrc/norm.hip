@@ -91,12 +91,21 @@ __device__ __forceinline__ void row_sums(float (&v)[N], lds_float* box) {
 
 // The columns of a lane's unit u of L lanes, and how many of them exist.
 template <int L>
-__device__ __forceinline__ int32_t column(int u) {
-    return (int32_t)((threadIdx.x % L + u * L) * 8);
+__device__ __forceinline__ uint32_t column(int u, uint32_t thread) {
+    return (thread % L + (uint32_t)u * L) * 8;
+}
+
+// The thread's number, to work out columns from where they are used: kept
+// through the loop over rows, they and what is worked out from them take a
+// third of the registers.
+__device__ __forceinline__ uint32_t this_thread() {
+    uint32_t t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
 }
 
 // Eight elements from column c of a row of `cols`; those that do not exist are 0.
-__device__ __forceinline__ u32x4v load_unit(const uint16_t* row, int32_t c, int32_t cols) {
+__device__ __forceinline__ u32x4v load_unit(const uint16_t* row, uint32_t c, uint32_t cols) {
     u32x4v w = 0;
     if (c + 8 <= cols) {
         w = load8_raw(row + c);
@@ -110,27 +119,29 @@ __device__ __forceinline__ u32x4v load_unit(const uint16_t* row, int32_t c, int3
 }
 
 // The same of a row that is read once.
-__device__ __forceinline__ u32x4v load_unit_once(const uint16_t* row, int32_t c, int32_t cols) {
+__device__ __forceinline__ u32x4v load_unit_once(const uint16_t* row, uint32_t c, uint32_t cols) {
     return c + 8 <= cols ? load8_raw<true>(row + c) : load_unit(row, c, cols);
 }
 
 // The units as they lie in memory are what stays in registers between the
 // passes over a row: without this the compiler keeps their widened elements,
-// twice the registers (one of 8 workgroups fits where two would).
+// twice the registers, which only lanes of one unit have.
 template <int U>
 __device__ __forceinline__ void forget(u32x4v (&w)[U]) {
+    if constexpr (U > 1) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) asm volatile("" : "+v"(w[u]));
+        for (int u = 0; u < U; ++u) asm volatile("" : "+v"(w[u]));
+    }
 }
 
-// v - mu where the element exists, else 0.
-__device__ __forceinline__ void centre(float (&v)[8], float mu, int32_t c, int32_t cols) {
-    if (c + 8 <= cols) {
+// v - mu where the element exists, else 0 (v is 0 there).
+__device__ __forceinline__ void centre(float (&v)[8], float mu, uint32_t c, uint32_t cols) {
+    mu = c < cols ? mu : 0.0f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] -= mu;
-    } else {
+    for (int k = 0; k < 8; ++k) v[k] -= mu;
+    if (cols % 8) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = c + k < cols ? v[k] - mu : 0.0f;
+        for (int k = 0; k < 8; ++k) v[k] = (int32_t)(cols - c) > k ? v[k] : 0.0f;
     }
 }
 
@@ -149,7 +160,7 @@ __device__ __forceinline__ float inv_sqrt(float v) { return __builtin_amdgcn_rsq
 struct NormForward {
     const uint16_t* x;
     int64_t ldx, rows;
-    int32_t cols;
+    uint32_t cols;
     float eps, inv_cols;
     const uint16_t *w, *b;
     uint16_t* y;
@@ -157,7 +168,7 @@ struct NormForward {
     uint8_t *x_kept, *y_kept;
 };
 
-__device__ __forceinline__ void keep(uint8_t* kept, int64_t rows, int64_t row, int32_t c,
+__device__ __forceinline__ void keep(uint8_t* kept, int64_t rows, int64_t row, uint32_t c,
                                      int64_t pitch, float (&v)[8]) {
     u32x2 q;
     const int e = act8_pack8(v, &q);
@@ -176,12 +187,12 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_forward_kern
     const uint16_t* from = p.x + row * p.ldx;
     u32x4v raw[U], w[U], b[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) raw[u] = load_unit_once(from, column<L>(u), p.cols);
+    for (int u = 0; u < U; ++u) raw[u] = load_unit_once(from, column<L>(u, threadIdx.x), p.cols);
 #pragma unroll
-    for (int u = 0; u < U; ++u) w[u] = load_unit(p.w, column<L>(u), p.cols);
+    for (int u = 0; u < U; ++u) w[u] = load_unit(p.w, column<L>(u, threadIdx.x), p.cols);
     if (p.b) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) b[u] = load_unit(p.b, column<L>(u), p.cols);
+        for (int u = 0; u < U; ++u) b[u] = load_unit(p.b, column<L>(u, threadIdx.x), p.cols);
     }
     float mu = 0.0f;
     if constexpr (LAYER) {
@@ -202,7 +213,7 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_forward_kern
     for (int u = 0; u < U; ++u) {
         float v[8];
         widen(raw[u], v);
-        if constexpr (LAYER) centre(v, mu, column<L>(u), p.cols);
+        if constexpr (LAYER) centre(v, mu, column<L>(u, threadIdx.x), p.cols);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             s[0] = __builtin_fmaf(v[k], v[k], s[0]);
@@ -216,7 +227,7 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_forward_kern
     const int64_t pitch = act8_pitch(p.cols);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int32_t c = column<L>(u);
+        const uint32_t c = column<L>(u, threadIdx.x);
         if (c >= pitch) break;  // the same in a quad, whose lanes pack together
         float v[8], f[8], y[8];
         widen(raw[u], v);
@@ -228,7 +239,7 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_forward_kern
 #pragma unroll
             for (int k = 0; k < 8; ++k) y[k] += f[k];
         }
-        if (c < p.cols) store8(p.y + row * p.ldy + c, p.cols - c, y);
+        if (c < p.cols) store8(p.y + row * p.ldy + c, (int64_t)p.cols - c, y);
         if (p.x_kept) keep(p.x_kept, p.rows, row, c, pitch, v);
         if (p.y_kept) {
             if (c + 8 > p.cols) {
@@ -254,29 +265,30 @@ struct NormBackward {
     int64_t ldadd;
     uint16_t* dx;
     int64_t lddx;
-    float *dw_sums, *db_sums;   // [chunks][pitch], or NULL
-    uint16_t *dweight, *dbias;  // the one chunk's sums go there, or NULL
-    int64_t rows, chunk, sums_pitch;
-    int32_t cols;
+    float *dw_sums, *db_sums;   // [workgroups][pitch], or NULL
+    uint16_t *dweight, *dbias;  // the one workgroup's sums go there, or NULL
+    int64_t rows, sums_pitch;
+    uint32_t cols;
     float eps, inv_cols;
 };
 
 // What a lane reads of a row; of a kept x a unit is 8 bytes and its scale.
 template <int U>
 struct RowParts {
-    u32x4v dy[U], x[U], add[U];
+    u32x4v dy[U], x[U];
 };
 
 template <int L, int U>
 __device__ __forceinline__ void load_row(const NormBackward& p, int64_t row, RowParts<U>& r) {
+    const uint32_t t = this_thread();
 #pragma unroll
-    for (int u = 0; u < U; ++u) r.dy[u] = load_unit_once(p.dy + row * p.lddy, column<L>(u), p.cols);
+    for (int u = 0; u < U; ++u) r.dy[u] = load_unit_once(p.dy + row * p.lddy, column<L>(u, t), p.cols);
     if (p.x_kept) {
         const int64_t pitch = act8_pitch(p.cols);
         const uint8_t* scales = p.x_kept + p.rows * pitch;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int32_t c = column<L>(u);
+            const uint32_t c = column<L>(u, t);
             const int64_t at = row * pitch + c;
             r.x[u] = 0;
             if (c < p.cols) {
@@ -287,29 +299,34 @@ __device__ __forceinline__ void load_row(const NormBackward& p, int64_t row, Row
         }
     } else if (p.x) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) r.x[u] = load_unit_once(p.x + row * p.ldx, column<L>(u), p.cols);
+        for (int u = 0; u < U; ++u) r.x[u] = load_unit_once(p.x + row * p.ldx, column<L>(u, t), p.cols);
     } else {  // db alone needs no x
 #pragma unroll
         for (int u = 0; u < U; ++u) r.x[u] = 0;
     }
+}
+
+template <int L, int U>
+__device__ __forceinline__ void load_add(const NormBackward& p, int64_t row, u32x4v (&add)[U]) {
     if (p.add) {
+        const uint32_t t = this_thread();
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            r.add[u] = load_unit_once(p.add + row * p.ldadd, column<L>(u), p.cols);
+        for (int u = 0; u < U; ++u) add[u] = load_unit_once(p.add + row * p.ldadd, column<L>(u, t), p.cols);
     }
 }
 
-__device__ __forceinline__ void x_values(u32x4v x, bool kept, float (&v)[8]) {
-    if (kept)
-        act8_unpack8(x.xy, act8_scale(x.z), v);
-    else
-        widen(x, v);
+// A kept unit's values as bf16, which holds them exactly (act8.h).
+__device__ __forceinline__ u32x4v kept_unit(u32x4v x) {
+    const float f = act8_scale(x.z);
+    return u32x4v{act8_bf16x2<false>(x.x, f), act8_bf16x2<true>(x.x, f), act8_bf16x2<false>(x.y, f),
+                  act8_bf16x2<true>(x.y, f)};
 }
 
-// A workgroup takes a chunk of rows, kRows of them at a time, and keeps its
-// columns' sums of dy n and (DB) of dy in registers; the next rows' loads are in
-// flight while these are worked on, but for rows of 1024 lanes, which have half
-// the registers (and read w again for each row).
+// A workgroup takes every gridDim-th row (kRows of them at a time), so that what
+// the chip works on at a time is one piece of memory, and keeps its columns'
+// sums of dy n and (DB) of dy in registers.  The next rows' loads are in flight
+// while these are worked on, as far as the registers go: of wide rows w is read
+// again for each row, `add` is not read ahead, and of the widest nothing is.
 template <int L, int U, bool LAYER, bool DB>
 __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_kernel(NormBackward p) {
     constexpr int kGroup = L > kThreads ? L : kThreads, kRows = kGroup / L;
@@ -317,29 +334,44 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
     constexpr int kSums = kRows > 1 ? (kRows - 1) * L * U * 8 : 1;
     __shared__ __attribute__((aligned(16))) float lds[kBox > kSums ? kBox : kSums];
     lds_float* box = (lds_float*)lds;
-    const bool kept = p.x_kept;
-    constexpr bool kAhead = L < 1024;
-    const int64_t end = min(p.rows, ((int64_t)blockIdx.x + 1) * p.chunk);
-    int64_t row = blockIdx.x * p.chunk + threadIdx.x / L;
+    // what a lane holds, in registers, of the L = 1024 lanes' 128 or the others' 256
+    constexpr int kHeld = 40 + (DB ? 32 : 24) * U, kMost = L == 1024 ? 124 : 248;
+    constexpr bool kAhead = kHeld + 8 * U <= kMost, kAheadAdd = kHeld + 12 * U <= kMost;
+    constexpr bool kKeepW = kAhead;
+    int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / L;
+    const int64_t stride = (int64_t)gridDim.x * kRows;
     u32x4v w[U];
     auto load_w = [&]() __attribute__((always_inline)) {
+        const uint32_t t = this_thread();
 #pragma unroll
-        for (int u = 0; u < U; ++u) w[u] = p.w ? load_unit(p.w, column<L>(u), p.cols) : (u32x4v)0u;
+        for (int u = 0; u < U; ++u) w[u] = p.w ? load_unit(p.w, column<L>(u, t), p.cols) : (u32x4v)0u;
     };
-    if (kAhead) load_w();
+    if (kKeepW) load_w();
     float dw[U][8] = {}, db[DB ? U : 1][8] = {};
     RowParts<U> next;
-    if (kAhead && row < end) load_row<L, U>(p, row, next);
+    u32x4v next_add[U], add[U];
+    if (kAhead && row < p.rows) load_row<L, U>(p, row, next);
+    if (kAheadAdd && row < p.rows) load_add<L, U>(p, row, next_add);
     int slot = 0;
 #pragma unroll 1
-    for (; row < end; row += kRows) {
+    for (; row < p.rows; row += stride) {
         RowParts<U> now;
-        if constexpr (kAhead) {
+        if constexpr (kAhead)
             now = next;
-            if (row + kRows < end) load_row<L, U>(p, row + kRows, next);
-        } else {
+        else
             load_row<L, U>(p, row, now);
-            load_w();
+        if constexpr (!kKeepW) load_w();
+        if constexpr (kAheadAdd) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) add[u] = next_add[u];
+        } else {
+            load_add<L, U>(p, row, add);
+        }
+        if (kAhead && row + stride < p.rows) load_row<L, U>(p, row + stride, next);
+        if (kAheadAdd && row + stride < p.rows) load_add<L, U>(p, row + stride, next_add);
+        if (p.x_kept) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) now.x[u] = kept_unit(now.x[u]);
         }
         // a slot is written again two rows later, with a barrier in between
         lds_float* mine = box + (L > 64 ? slot * 6 * (L / 64) : 0);
@@ -349,8 +381,8 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
             float s[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                float v[8], d[8], f[8];
-                x_values(now.x[u], kept, v);
+                    float v[8], d[8], f[8];
+                widen(now.x[u], v);
                 widen(now.dy[u], d);
                 widen(w[u], f);
 #pragma unroll
@@ -368,11 +400,12 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
             mine += L > 64 ? 2 * (L / 64) : 0;
         }
         float s[LAYER ? 3 : 2] = {};
+        const uint32_t t = this_thread();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float v[8], d[8], f[8];
-            x_values(now.x[u], kept, v);
-            if constexpr (LAYER) centre(v, mu, column<L>(u), p.cols);
+            widen(now.x[u], v);
+            if constexpr (LAYER) centre(v, mu, column<L>(u, t), p.cols);
             widen(now.dy[u], d);
             widen(w[u], f);
 #pragma unroll
@@ -389,12 +422,13 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
         const float off = LAYER ? s[LAYER ? 2 : 0] * p.inv_cols : 0.0f;
         const float r = inv_sqrt(variance(s[0] * p.inv_cols, off) + p.eps);
         // mean(c n) n = (r^2 mean(c (x - mu))) (x - mu)
+        const uint32_t t2 = this_thread();
         const float along = r * (r * __builtin_fmaf(-off, mean_c, s[1] * p.inv_cols));
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int32_t c = column<L>(u);
+            const uint32_t c = column<L>(u, t2);
             float v[8], d[8], f[8];
-            x_values(now.x[u], kept, v);
+            widen(now.x[u], v);
             if constexpr (LAYER) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] = v[k] - mu - off;
@@ -407,11 +441,11 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
                 for (int k = 0; k < 8; ++k)
                     g[k] = r * (__builtin_fmaf(-along, v[k], d[k] * f[k]) - mean_c);
                 if (p.add) {
-                    widen(now.add[u], f);
+                    widen(add[u], f);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) g[k] += f[k];
                 }
-                store8(p.dx + row * p.lddx + c, p.cols - c, g);
+                store8(p.dx + row * p.lddx + c, (int64_t)p.cols - c, g);
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) dw[u][k] = __builtin_fmaf(d[k], v[k] * r, dw[u][k]);
@@ -423,6 +457,7 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
     }
     // the sums of the workgroup's other groups of lanes, then out
     auto finish = [&](auto& sum, float* sums, uint16_t* out) __attribute__((always_inline)) {
+        const uint32_t t = threadIdx.x;
         if constexpr (kRows > 1) {
             __syncthreads();
             const int group = threadIdx.x / L, lane = threadIdx.x % L;
@@ -443,10 +478,10 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int32_t c = column<L>(u);
+            const uint32_t c = column<L>(u, t);
             if (c >= p.cols) break;
             if (out) {
-                store8(out + c, p.cols - c, sum[u]);
+                store8(out + c, (int64_t)p.cols - c, sum[u]);
             } else {
                 float* to = sums + (int64_t)blockIdx.x * p.sums_pitch + c;
 #pragma unroll
@@ -505,9 +540,10 @@ constexpr int64_t kMaxNormCols = 32768;  // 4096 units: 1024 lanes of 4
 constexpr int64_t kMaxNormRows = (int64_t)1 << 27;  // 16 lanes each in one grid
 constexpr float kMinEps = 1e-30f;
 
-// Lanes and units a row takes: the fewest lanes whose units hold it.
+// Lanes and units a row takes (the first form that holds it) and, backward, how
+// many workgroups at most, each of which leaves a row of sums.
 struct RowShape {
-    int lanes, units;
+    int lanes, units, groups;
 };
 
 using ForwardKernel = void (*)(NormForward);
@@ -523,21 +559,29 @@ struct BackwardForm {
 };
 
 #define TIDE_FORWARD_FORM(L, U) \
-    {{L, U}, norm_forward_kernel<L, U, false>, norm_forward_kernel<L, U, true>}
-#define TIDE_BACKWARD_FORM(L, U)                                                    \
-    {{L, U}, norm_backward_kernel<L, U, false, false>, norm_backward_kernel<L, U, true, false>, \
+    {{L, U, 0}, norm_forward_kernel<L, U, false>, norm_forward_kernel<L, U, true>}
+#define TIDE_BACKWARD_FORM(L, U, GROUPS)                                                         \
+    {{L, U, GROUPS}, norm_backward_kernel<L, U, false, false>, norm_backward_kernel<L, U, true, false>, \
      norm_backward_kernel<L, U, false, true>, norm_backward_kernel<L, U, true, true>}
 
 const ForwardForm kForwardForms[] = {
     TIDE_FORWARD_FORM(16, 1),  TIDE_FORWARD_FORM(64, 1),  TIDE_FORWARD_FORM(64, 2),
     TIDE_FORWARD_FORM(256, 1), TIDE_FORWARD_FORM(256, 2), TIDE_FORWARD_FORM(256, 3),
-    TIDE_FORWARD_FORM(256, 4), TIDE_FORWARD_FORM(512, 3), TIDE_FORWARD_FORM(512, 4),
+    TIDE_FORWARD_FORM(512, 2), TIDE_FORWARD_FORM(512, 3), TIDE_FORWARD_FORM(512, 4),
     TIDE_FORWARD_FORM(1024, 3), TIDE_FORWARD_FORM(1024, 4)};
+// The most lanes for a row (one unit each as far as they go) and few workgroups,
+// each of which writes a row of sums that another launch reads: us for 8192 rows
+// of 5120 with rms, 1024 lanes and 256 workgroups 61.8, 512 workgroups 66.5, 512
+// lanes of 2 units 100, 256 of 3 and 512 workgroups 75.8; 777 rows with layer norm
+// and both sums 18.5, 256 lanes of 3 20.3.  Rows of 2048 (8192 of them): 256
+// lanes and 512 workgroups 29.4, 1024 workgroups 30.9, 512 lanes and 256 36.8.
+// Past 16384 columns 512 lanes have the registers that 1024 have not: 2300 rows
+// of 28672 118 us, layer norm with both sums 152 (1024 lanes of 4: 118 and 231).
 const BackwardForm kBackwardForms[] = {
-    TIDE_BACKWARD_FORM(16, 1),  TIDE_BACKWARD_FORM(64, 1),  TIDE_BACKWARD_FORM(64, 2),
-    TIDE_BACKWARD_FORM(256, 1), TIDE_BACKWARD_FORM(256, 2), TIDE_BACKWARD_FORM(256, 3),
-    TIDE_BACKWARD_FORM(512, 2), TIDE_BACKWARD_FORM(512, 3), TIDE_BACKWARD_FORM(1024, 2),
-    TIDE_BACKWARD_FORM(1024, 3), TIDE_BACKWARD_FORM(1024, 4)};
+    TIDE_BACKWARD_FORM(16, 1, 512),  TIDE_BACKWARD_FORM(64, 1, 512),   TIDE_BACKWARD_FORM(64, 2, 512),
+    TIDE_BACKWARD_FORM(256, 1, 512), TIDE_BACKWARD_FORM(512, 1, 256),  TIDE_BACKWARD_FORM(1024, 1, 256),
+    TIDE_BACKWARD_FORM(1024, 2, 256), TIDE_BACKWARD_FORM(512, 5, 256), TIDE_BACKWARD_FORM(512, 6, 256),
+    TIDE_BACKWARD_FORM(512, 7, 256), TIDE_BACKWARD_FORM(512, 8, 256)};
 
 template <typename Form, size_t N>
 const Form& form_of(const Form (&forms)[N], int64_t cols) {
@@ -581,7 +625,7 @@ extern "C" tide_status tide_norm_forward(const tide_norm_forward_args* args, tid
     p.x = static_cast<const uint16_t*>(a.x);
     p.ldx = a.ldx;
     p.rows = T;
-    p.cols = (int32_t)C;
+    p.cols = (uint32_t)C;
     p.eps = a.eps;
     p.inv_cols = 1.0f / (float)C;
     p.w = static_cast<const uint16_t*>(a.weight);
@@ -600,7 +644,7 @@ namespace {
 
 struct NormBackwardPlan {
     const BackwardForm* form;
-    int64_t chunk, chunks, pitch;
+    int64_t groups, pitch;  // workgroups; columns of their sums
     float *dw = nullptr, *db = nullptr;
     int64_t bytes;
 };
@@ -633,15 +677,13 @@ NormBackwardPlan plan_backward(const tide_norm_backward_args& a, void* ws) {
     b.form = &form_of(kBackwardForms, a.cols);
     const int threads = threads_of(b.form->shape);
     const int64_t at_once = threads / b.form->shape.lanes;
-    // as many workgroups as the chip holds at two (of 1024 threads) to four
-    // (of 256) a compute unit
-    const int64_t groups = 256 * std::max(1, std::min(4, 1024 / threads));
-    b.chunk = round_up(std::max<int64_t>(1, ceil_div(a.rows, groups)), at_once);
-    b.chunks = ceil_div(a.rows, b.chunk);
+    const int64_t most = b.form->shape.groups;
+    const int64_t each = std::max<int64_t>(1, ceil_div(a.rows, most * at_once));
+    b.groups = ceil_div(a.rows, each * at_once);
     b.pitch = round_up(a.cols, 8);
-    if (b.chunks > 1) {
-        if (a.dweight) b.dw = c.take<float>(b.chunks * b.pitch);
-        if (a.dbias) b.db = c.take<float>(b.chunks * b.pitch);
+    if (b.groups > 1) {
+        if (a.dweight) b.dw = c.take<float>(b.groups * b.pitch);
+        if (a.dbias) b.db = c.take<float>(b.groups * b.pitch);
     }
     b.bytes = c.used;
     return b;
@@ -696,24 +738,23 @@ extern "C" tide_status tide_norm_backward(const tide_norm_backward_args* args, v
     }
     p.dw_sums = b.dw;
     p.db_sums = b.db;
-    if (b.chunks <= 1) {
+    if (b.groups <= 1) {
         p.dweight = static_cast<uint16_t*>(a.dweight);
         p.dbias = static_cast<uint16_t*>(a.dbias);
     }
     p.rows = T;
-    p.chunk = b.chunk;
     p.sums_pitch = b.pitch;
-    p.cols = (int32_t)C;
+    p.cols = (uint32_t)C;
     p.eps = a.eps;
     p.inv_cols = 1.0f / (float)C;
     const bool layer = a.kind == TIDE_NORM_LAYER;
     const BackwardForm& f = *b.form;
     auto k = layer ? a.dbias ? f.layer_db : f.layer : a.dbias ? f.rms_db : f.rms;
     // without rows one workgroup writes the empty sums
-    const int64_t grid = T ? b.chunks : a.dweight || a.dbias ? 1 : 0;
+    const int64_t grid = T ? b.groups : a.dweight || a.dbias ? 1 : 0;
     TIDE_TRY(launch(k, grid, threads_of(f.shape), stream, p));
-    if (b.chunks <= 1 || !(b.dw || b.db)) return TIDE_OK;
+    if (b.groups <= 1 || !(b.dw || b.db)) return TIDE_OK;
     return launch(norm_sums_kernel, ceil_div(C, 64) * ((b.dw ? 1 : 0) + (b.db ? 1 : 0)),
-                  64 * kSumWaves, stream, (const float*)b.dw, (const float*)b.db, b.chunks, b.pitch, C,
+                  64 * kSumWaves, stream, (const float*)b.dw, (const float*)b.db, b.groups, b.pitch, C,
                   static_cast<uint16_t*>(a.dweight), static_cast<uint16_t*>(a.dbias));
 }
