@@ -35,7 +35,7 @@ namespace {
 // What happens to finished g and u.  I: rows of the two matrices together as the
 // tile loop counts them, J: tokens.
 struct GatedEpilogue {
-    static constexpr bool kPairs = true, kNarrow = true;
+    static constexpr bool kPairs = true;
     int64_t I, J, N;
     uint16_t* out;
     int64_t ldo;
@@ -471,7 +471,7 @@ BackwardPlan plan_backward(const tide_gated_backward_args& a, void* ws) {
     b.up = {a.up, K, dx ? N : 0, K};
     b.gate.plan(c);
     b.up.plan(c);
-    b.g = choose_gradients(T, 2 * b.turn, K, dx, dw);
+    b.g = choose_gated_gradients(T, b.turn, K, dx, dw);
     // the 256-wide tiles read x from here, widened (tile_product.h)
     if (dw && b.g.weight.bi == 256) b.x = c.take<uint16_t>(T * act8_pitch(K));
     int64_t floats = 0;

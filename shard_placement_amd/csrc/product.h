@@ -137,9 +137,18 @@ __device__ __forceinline__ void wave_lds_order() { asm volatile("s_waitcnt lgkmc
 template <int BI, int BJ, int K>
 constexpr int kProductLds = 2 * (BI + BJ) * K * 2;
 
+// Forms whose tiles are a ring (tile_product.h), and how many: as many as 160 KB
+// hold.
+constexpr bool in_ring(Layout a, int h) { return h == 2 && (a == kPairRows || a == kPairRowsOnce); }
+template <int BI, int BJ, int K>
+constexpr int kRing = (160 << 10) / ((BI + BJ) * K * 2);
+template <int BI, int BJ, int K, Layout CA, int H>
+constexpr int kTileLds = in_ring(CA, H) ? kRing<BI, BJ, K> * (BI + BJ) * K * 2 : kProductLds<BI, BJ, K> * H;
+
 // The tile of workgroup `block` of `blocks`.  H = 2: the contraction in two
-// halves, each by WI * WJ waves with tiles in LDS of their own, whose sums are
-// added in LDS; each set of waves then finishes half of the tile.
+// halves, each by WI * WJ waves with tiles in LDS of their own (in a ring: half of
+// each tile, which they share), whose sums are added in
+// LDS; each set of waves then finishes half of the tile.
 template <int BI, int BJ, int K, int WI, int WJ, Layout CA, Layout CB, int H, typename P>
 __device__ __forceinline__ void product_tile(const P& p, uint32_t block, uint32_t blocks,
                                              TIDE_LDS char* lds) {
@@ -149,8 +158,12 @@ __device__ __forceinline__ void product_tile(const P& p, uint32_t block, uint32_
     tile_at(p, block, blocks, &ti, &tj, &sp);
     const int64_t i0 = (int64_t)ti * BI, j0 = (int64_t)tj * BJ;
     f32x4v acc[TI][TJ];
-    tile_loop<BI, BJ, K, WI, WJ, CA, CB, H>(p.A, p.B, p.depth, sp * p.split_depth,
-                                            min(p.depth, (sp + 1) * p.split_depth), i0, j0, lds, acc);
+    const int64_t k0 = sp * p.split_depth, k1 = min(p.depth, (sp + 1) * p.split_depth);
+    constexpr int kLds = kTileLds<BI, BJ, K, CA, H>;
+    if constexpr (in_ring(CA, H))
+        ring_loop<BI, BJ, K, WI, WJ, CA, CB, kRing<BI, BJ, K>>(p.A, p.B, p.depth, k0, k1, i0, j0, lds, acc);
+    else
+        tile_loop<BI, BJ, K, WI, WJ, CA, CB, H>(p.A, p.B, p.depth, k0, k1, i0, j0, lds, acc);
 
     // The accumulators pass through LDS, 16 rows of a wave at a time, so that
     // each lane ends with 8 consecutive columns and a row's stores are whole
@@ -160,7 +173,7 @@ __device__ __forceinline__ void product_tile(const P& p, uint32_t block, uint32_
     constexpr int kStaging = WI * WJ * H * 16 * kPitch * 4;
     constexpr int kDone = H == 2 && TJ > 1 ? TJ / 2 : TJ;  // 16-row pieces that a wave finishes
     static_assert(H == 1 || TJ == 1 || TJ % 2 == 0, "the halves share the tile");
-    static_assert(kStaging <= kProductLds<BI, BJ, K> * H, "the staging fits");
+    static_assert(kStaging <= kLds, "the staging fits");
     tile_barrier(lds, lds);
     // (what follows from the thread is worked out here, not kept in registers
     // through the loop)
@@ -171,7 +184,7 @@ __device__ __forceinline__ void product_tile(const P& p, uint32_t block, uint32_
     if constexpr (H == 2) {
         // what the other half's wave finishes goes to it; staging lies behind
         constexpr int kPiece = 64 * 16, kWave = TI * kDone * kPiece;
-        static_assert(kStaging + 2 * WI * WJ * kWave <= 2 * kProductLds<BI, BJ, K>, "both fit");
+        static_assert(kStaging + 2 * WI * WJ * kWave <= kLds, "both fit");
         TIDE_LDS char* box = lds + kStaging + wave * kWave + lane * 16;
         constexpr int kOther = WI * WJ * kWave;
         if (half) {
@@ -260,7 +273,7 @@ __device__ __forceinline__ void product_tile(const P& p, uint32_t block, uint32_
 
 template <int BI, int BJ, int K, int WI, int WJ, Layout CA, Layout CB, int H, typename P>
 __global__ __launch_bounds__(WI* WJ * 64 * H, BI == 256 ? 2 : 1) void product_kernel(P p) {
-    __shared__ __attribute__((aligned(1024))) char lds[kProductLds<BI, BJ, K> * H];
+    __shared__ __attribute__((aligned(1024))) char lds[kTileLds<BI, BJ, K, CA, H>];
     product_tile<BI, BJ, K, WI, WJ, CA, CB, H>(p, blockIdx.x, gridDim.x, (TIDE_LDS char*)lds);
 }
 
@@ -482,6 +495,25 @@ void (*kernel_of())(P) {
         return product_kernel<BI, BJ, K, WI, WJ, BI == 256 ? kColumns : kKept, kColumns, H, P>;
 }
 
+// The forms of 128 rows of two matrices' rows in turn: a wave takes 64 of them, so
+// that it holds whole blocks of the output's checkpoints.
+template <typename P, int BJ, int K, int WJ>
+void (*ring_of(bool once))(P) {
+    return once ? product_kernel<128, BJ, K, 2, WJ, kPairRowsOnce, kRows, 2, P>
+                : product_kernel<128, BJ, K, 2, WJ, kPairRows, kRows, 2, P>;
+}
+template <typename P>
+void (*pairs_of(const Shape& s, bool once, int* threads))(P) {
+    *threads = 512;
+    if (s.bj == 128 && s.halves == 2) return ring_of<P, 128, 64, 2>(once);
+    if (s.bj == 64) return ring_of<P, 64, 128, 2>(once);
+    if (s.bj == 32 && s.halves == 2) return ring_of<P, 32, 128, 2>(once);
+    *threads = 256;
+    if (s.bj == 128) return kernel_of<kForward, P, 128, 128, 64, 2, 2>();
+    if (s.bj == 32) return kernel_of<kForward, P, 128, 32, 256, 2, 2>();
+    return ring_of<P, 16, 128, 1>(once);
+}
+
 template <typename P>
 void set_shape(P* p, const Shape& s, float* partial) {
     p->tiles_i = s.tiles_i;
@@ -514,6 +546,8 @@ tide_status run_product(P p, const Shape& s, float* partial, tide_stream_t strea
             : s.bj == 192 ? kernel_of<KIND, P, 256, 192, 64, 2, 4>()
                           : kernel_of<KIND, P, 256, 128, 64, 2, 4>();
         threads = 512;
+    } else if constexpr (kPairsOut<P>) {
+        k = pairs_of<P>(s, past_the_cache(p.e.I, p.depth) && s.tiles_j == 1, &threads);
     } else if (s.bj == 128) {
         k = s.halves == 2 ? kernel_of<KIND, P, 128, 128, 64, 2, 2, 2>()
                           : kernel_of<KIND, P, 128, 128, 64, 2, 2>();
@@ -522,15 +556,6 @@ tide_status run_product(P p, const Shape& s, float* partial, tide_stream_t strea
     } else if (s.bj == 64) {
         k = s.halves == 2 ? kernel_of<KIND, P, 128, 64, 64, 2, 2, 2>()
                           : kernel_of<KIND, P, 128, 64, 64, 2, 2>();
-    } else if constexpr (kPairsOut<P>) {
-        // a wave takes 64 rows of A, so that it holds whole blocks of the
-        // output's checkpoints: 16 rows of B are two sets of two waves
-        if (s.bj == 32)
-            k = s.bk == 256     ? kernel_of<KIND, P, 128, 32, 256, 2, 2>()
-                : s.halves == 2 ? kernel_of<KIND, P, 128, 32, 64, 2, 2, 2>()
-                                : kernel_of<KIND, P, 128, 32, 64, 2, 2>();
-        else
-            k = kernel_of<KIND, P, 128, 16, 64, 2, 1, 2>(), threads = 256;
     } else if (s.bj == 32) {
         k = s.halves == 2 ? kernel_of<KIND, P, 128, 32, 64, 4, 1, 2>()
                           : kernel_of<KIND, P, 128, 32, 64, 4, 1>();
@@ -567,8 +592,9 @@ tide_status run_gradients(const Gradients& g, PW w, bool want_w, PX x, bool want
                                                             : wide_pair_kernel<256, 192, PW, PX>
                         : g.in.bj == 256   ? wide_pair_kernel<192, 256, PW, PX>
                                            : wide_pair_kernel<192, 192, PW, PX>;
-            return launch(wide, n_w + n_x, 512, stream, w, x, (int32_t)(x_first ? n_x : 0),
-                          (int32_t)(x_first ? 0 : n_w));
+            TIDE_TRY(launch(wide, n_w + n_x, 512, stream, w, x, (int32_t)(x_first ? n_x : 0),
+                            (int32_t)(x_first ? 0 : n_w)));
+            return run_join(x, stream);
         }
         const int halves = n_w + n_x <= kCus ? 2 : 1;
         auto k = halves == 2 ? pair_of<2, PW, PX>(g.in.bj) : pair_of<1, PW, PX>(g.in.bj);

@@ -75,7 +75,8 @@ inline double product_us(Kind kind, const TileCost& c, const Shape& s, int64_t I
     const double steps = (double)steps_of(s, depth);
     double us;
     if (c.halves == 2) {
-        us = rounds * (std::ceil(steps / 2) * c.step + c.rest);
+        const double used = (double)groups / (rounds * kCus);
+        us = rounds * (std::ceil(steps / 2) * (c.step + c.power * used * used) + c.rest);
     } else if (c.bi == 128) {
         const double pairs = (double)(int64_t)(rounds / 2), single = rounds - 2 * pairs;
         us = pairs * (steps * kPairStep + c.rest) + single * (steps * c.step + c.rest);
@@ -112,7 +113,10 @@ inline double product_us(Kind kind, const TileCost& c, const Shape& s, int64_t I
 // (dx) and 0.91 (dW) of what they take in the median, and the choice is 2% off
 // the best, 20% at worst.  Operand bytes are not among the costs: a weight of
 // hundreds of MB with 65 to 256 tokens takes up to half as long again.
-inline Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth, double* estimate = nullptr) {
+constexpr int kTileForms = 5;
+
+inline Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth, double* estimate = nullptr,
+                    const TileCost* tiles = kTiles) {
     Shape s = {};
     s.bk = 64;
     s.halves = 1;
@@ -140,7 +144,8 @@ inline Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth, double* esti
     }
     const int64_t most = std::min<int64_t>(16, std::max<int64_t>(1, ceil_div(depth, kSplitUnit)));
     double best = 0.0;
-    for (const TileCost& c : kTiles) {
+    for (int f = 0; f < kTileForms; ++f) {
+        const TileCost& c = tiles[f];
         for (int64_t splits = 1; splits <= most; ++splits) {
             Shape t = s;
             t.bi = c.bi;
@@ -161,13 +166,40 @@ inline Shape choose(Kind kind, int64_t I, int64_t J, int64_t depth, double* esti
     return s;
 }
 
+// Operands of more bytes than the 256 MB cache holds.
+inline bool past_the_cache(int64_t rows, int64_t depth) { return rows * depth > ((int64_t)128 << 20); }
+
 // The same for a product with the rows of two matrices in turn (I: both), whose
-// waves hold whole checkpoint blocks of the output: 16 rows are always two sets
-// of waves, and reading 512 bytes of a row at a time takes tiles of 32.
+// 128-wide tiles are rings (tile_product.h; halves = 2).
+//
+// Up to 64 tokens: the contraction is split to about 128 workgroups and not below
+// 512 elements each.  Half of the compute units with rings read as fast as all of
+// them and leave fewer sums to join: us at 1, 2, 4 splits for 16 x 4096 x 4096 (64
+// tiles) 17.9, 17.4, 19.9; 5 x 1001 x 8192 (16 tiles) at 2, 4, 8 splits 20.8, 15.2,
+// 14.6; 5 x 768 x 2048 (12) at 1, 2, 4, 8 10.4, 10.3, 10.0, 10.6.  Of weights past the
+// cache with more tiles than compute units, up to 32 tokens read 512 bytes of a row
+// at a time instead (24 x 28672 x 8192 147.5 us, with rings 155; 24 x 13824 x 5120, 216
+// tiles, 45.4 with rings, 50.3 so).
+//
+// More tokens: the least estimate, as above, with the ring's costs for two sets
+// of waves (0.38 us a step of 64 with a quarter of the compute units, 0.50 with
+// all: 512 x 768 x 2048 18.1 us, 512 x 4096 x 4096 36.8).
+constexpr TileCost kRingTiles[] = {kTiles[0], kTiles[1], kTiles[2], kTiles[3], {128, 128, 2, 0.76, 0.24, 5.5}};
+
 inline Shape choose_gated(int64_t I, int64_t J, int64_t depth) {
-    Shape s = choose(kForward, I, J, depth);
-    if (s.bk == 256) s.bj = 32;
-    else if (s.bj == 16) s.halves = 2;
+    if (J > 64) return choose(kForward, I, J, depth, nullptr, kRingTiles);
+    Shape s = {};
+    s.bi = 128;
+    s.bj = J <= 16 ? 16 : J <= 32 ? 32 : 64;
+    s.bk = 128;
+    s.halves = 2;
+    const int64_t tiles = ceil_div(I, s.bi);
+    if (J <= 32 && tiles > kCus && past_the_cache(I, depth)) {
+        s.bj = 32;
+        s.bk = 256;
+        s.halves = 1;
+    }
+    set_split(&s, I, J, depth, std::min(std::max<int64_t>(1, kCus / 2 / tiles), std::max<int64_t>(1, depth / 512)));
     return s;
 }
 
@@ -177,18 +209,25 @@ inline Shape choose_gated(int64_t I, int64_t J, int64_t depth) {
 // (Measured, both gradients with dz, against two launches: 2048 x 13824 x 5120
 // 496 us, 600; 8192 x 8192 x 1024 272, 331; 3000 x 1280 x 8192 129, 141; and 748
 // against 729 for 700 x 28672 x 8192, whose estimates were 0.7% apart.)
+//
+// most: splits of dx's contraction that are looked at.  The layer product takes
+// none (its sums keep their order); the gated block's dx has twice the terms, few
+// tiles of which are long: its splits fill the chip together with dW's tiles, and
+// the join is cheap beside them.
 inline bool choose_pair(int64_t T, int64_t N, int64_t K, double best, Shape* in, Shape* weight,
-                        bool* in_first) {
+                        bool* in_first, int64_t most = 1) {
     constexpr int kWide = 2;  // 256 x 256 and 256 x 192
     bool found = false;
     best *= 0.97;
     for (int a = 0; a < kWide; ++a) {
-        for (int b = 0; b < kWide; ++b) {
+        for (int64_t bs = 0; bs < kWide * most; ++bs) {
+            const int b = (int)(bs % kWide);
             const TileCost &cx = kTiles[a], &cw = kTiles[b];
             Shape x = {cx.bi, cx.bj, 64, 1, 0, 0, 1, 0}, w = {cw.bi, cw.bj, 64, 1, 0, 0, 1, 0};
-            set_split(&x, K, T, N, 1);
+            set_split(&x, K, T, N, 1 + bs / kWide);
             set_split(&w, K, N, T, 1);
-            const int64_t nx = (int64_t)x.tiles_i * x.tiles_j, nw = (int64_t)w.tiles_i * w.tiles_j;
+            const int64_t nx = (int64_t)x.tiles_i * x.tiles_j * x.splits, nw = (int64_t)w.tiles_i * w.tiles_j;
+            if (x.splits < 1 + bs / kWide) continue;
             const double tx = wide_tile_us(cx, (double)steps_of(x, N), 1.0),
                          tw = wide_tile_us(cw, (double)steps_of(w, T), 1.0);
             const double longer = std::max(tx, tw), shorter = std::min(tx, tw);
@@ -203,6 +242,8 @@ inline bool choose_pair(int64_t T, int64_t N, int64_t K, double best, Shape* in,
                 n_short -= (kCus - rest) * (int64_t)(longer / shorter);
             }
             if (n_short > 0) us += (double)ceil_div(n_short, kCus) * shorter;
+            if (x.splits > 1)  // the partial sums, as in product_us
+                us += 4.0 * cx.bi * cx.bj / 40e3 + 4.0 + 4.0 * (double)x.splits * (double)K * (double)T / 5.5e6;
             if (us < best) {
                 best = us;
                 *in = x;
@@ -244,7 +285,8 @@ struct Gradients {
     bool in_first;  // of 256-wide tiles in one launch: dx's are the longer ones
 };
 
-inline Gradients choose_gradients(int64_t T, int64_t N, int64_t K, bool dx, bool dw) {
+inline Gradients choose_gradients(int64_t T, int64_t N, int64_t K, bool dx, bool dw,
+                                  int64_t pair_splits = 1) {
     const int64_t width = round_up(N, 8);
     Gradients g = {};
     double in_us = 0.0, w_us = 0.0;
@@ -269,8 +311,15 @@ inline Gradients choose_gradients(int64_t T, int64_t N, int64_t K, bool dx, bool
         if (g.pair) g.in = in;
     }
     if (dx && dw && !g.pair && in_us > 0.0 && w_us > 0.0)
-        g.pair = choose_pair(T, width, K, in_us + w_us, &g.in, &g.weight, &g.in_first);
+        g.pair = choose_pair(T, width, K, in_us + w_us, &g.in, &g.weight, &g.in_first,
+                             pair_splits);
     return g;
+}
+
+// The gated block's gradients' products: of both matrices' dz side by side, `turn`
+// columns each.
+inline Gradients choose_gated_gradients(int64_t T, int64_t turn, int64_t K, bool dx, bool dw) {
+    return choose_gradients(T, 2 * turn, K, dx, dw, 16);
 }
 
 }  // namespace tide

@@ -56,10 +56,12 @@ typedef float f32x4v __attribute__((ext_vector_type(4)));
 // with the same element of both products.  "Pair columns": columns, the
 // contraction going through the first and then, from element `turn` (a multiple
 // of 64, `depth` or more; what lies between reads as 0) on, through the second.
-enum Layout { kRows, kColumns, kKept, kPairRows, kPairColumns };
+// "Pair rows once": pair rows that no other workgroup reads and that come past the
+// caches.
+enum Layout { kRows, kColumns, kKept, kPairRows, kPairColumns, kPairRowsOnce };
 
 // The contraction index runs across memory.
-constexpr bool across(Layout l) { return l != kRows && l != kPairRows; }
+constexpr bool across(Layout l) { return l == kColumns || l == kKept || l == kPairColumns; }
 
 struct Operand {
     const void* p;
@@ -337,6 +339,10 @@ struct StagerOf<N, K, WAVES, kPairRows, ONCE> {
     using type = PairRowsStager<N, K, WAVES, ONCE>;
 };
 template <int N, int K, int WAVES, bool ONCE>
+struct StagerOf<N, K, WAVES, kPairRowsOnce, ONCE> {
+    using type = PairRowsStager<N, K, WAVES, true>;
+};
+template <int N, int K, int WAVES, bool ONCE>
 struct StagerOf<N, K, WAVES, kPairColumns, ONCE> {
     using type = PairColumnsStager<N, K, WAVES>;
 };
@@ -347,6 +353,9 @@ template <int N, int K, Layout L>
 struct Reader {
     template <int S>
     __device__ __forceinline__ static bf16x8 read(const TIDE_LDS char* lds, int m0, int lane) {
+        return read(lds, m0, lane, S);
+    }
+    __device__ __forceinline__ static bf16x8 read(const TIDE_LDS char* lds, int m0, int lane, int S) {
         if constexpr (across(L)) {
             constexpr int kRow = 2 * N;
             const int g = lane >> 4, i = lane & 15;
@@ -552,6 +561,101 @@ __device__ __forceinline__ void tile_loop(const OA& A, const Operand& B, int64_t
                                                valid, wi, wj, lane, acc);
             at ^= kTile;
         }
+    }
+}
+
+// All but the latest N loads of this wave have landed.
+template <int N>
+__device__ __forceinline__ void wait_loads(const TIDE_LDS char* tile) {
+    static_assert(N < 64, "the counter has 6 bits");
+    asm volatile("s_waitcnt vmcnt(%1)" ::"s"(tile), "n"(N) : "memory");
+}
+// Every LDS read of every wave has returned, and what each has waited for is
+// there for all.
+__device__ __forceinline__ void ring_barrier(const TIDE_LDS char* a, const TIDE_LDS char* b) {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::"s"(a), "s"(b) : "memory");
+}
+
+// A step of a ring: loads into one tile, the set's half of another.
+template <int BI, int BJ, int K, int TI, int TJ, Layout CA, Layout CB, typename SA, typename SB>
+__device__ __forceinline__ void ring_step(TIDE_LDS char* __restrict__ next,
+                                          const TIDE_LDS char* __restrict__ now, SA& sa, SB& sb,
+                                          int64_t valid, int wi, int wj, int lane, int set,
+                                          f32x4v (&acc)[TI][TJ]) {
+    sa.stage(next, valid);
+    sb.stage(next + SA::kBytes, valid);
+#pragma unroll
+    for (int k = 0; k < K / 64; ++k) {
+        bf16x8 a[TI], b[TJ];
+#pragma unroll
+        for (int t = 0; t < TI; ++t)
+            a[t] = Reader<BI, K, CA>::read(now, wi + 16 * t, lane, set * (K / 64) + k);
+#pragma unroll
+        for (int t = 0; t < TJ; ++t)
+            b[t] = Reader<BJ, K, CB>::read(now + SA::kBytes, wj + 16 * t, lane, set * (K / 64) + k);
+        multiply_part<TI, TJ>(a, b, acc);
+    }
+}
+
+// The same loop with R tiles in LDS, R - 1 of them under way: a step waits for the
+// oldest only, so the loads never run dry.  Two sets of WI * WJ waves share the
+// tiles, each with half of a tile's contraction.  Past the contraction's end
+// loads are issued all the same, outside the operands' descriptors (they read
+// as 0), so that every step has as many to wait for.
+//
+// For rows of two matrices (the gated block's forward product, where the plain
+// step's pair of tiles leaves a compute unit waiting for memory): us with the
+// ring and, before it, with tiles in pairs, T x N x K: 16 x 4096 x 4096 17.4 and
+// 27.8, 16 x 1001 x 8192 15.2 and 25.4, 64 x 13824 x 5120 51.0 and 69.9, 1003 x 768 x
+// 2048 18.4 and 22.5.  Tiles of 128 contraction elements against 64: 49.8 and
+// 51.3 for 16 x 13824 x 5120.  Operands across memory gain nothing (dx of 64 x
+// 4096 x 4096 25.1, in pairs 24.3): their reads from LDS are twice as many.
+template <int BI, int BJ, int K, int WI, int WJ, Layout CA, Layout CB, int R, typename OA>
+__device__ __forceinline__ void ring_loop(const OA& A, const Operand& B, int64_t depth, int64_t k0,
+                                          int64_t k1, int64_t i0, int64_t j0, TIDE_LDS char* lds,
+                                          f32x4v (&acc)[BI / WI / 16][BJ / WJ / 16]) {
+    constexpr int kSet = WI * WJ, kWaves = 2 * kSet, TI = BI / WI / 16, TJ = BJ / WJ / 16;
+    using SA = typename StagerOf<BI, K, kWaves, CA, false>::type;
+    using SB = typename StagerOf<BJ, K, kWaves, CB, false>::type;
+    constexpr int kTile = SA::kBytes + SB::kBytes;
+    // B's loads may be fewer than the waves; A's are not
+    constexpr int kMost = SA::kMine + SB::kMine;
+    constexpr bool kUneven = SB::kBytes / 1024 < kWaves;
+    static_assert(SA::kBytes / 1024 % kWaves == 0 && (kUneven || SB::kBytes / 1024 % kWaves == 0), "");
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int set = wave / kSet, of = wave - set * kSet;
+    const int wi = (of / WJ) * TI * 16, wj = (of % WJ) * TJ * 16;
+    const int steps = (int)((k1 - k0 + K - 1) / K);
+    SA sa;
+    SB sb;
+    sa.init(A, i0, k0, lane, wave);
+    sb.init(B, j0, k0, lane, wave);
+#pragma unroll
+    for (int x = 0; x < TI; ++x)
+#pragma unroll
+        for (int y = 0; y < TJ; ++y) acc[x][y] = 0;
+    int64_t valid = depth - k0;
+    auto stage = [&](int at) __attribute__((always_inline)) {
+        sa.stage(lds + at, valid);
+        sb.stage(lds + at + SA::kBytes, valid);
+        valid -= K;
+    };
+#pragma unroll
+    for (int r = 0; r < R - 1; ++r) stage(r * kTile);
+    int now = 0, next = (R - 1) * kTile;
+#pragma unroll 1
+    for (int s = 0; s < steps; ++s) {
+        if (kUneven && wave >= SB::kBytes / 1024)
+            wait_loads<(R - 2) * (kMost - 1)>(lds + now);
+        else
+            wait_loads<(R - 2) * kMost>(lds + now);
+        ring_barrier(lds + now, lds + next);
+        ring_step<BI, BJ, K, TI, TJ, CA, CB>(lds + next, lds + now, sa, sb, valid, wi, wj, lane, set, acc);
+        valid -= K;
+        next = now;
+        now += kTile;
+        if (now == R * kTile) now = 0;
     }
 }
 

@@ -6,14 +6,25 @@ import os
 import subprocess
 import tempfile
 
-from tests.shape_rules import HDR, Shape, gradients, lib as linear_lib, round8
+from tests.shape_rules import HDR, Shape, lib as linear_lib, round8
 
 SRC = r"""
 #include "product_shape.h"
-extern "C" void choose_gated_of(long long I, long long J, long long depth, long long* o) {
-    const tide::Shape s = tide::choose_gated(I, J, depth);
+static void put(const tide::Shape& s, long long* o) {
     const long long v[] = {s.bi, s.bj, s.bk, s.halves, s.tiles_i, s.tiles_j, s.splits, s.split_depth};
     for (int k = 0; k < 8; ++k) o[k] = v[k];
+}
+extern "C" int past(long long rows, long long depth) { return tide::past_the_cache(rows, depth); }
+extern "C" int gradients_of(long long T, long long turn, long long K, int dx, int dw, long long* in,
+                            long long* weight, int* in_first) {
+    const tide::Gradients g = tide::choose_gated_gradients(T, turn, K, dx != 0, dw != 0);
+    put(g.in, in);
+    put(g.weight, weight);
+    *in_first = g.in_first;
+    return g.pair;
+}
+extern "C" void choose_gated_of(long long I, long long J, long long depth, long long* o) {
+    put(tide::choose_gated(I, J, depth), o);
 }
 """
 _lib = None
@@ -32,6 +43,9 @@ def lib():
         ll = ctypes.c_longlong
         _lib.choose_gated_of.argtypes = [ll, ll, ll, ctypes.POINTER(ll)]
         _lib.choose_gated_of.restype = None
+        _lib.past.argtypes = [ll, ll]
+        _lib.gradients_of.argtypes = [ll, ll, ll, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ll),
+                                      ctypes.POINTER(ll), ctypes.POINTER(ctypes.c_int)]
     return _lib
 
 
@@ -51,6 +65,14 @@ def turn(N):
     return -(-N // 64) * 64
 
 
+def gradients(T, N, K, dx=True, dw=True):
+    """(dx's Shape, the weights', whether they share a launch, whether dx's tiles
+    come first in one of 256-wide tiles)."""
+    a, b, first = (ctypes.c_longlong * 8)(), (ctypes.c_longlong * 8)(), ctypes.c_int(0)
+    pair = lib().gradients_of(T, turn(N), K, dx, dw, a, b, ctypes.byref(first))
+    return Shape(*a), Shape(*b), bool(pair), bool(first.value)
+
+
 def forward(T, N, K, keep=False):
     """The forward product's Shape, or None where it goes by the weights' rows."""
     if linear_lib().by_rows(T, 2 * N, K, keep, K % 8 == 0):
@@ -66,13 +88,14 @@ def forms(T, N, K):
     out = set()
     for keep in (False, True):
         s = forward(T, N, K, keep)
-        out.add(("forward by rows", min(T, 3)) if s is None else ("forward",) + name(s))
-    x, w, pair, first = gradients(T, 2 * turn(N), K)
+        once = s is not None and s.tiles_j == 1 and s.bi == 128 and bool(lib().past(rows(N), round8(K)))
+        out.add(("forward by rows", min(T, 3)) if s is None else ("forward",) + name(s) + (once,))
+    x, w, pair, first = gradients(T, N, K)
     if pair and w.bi == 256:
-        out.add(("both, wide", x.bj, w.bj, "dx first" if first else "dW first"))
+        out.add(("both, wide", x.bj, w.bj, "dx first" if first else "dW first", x.splits > 1))
     elif pair:
         groups = x.tiles_i * x.tiles_j * x.splits + w.tiles_i * w.tiles_j
         out.add(("both", x.bj, 2 if groups <= 256 else 1, x.splits > 1))
-    out.add(("dx",) + name(gradients(T, 2 * turn(N), K, dw=False)[0]))
-    out.add(("dW",) + name(gradients(T, 2 * turn(N), K, dx=False)[1]))
+    out.add(("dx",) + name(gradients(T, N, K, dw=False)[0]))
+    out.add(("dW",) + name(gradients(T, N, K, dx=False)[1]))
     return out

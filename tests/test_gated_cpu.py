@@ -191,34 +191,58 @@ def test_cpu_tensors_are_refused():
 
 # ---- the rules ---------------------------------------------------------------------------------
 
-def test_every_choice_holds_blocks_and_covers_the_product():
-    """A wave holds whole checkpoint blocks: 256- or 128-wide tiles, 64 and 32
-    rows of B by two waves each, 16 by two sets of waves."""
-    rng = random.Random(3)
+def drawn(n, seed):
+    rng = random.Random(seed)
     size = lambda hi: int(round(hi ** rng.random()))  # noqa: E731
-    for _ in range(20000):
-        T, N, K = size(16384), size(30000), size(30000)
+    return [(size(16384), size(30000), size(30000)) for _ in range(n)]
+
+
+def threads(s):
+    return 512 if s.bi == 256 or (s.halves == 2 and s.bj > 16) else 256
+
+
+def test_every_choice_is_a_form_and_covers_the_product():
+    """What is chosen is compiled: 256-wide tiles, 128 x 128 ones, rings of 128
+    contraction elements for up to 64 tokens, and tiles of 256 of them for weights
+    past the cache; a split is a whole number of their steps."""
+    for T, N, K in drawn(20000, 3):
         I, depth = rules.rows(N), rules.round8(K)
         s = rules.choose(I, T, depth)
         assert (s.tiles_i - 1) * s.bi < I <= s.tiles_i * s.bi
         assert (s.tiles_j - 1) * s.bj < T <= s.tiles_j * s.bj
         assert (s.splits - 1) * s.split_depth < depth <= s.splits * s.split_depth
-        assert s.bj > 16 or (s.halves == 2 and s.bk == 64)
-        assert s.bk == 64 or (s.bj, s.halves) == (32, 1)
-        threads = 512 if s.bi == 256 else 256 if s.bj == 16 else 256 * s.halves
-        assert s.tiles_i * s.tiles_j * s.splits * threads < 1 << 32
+        assert s.split_depth % 256 == 0
+        form = (s.bi, s.bj, s.bk, s.halves)
+        if T <= 64:
+            assert form in {(128, 16, 128, 2), (128, 32, 128, 2), (128, 64, 128, 2), (128, 32, 256, 1)}
+        else:
+            assert form in {(256, 256, 64, 1), (256, 192, 64, 1), (256, 128, 64, 1), (128, 128, 64, 1),
+                            (128, 128, 64, 2)}
+
+
+def test_splits_of_few_tokens():
+    for T, N, K, splits in ((16, 4096, 4096, 2), (5, 1001, 8192, 8), (64, 1001, 8192, 8), (24, 768, 2048, 4),
+                            (24, 13824, 5120, 1), (40, 768, 1000, 1), (30, 28672, 8192, 1)):
+        assert rules.forward(T, N, K, keep=True).splits == splits, (T, N, K)
+    assert rules.forward(30, 28672, 8192).bk == 256 and rules.forward(30, 13824, 5120).bk == 128
+    assert rules.forward(40, 28672, 8192).bk == 128
+
+
+def test_the_inputs_gradient_is_split_beside_the_weights():
+    """dx's few long tiles in splits, in one launch with the weights' gradients."""
+    for T, N, K, pair in ((1003, 13824, 5120, True), (700, 28672, 8192, True), (4096, 28672, 8192, False)):
+        x, w, joint, first = rules.gradients(T, N, K)
+        assert joint == pair and (not pair or (x.splits > 1 and w.splits == 1 and first))
 
 
 def test_every_launch_is_tested():
     """No launch that random sizes take is missing from the GPU tests' lists."""
-    from tests.test_gated_gpu import FORMS, PRODUCTS
+    from tests.test_gated_gpu import FORMS, PAST_THE_CACHE, PRODUCTS
 
     covered = set().union(*(rules.forms(*s) for s in PRODUCTS + FORMS))
-    rng = random.Random(8)
-    size = lambda hi: int(round(hi ** rng.random()))  # noqa: E731
+    covered |= {f for s in PAST_THE_CACHE for f in rules.forms(*s) if f[0].startswith("forward")}
     missing = {}
-    for _ in range(60000):
-        s = (size(16384), size(30000), size(30000))
+    for s in drawn(60000, 8):
         for f in rules.forms(*s) - covered:
             missing.setdefault(f, s)
     assert not missing, missing
@@ -232,8 +256,7 @@ def test_grids_fit_at_the_limits():
                 if I * T > max(elements, 32 * T) or max(I, T) * depth > elements:
                     continue
                 s = rules.choose(I, T, depth)
-                threads = 512 if s.bi == 256 else 256 if s.bj == 16 else 256 * s.halves
-                assert s.tiles_i * s.tiles_j * s.splits * threads < 1 << 32, (I, T, depth, s)
+                assert s.tiles_i * s.tiles_j * s.splits * threads(s) < 1 << 32, (I, T, depth, s)
 
 
 # ---- the reference -----------------------------------------------------------------------------

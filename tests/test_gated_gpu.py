@@ -27,11 +27,16 @@ PRODUCTS = [(1, 1, 1), (1, 8, 8), (1, 1000, 2048), (2, 33, 64), (3, 70, 65), (4,
             (127, 255, 63), (128, 128, 64), (129, 257, 520), (300, 1001, 1000), (257, 31, 4100), (513, 520, 8),
             (2100, 2100, 136), (1800, 1700, 192)]
 # what else the rules choose; tests/test_gated_cpu.py checks that none is left out
-FORMS = [(780, 821, 6159), (5872, 210, 8992), (6183, 2999, 654), (19, 641, 550), (35, 258, 6175),
-         (2333, 916, 3427), (1401, 1710, 5171), (2, 525, 11), (33, 2150, 662), (4084, 14706, 1),
-         (148, 1574, 18271), (506, 2171, 4122), (1, 1, 16817), (19, 13163, 1), (19, 1, 19162), (66, 1, 18556),
-         (1, 4486, 14973), (1, 9124, 7504), (210, 196, 16539), (795, 465, 6769), (2673, 9361, 142),
-         (4020, 10936, 136)]
+FORMS = [(140, 8848, 2710), (3835, 1644, 1206), (5255, 529, 4096), (35, 258, 6175), (4796, 9572, 170), (393, 1615,
+         16293), (2, 525, 11), (424, 332, 25508), (219, 2295, 8229), (107, 2928, 25934), (4538, 3586, 630), (18, 554,
+         1), (1, 1, 16817), (19, 13163, 1), (19, 1, 19162), (33, 14137, 1), (66, 1, 18556), (75, 16985, 1), (1, 3257,
+         20759), (131, 332, 19254), (18, 3008, 23383), (132, 2405, 4717), (34, 2554, 26228), (795, 465, 6769), (1051,
+         1691, 1951), (2201, 6197, 283), (65, 27843, 2500), (65, 9598, 7303), (1434, 543, 5859), (75, 11598, 5865),
+         (2211, 4989, 538)]
+# few tokens through weights of more than 256 MB together: a ring past the caches, and
+# 512 bytes of a row at a time where there are more tiles than compute units
+PAST_THE_CACHE = [(5, 8203, 8216), (30, 8203, 8209), (12, 8203, 8216), (64, 8200, 8200), (100, 8200, 8200),
+                  (12, 16403, 4104), (30, 16403, 4104)]
 
 
 def kept_within(kept, want, err, what):
@@ -124,11 +129,10 @@ def test_each_gradient_alone(T, N, K):
         within(db, *want["db" + name], "db" + name)
 
 
-@pytest.mark.parametrize("T", [5, 12, 30])
-@pytest.mark.parametrize("K", [8216, 8209])
-def test_forward_of_weights_past_the_cache(T, K):
-    """Few tokens through weights of more than 256 MB together: deep tiles."""
-    check_forward(T, 8203, K, "gelu", True, "guh" if T != 12 else "")
+@pytest.mark.parametrize("T,N,K", PAST_THE_CACHE)
+def test_forward_of_weights_past_the_cache(T, N, K):
+    check_forward(T, N, K, "gelu", True, "guh")
+    check_forward(T, N, K, "silu", False, "")
 
 
 def test_flat_calls_are_the_class_ones():
