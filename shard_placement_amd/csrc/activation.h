@@ -87,6 +87,33 @@ __device__ __forceinline__ float act_slope(float z) {
     return 1.0f;
 }
 
+// act(z) and act'(z) together, for a z that was kept: where it reads back as minus
+// infinity act's limit is 0, not infinity times 0.
+template <int ACT>
+__device__ __forceinline__ float act_both(float z, float* slope) {
+    if constexpr (ACT == TIDE_ACT_GELU || ACT == TIDE_ACT_GELU_TANH || ACT == TIDE_ACT_SILU) {
+        const float low = z < -256.0f ? -256.0f : z;  // NaN stays NaN
+        if constexpr (ACT == TIDE_ACT_GELU) {
+            float bell;
+            const float cdf = normal_cdf(z, &bell);
+            *slope = __builtin_fmaf(within(z) * kInvSqrt2Pi, bell, cdf);
+            return low * cdf;
+        } else if constexpr (ACT == TIDE_ACT_GELU_TANH) {
+            const float t = z * z;
+            const float s = sigmoid(z * __builtin_fmaf(kTanhA, t, kTanhC));
+            const float q = __builtin_fmaf(-s, s, s);
+            *slope = q > 0.0f ? __builtin_fmaf(z * q, __builtin_fmaf(3.0f * kTanhA, t, kTanhC), s) : s;
+            return low * s;
+        } else {
+            const float s = sigmoid(z);
+            *slope = s * __builtin_fmaf(within(z), 1.0f - s, 1.0f);
+            return low * s;
+        }
+    }
+    *slope = act_slope<ACT>(z);
+    return act_value<ACT>(z);
+}
+
 // v to act(v), eight at a time: the choice is made once for all of them.
 template <int ACT>
 __device__ __forceinline__ void apply_act(float (&v)[8]) {

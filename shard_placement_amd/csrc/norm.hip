@@ -11,13 +11,16 @@
 //
 // Memory bounds both directions: a row is read once, kept in registers as it
 // lies in memory, and its statistics and results are worked out from there.
+// 8192 x 8192 with rms: forward 46.4 us (5.8 TB/s), with both checkpoints 66.4 (6.1),
+// backward from a checkpoint and onto a stream's gradient 80.0 (5.9); few rows are
+// bound by launches (1 x 8192 forward 2.5 us) and by the second one backward.
 // The backward pass works mu and r out again from x (or from its checkpoint)
 // instead of keeping them: the row is in registers anyway.
 //
-// A row belongs to a group of L lanes: 16 or 64 lanes of a wave for narrow
-// rows, a workgroup of 256 to 1024 for wide ones; a lane owns U units of 8
-// consecutive columns, L units apart, so every access is contiguous over the
-// wave and the 4 lanes of a quad hold a checkpoint block.
+// A row belongs to a group of lanes: 16 or 64 lanes of a wave for narrow rows, a
+// workgroup of as many waves as hold it for wide ones (up to L lanes); a lane owns
+// U units of 8 consecutive columns, the group's lanes apart, so every access is
+// contiguous over the wave and the 4 lanes of a quad hold a checkpoint block.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -39,9 +42,9 @@ constexpr int kThreads = 256;  // of a workgroup whose rows take fewer lanes
 
 // ---- sums over a row's lanes -------------------------------------------------
 
-template <int CTRL>
+template <int CTRL, int ROWS = 0xf>
 __device__ __forceinline__ float add_dpp(float v) {
-    const int moved = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true);
+    const int moved = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, ROWS == 0xf);
     return v + __builtin_bit_cast(float, moved);
 }
 
@@ -58,9 +61,19 @@ __device__ __forceinline__ float sum_lanes(float v) {
 __device__ __forceinline__ float lane_value(float v, int lane) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
 }
+// The sum over the wave, in its last lane: rows 1 and 3 take the sums of rows 0
+// and 2, then rows 2 and 3 that of the first half.
 __device__ __forceinline__ float sum64(float v) {
     v = sum_lanes<16>(v);
-    return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+    v = add_dpp<0x142, 0xa>(v);
+    return add_dpp<0x143, 0xc>(v);
+}
+
+// Every wave's LDS accesses before it are done.  (__syncthreads() would wait for
+// the loads from memory too, the next row's among them: 2% of 8192 rows of 5120
+// with layer norm.)
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 // N sums over the L lanes of a row, in all of them, always added in the same
@@ -74,16 +87,22 @@ __device__ __forceinline__ void row_sums(float (&v)[N], lds_float* box) {
 #pragma unroll
         for (int k = 0; k < N; ++k) v[k] = sum64(v[k]);
     }
+    if constexpr (L == 64) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = lane_value(v[k], 63);
+    }
     if constexpr (L > 64) {
         constexpr int kWaves = L / 64;
-        if ((threadIdx.x & 63) == 0) {
+        if ((threadIdx.x & 63) == 63) {
 #pragma unroll
             for (int k = 0; k < N; ++k) box[k * kWaves + (threadIdx.x >> 6)] = v[k];
         }
-        __syncthreads();
+        lds_barrier();
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-            v[k] = sum_lanes<kWaves>(box[k * kWaves + (threadIdx.x & (kWaves - 1))]);
+        for (int k = 0; k < N; ++k) {
+            const uint32_t w = threadIdx.x & (kWaves - 1);
+            v[k] = sum_lanes<kWaves>(w < blockDim.x / 64 ? box[k * kWaves + w] : 0.0f);
+        }
     }
 }
 
@@ -92,6 +111,7 @@ __device__ __forceinline__ void row_sums(float (&v)[N], lds_float* box) {
 // The columns of a lane's unit u of L lanes, and how many of them exist.
 template <int L>
 __device__ __forceinline__ uint32_t column(int u, uint32_t thread) {
+    if constexpr (L > 64) return (thread + (uint32_t)u * blockDim.x) * 8;
     return (thread % L + (uint32_t)u * L) * 8;
 }
 
@@ -104,23 +124,38 @@ __device__ __forceinline__ uint32_t this_thread() {
     return t;
 }
 
-// Eight elements from column c of a row of `cols`; those that do not exist are 0.
-__device__ __forceinline__ u32x4v load_unit(const uint16_t* row, uint32_t c, uint32_t cols) {
-    u32x4v w = 0;
-    if (c + 8 <= cols) {
-        w = load8_raw(row + c);
-    } else if (c < cols) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (c + k < cols)
-                w[k / 2] |= (uint32_t) * (const TIDE_GLOBAL_AS uint16_t*)(row + c + k) << (k % 2 * 16);
-    }
+// Eight elements of which the first `less` are dropped, zeros moving in.
+__device__ __forceinline__ u32x4v drop(u32x4v w, uint32_t less) {
+    if (less & 4) w = u32x4v{w.z, w.w, 0u, 0u};
+    if (less & 2) w = u32x4v{w.y, w.z, w.w, 0u};
+    if (less & 1)
+        w = u32x4v{w.x >> 16 | w.y << 16, w.y >> 16 | w.z << 16, w.z >> 16 | w.w << 16, w.w >> 16};
     return w;
 }
 
-// The same of a row that is read once.
-__device__ __forceinline__ u32x4v load_unit_once(const uint16_t* row, uint32_t c, uint32_t cols) {
-    return c + 8 <= cols ? load8_raw<true>(row + c) : load_unit(row, c, cols);
+// Eight elements from column c of a row of `cols`, as far as loading goes: every
+// lane loads, where its eight columns pass the row's end the row's last eight,
+// and settle() makes them its own with zeros behind, where they are used: here it
+// would wait for them.  (Loading the elements before the end one by one, a wait
+// for each, took 2 of 7 us for 4099 x 1001.)  ONCE: the row is read once.
+template <bool ONCE = false>
+__device__ __forceinline__ u32x4v load_unit(const uint16_t* row, uint32_t c, uint32_t cols) {
+    if (cols >= 8) return load8_raw<ONCE>(row + min(c, cols - 8));
+    u32x4v w = 0;
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+        if (c + k < cols)
+            w[k / 2] |= (uint32_t) * (const TIDE_GLOBAL_AS uint16_t*)(row + c + k) << (k % 2 * 16);
+    return w;
+}
+__device__ __forceinline__ void settle(u32x4v& w, uint32_t c, uint32_t cols) {
+    if (cols >= 8 && c + 8 > cols) w = c < cols ? drop(w, c + 8 - cols) : (u32x4v)0u;
+}
+// Of all of a lane's units.
+template <int L, int U>
+__device__ __forceinline__ void settle(u32x4v (&w)[U], uint32_t thread, uint32_t cols) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) settle(w[u], column<L>(u, thread), cols);
 }
 
 // The units as they lie in memory are what stays in registers between the
@@ -134,12 +169,14 @@ __device__ __forceinline__ void forget(u32x4v (&w)[U]) {
     }
 }
 
-// v - mu where the element exists, else 0 (v is 0 there).
+// v - mu where the element exists, else 0 (v is 0 there).  (A branch over several
+// units keeps them all in registers.)
+template <int U>
 __device__ __forceinline__ void centre(float (&v)[8], float mu, uint32_t c, uint32_t cols) {
     mu = c < cols ? mu : 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] -= mu;
-    if (cols % 8) {
+    if (U > 4 || cols % 8) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = (int32_t)(cols - c) > k ? v[k] : 0.0f;
     }
@@ -182,18 +219,19 @@ template <int L, int U, bool LAYER>
 __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_forward_kernel(NormForward p) {
     __shared__ float box[L > 64 ? 3 * (L / 64) : 1];
     constexpr int kRows = (L > kThreads ? L : kThreads) / L;
-    const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / L;
+    const int64_t row = L > 64 ? blockIdx.x : (int64_t)blockIdx.x * kRows + threadIdx.x / L;
     if (row >= p.rows) return;  // the whole group of lanes; L > 64: never
     const uint16_t* from = p.x + row * p.ldx;
     u32x4v raw[U], w[U], b[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) raw[u] = load_unit_once(from, column<L>(u, threadIdx.x), p.cols);
+    for (int u = 0; u < U; ++u) raw[u] = load_unit<true>(from, column<L>(u, threadIdx.x), p.cols);
 #pragma unroll
     for (int u = 0; u < U; ++u) w[u] = load_unit(p.w, column<L>(u, threadIdx.x), p.cols);
     if (p.b) {
 #pragma unroll
         for (int u = 0; u < U; ++u) b[u] = load_unit(p.b, column<L>(u, threadIdx.x), p.cols);
     }
+    settle<L>(raw, threadIdx.x, p.cols);
     float mu = 0.0f;
     if constexpr (LAYER) {
         float s[1] = {0.0f};
@@ -213,7 +251,7 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_forward_kern
     for (int u = 0; u < U; ++u) {
         float v[8];
         widen(raw[u], v);
-        if constexpr (LAYER) centre(v, mu, column<L>(u, threadIdx.x), p.cols);
+        if constexpr (LAYER) centre<U>(v, mu, column<L>(u, threadIdx.x), p.cols);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             s[0] = __builtin_fmaf(v[k], v[k], s[0]);
@@ -225,6 +263,8 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_forward_kern
     const float off = LAYER ? s[LAYER] * p.inv_cols : 0.0f;
     const float r = inv_sqrt(variance(s[0] * p.inv_cols, off) + p.eps);
     const int64_t pitch = act8_pitch(p.cols);
+    settle<L>(w, threadIdx.x, p.cols);
+    if (p.b) settle<L>(b, threadIdx.x, p.cols);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const uint32_t c = column<L>(u, threadIdx.x);
@@ -282,7 +322,7 @@ template <int L, int U>
 __device__ __forceinline__ void load_row(const NormBackward& p, int64_t row, RowParts<U>& r) {
     const uint32_t t = this_thread();
 #pragma unroll
-    for (int u = 0; u < U; ++u) r.dy[u] = load_unit_once(p.dy + row * p.lddy, column<L>(u, t), p.cols);
+    for (int u = 0; u < U; ++u) r.dy[u] = load_unit<true>(p.dy + row * p.lddy, column<L>(u, t), p.cols);
     if (p.x_kept) {
         const int64_t pitch = act8_pitch(p.cols);
         const uint8_t* scales = p.x_kept + p.rows * pitch;
@@ -299,7 +339,7 @@ __device__ __forceinline__ void load_row(const NormBackward& p, int64_t row, Row
         }
     } else if (p.x) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) r.x[u] = load_unit_once(p.x + row * p.ldx, column<L>(u, t), p.cols);
+        for (int u = 0; u < U; ++u) r.x[u] = load_unit<true>(p.x + row * p.ldx, column<L>(u, t), p.cols);
     } else {  // db alone needs no x
 #pragma unroll
         for (int u = 0; u < U; ++u) r.x[u] = 0;
@@ -311,7 +351,7 @@ __device__ __forceinline__ void load_add(const NormBackward& p, int64_t row, u32
     if (p.add) {
         const uint32_t t = this_thread();
 #pragma unroll
-        for (int u = 0; u < U; ++u) add[u] = load_unit_once(p.add + row * p.ldadd, column<L>(u, t), p.cols);
+        for (int u = 0; u < U; ++u) add[u] = load_unit<true>(p.add + row * p.ldadd, column<L>(u, t), p.cols);
     }
 }
 
@@ -338,13 +378,14 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
     constexpr int kHeld = 40 + (DB ? 32 : 24) * U, kMost = L == 1024 ? 124 : 248;
     constexpr bool kAhead = kHeld + 8 * U <= kMost, kAheadAdd = kHeld + 12 * U <= kMost;
     constexpr bool kKeepW = kAhead;
-    int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / L;
+    int64_t row = L > 64 ? blockIdx.x : (int64_t)blockIdx.x * kRows + threadIdx.x / L;
     const int64_t stride = (int64_t)gridDim.x * kRows;
     u32x4v w[U];
     auto load_w = [&]() __attribute__((always_inline)) {
         const uint32_t t = this_thread();
 #pragma unroll
         for (int u = 0; u < U; ++u) w[u] = p.w ? load_unit(p.w, column<L>(u, t), p.cols) : (u32x4v)0u;
+        settle<L>(w, t, p.cols);
     };
     if (kKeepW) load_w();
     float dw[U][8] = {}, db[DB ? U : 1][8] = {};
@@ -364,14 +405,18 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
         if constexpr (kAheadAdd) {
 #pragma unroll
             for (int u = 0; u < U; ++u) add[u] = next_add[u];
-        } else {
+        } else if constexpr (kAhead) {
             load_add<L, U>(p, row, add);
         }
         if (kAhead && row + stride < p.rows) load_row<L, U>(p, row + stride, next);
         if (kAheadAdd && row + stride < p.rows) load_add<L, U>(p, row + stride, next_add);
+        const uint32_t t0 = this_thread();
+        settle<L>(now.dy, t0, p.cols);
         if (p.x_kept) {
 #pragma unroll
             for (int u = 0; u < U; ++u) now.x[u] = kept_unit(now.x[u]);
+        } else {
+            settle<L>(now.x, t0, p.cols);
         }
         // a slot is written again two rows later, with a barrier in between
         lds_float* mine = box + (L > 64 ? slot * 6 * (L / 64) : 0);
@@ -400,12 +445,13 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
             mine += L > 64 ? 2 * (L / 64) : 0;
         }
         float s[LAYER ? 3 : 2] = {};
+        float held[U == 1 ? 8 : 1];  // x - mu of lanes of one unit
         const uint32_t t = this_thread();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float v[8], d[8], f[8];
             widen(now.x[u], v);
-            if constexpr (LAYER) centre(v, mu, column<L>(u, t), p.cols);
+            if constexpr (LAYER) centre<U>(v, mu, column<L>(u, t), p.cols);
             widen(now.dy[u], d);
             widen(w[u], f);
 #pragma unroll
@@ -413,45 +459,62 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
                 s[0] = __builtin_fmaf(v[k], v[k], s[0]);
                 s[1] = __builtin_fmaf(d[k] * f[k], v[k], s[1]);
                 if constexpr (LAYER) s[2] += v[k];
+                if constexpr (U == 1) held[k] = v[k];
             }
         }
         row_sums<L>(s, mine);
         forget(now.x);
         forget(now.dy);
-        forget(w);
+        if constexpr (kAhead) {
+            forget(w);
+        } else {
+            load_add<L, U>(p, row, add);
+            load_w();
+        }
+        // With d = x - mu still off by `off`, n = (d - off) r:
+        //   dx = r c - (r^3 mean(c (d - off))) (d - off) - r mean(c)
         const float off = LAYER ? s[LAYER ? 2 : 0] * p.inv_cols : 0.0f;
         const float r = inv_sqrt(variance(s[0] * p.inv_cols, off) + p.eps);
-        // mean(c n) n = (r^2 mean(c (x - mu))) (x - mu)
-        const uint32_t t2 = this_thread();
         const float along = r * (r * __builtin_fmaf(-off, mean_c, s[1] * p.inv_cols));
+        const float by_d = -r * along, rest = -r * __builtin_fmaf(-along, off, mean_c);
+        const uint32_t t2 = this_thread();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t c = column<L>(u, t2);
             float v[8], d[8], f[8];
-            widen(now.x[u], v);
-            if constexpr (LAYER) {
+            if constexpr (U == 1) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = v[k] - mu - off;
+                for (int k = 0; k < 8; ++k) v[k] = held[k];
+            } else {
+                widen(now.x[u], v);
+                if constexpr (LAYER) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] -= mu;
+                }
             }
             widen(now.dy[u], d);
+            if constexpr (DB) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) db[u][k] += d[k];
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                d[k] *= r;
+                dw[u][k] = __builtin_fmaf(d[k], LAYER ? v[k] - off : v[k], dw[u][k]);
+            }
             if (p.dx && c < p.cols) {
                 float g[8];
                 widen(w[u], f);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    g[k] = r * (__builtin_fmaf(-along, v[k], d[k] * f[k]) - mean_c);
+                    g[k] = __builtin_fmaf(d[k], f[k], LAYER ? __builtin_fmaf(by_d, v[k], rest) : by_d * v[k]);
                 if (p.add) {
+                    settle(add[u], c, p.cols);
                     widen(add[u], f);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) g[k] += f[k];
                 }
                 store8(p.dx + row * p.lddx + c, (int64_t)p.cols - c, g);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) dw[u][k] = __builtin_fmaf(d[k], v[k] * r, dw[u][k]);
-            if constexpr (DB) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) db[u][k] += d[k];
             }
         }
     }
@@ -495,43 +558,52 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
     if constexpr (DB) finish(db, p.db_sums, p.dbias);
 }
 
-// dw and db from the chunks' sums, in the chunks' order within a wave and then
-// over the waves: a lane takes a column, the workgroup's waves every
-// kSumWaves-th chunk.
-constexpr int kSumWaves = 16;
-constexpr int kSumAhead = 8;  // chunks whose loads are in flight together
+// dw and db from the workgroups' sums.  A workgroup takes 64 columns, 16 lanes of
+// 4, and its 64 such sets of lanes a row of sums in turn, so that few workgroups
+// (narrow rows) have many loads in flight; the sets' sums are added in order.
+constexpr int kSumCols = 64, kSumSets = 64;
+constexpr int kSumAhead = 8;  // rows whose loads are in flight together
 
-__global__ __launch_bounds__(64 * kSumWaves) void norm_sums_kernel(const float* dw_sums,
-                                                                   const float* db_sums,
-                                                                   int64_t chunks, int64_t pitch,
-                                                                   int64_t cols, uint16_t* dweight,
-                                                                   uint16_t* dbias) {
-    __shared__ float part[kSumWaves][64];
-    const int64_t groups = (cols + 63) / 64;
+__global__ __launch_bounds__(16 * kSumSets) void norm_sums_kernel(const float* dw_sums,
+                                                                  const float* db_sums,
+                                                                  int64_t rows, int64_t pitch,
+                                                                  int64_t cols, uint16_t* dweight,
+                                                                  uint16_t* dbias) {
+    __shared__ __attribute__((aligned(16))) float part[kSumSets][kSumCols + 4];
+    const int64_t groups = (cols + kSumCols - 1) / kSumCols;
     const bool second = blockIdx.x >= groups || !dw_sums;
     const float* sums = second ? db_sums : dw_sums;
     uint16_t* out = second ? dbias : dweight;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c = (blockIdx.x - (blockIdx.x >= groups ? groups : 0)) * 64 + lane;
-    float s = 0.0f;
-    if (c < cols) {
-        for (int64_t k = wave; k < chunks; k += kSumWaves * kSumAhead) {
-            float v[kSumAhead];
+    const int64_t c0 = (blockIdx.x - (blockIdx.x >= groups ? groups : 0)) * kSumCols;
+    const int set = threadIdx.x / 16, lane = threadIdx.x % 16;
+    f32x4 s = 0.0f;
+    if (c0 + lane * 4 < pitch) {
+        const float* from = sums + c0 + lane * 4;
+        for (int64_t k = set; k < rows; k += kSumSets * kSumAhead) {
+            f32x4 v[kSumAhead];
 #pragma unroll
             for (int a = 0; a < kSumAhead; ++a) {
-                const int64_t at = k + a * kSumWaves;
-                v[a] = at < chunks ? *(const TIDE_GLOBAL_AS float*)(sums + at * pitch + c) : 0.0f;
+                const int64_t at = k + a * kSumSets;
+                v[a] = at < rows ? *(const TIDE_GLOBAL_AS f32x4*)(from + at * pitch) : (f32x4)0.0f;
             }
 #pragma unroll
             for (int a = 0; a < kSumAhead; ++a) s += v[a];
         }
     }
-    part[wave][lane] = s;
-    __syncthreads();
-    if (wave || c >= cols) return;
 #pragma unroll
-    for (int w = 1; w < kSumWaves; ++w) s += part[w][lane];
-    *(TIDE_GLOBAL_AS uint16_t*)(out + c) = to_bf16(s);
+    for (int k = 0; k < 4; ++k) part[set][lane * 4 + k] = s[k];
+    __syncthreads();
+    const int c = threadIdx.x % kSumCols, quarter = threadIdx.x / kSumCols;  // of 16
+    float q = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kSumSets / 16; ++k) q += part[quarter * (kSumSets / 16) + k][c];
+    __syncthreads();
+    part[quarter][c] = q;
+    __syncthreads();
+    if (threadIdx.x >= kSumCols || c0 + c >= cols) return;
+#pragma unroll
+    for (int k = 1; k < 16; ++k) q += part[k][c];
+    *(TIDE_GLOBAL_AS uint16_t*)(out + c0 + c) = to_bf16(q);
 }
 
 // ---- host ----------------------------------------------------------------------
@@ -540,10 +612,9 @@ constexpr int64_t kMaxNormCols = 32768;  // 4096 units: 1024 lanes of 4
 constexpr int64_t kMaxNormRows = (int64_t)1 << 27;  // 16 lanes each in one grid
 constexpr float kMinEps = 1e-30f;
 
-// Lanes and units a row takes (the first form that holds it) and, backward, how
-// many workgroups at most, each of which leaves a row of sums.
+// Lanes (at most) and units of a row: the first form that holds it is taken.
 struct RowShape {
-    int lanes, units, groups;
+    int lanes, units;
 };
 
 using ForwardKernel = void (*)(NormForward);
@@ -559,29 +630,24 @@ struct BackwardForm {
 };
 
 #define TIDE_FORWARD_FORM(L, U) \
-    {{L, U, 0}, norm_forward_kernel<L, U, false>, norm_forward_kernel<L, U, true>}
-#define TIDE_BACKWARD_FORM(L, U, GROUPS)                                                         \
-    {{L, U, GROUPS}, norm_backward_kernel<L, U, false, false>, norm_backward_kernel<L, U, true, false>, \
+    {{L, U}, norm_forward_kernel<L, U, false>, norm_forward_kernel<L, U, true>}
+#define TIDE_BACKWARD_FORM(L, U)                                                    \
+    {{L, U}, norm_backward_kernel<L, U, false, false>, norm_backward_kernel<L, U, true, false>, \
      norm_backward_kernel<L, U, false, true>, norm_backward_kernel<L, U, true, true>}
 
 const ForwardForm kForwardForms[] = {
     TIDE_FORWARD_FORM(16, 1),  TIDE_FORWARD_FORM(64, 1),  TIDE_FORWARD_FORM(64, 2),
-    TIDE_FORWARD_FORM(256, 1), TIDE_FORWARD_FORM(256, 2), TIDE_FORWARD_FORM(256, 3),
-    TIDE_FORWARD_FORM(512, 2), TIDE_FORWARD_FORM(512, 3), TIDE_FORWARD_FORM(512, 4),
-    TIDE_FORWARD_FORM(1024, 3), TIDE_FORWARD_FORM(1024, 4)};
-// The most lanes for a row (one unit each as far as they go) and few workgroups,
-// each of which writes a row of sums that another launch reads: us for 8192 rows
-// of 5120 with rms, 1024 lanes and 256 workgroups 61.8, 512 workgroups 66.5, 512
-// lanes of 2 units 100, 256 of 3 and 512 workgroups 75.8; 777 rows with layer norm
-// and both sums 18.5, 256 lanes of 3 20.3.  Rows of 2048 (8192 of them): 256
-// lanes and 512 workgroups 29.4, 1024 workgroups 30.9, 512 lanes and 256 36.8.
-// Past 16384 columns 512 lanes have the registers that 1024 have not: 2300 rows
-// of 28672 118 us, layer norm with both sums 152 (1024 lanes of 4: 118 and 231).
+    TIDE_FORWARD_FORM(256, 1), TIDE_FORWARD_FORM(512, 2), TIDE_FORWARD_FORM(512, 3),
+    TIDE_FORWARD_FORM(512, 4), TIDE_FORWARD_FORM(1024, 3), TIDE_FORWARD_FORM(1024, 4)};
+// One unit a lane as far as 1024 lanes go, which keeps what the lane holds of the
+// weight, the sums and the next row in few registers: us for 8192 rows of 5120 with
+// rms and 640 lanes 56 (295 MB, 5.3 TB/s), with 256 lanes of 3 units 76.  Past 16384
+// columns 512 lanes have the registers that 1024 have not: 2300 rows of 28672 118
+// with 7 units, with 1024 lanes of 4 178.
 const BackwardForm kBackwardForms[] = {
-    TIDE_BACKWARD_FORM(16, 1, 512),  TIDE_BACKWARD_FORM(64, 1, 512),   TIDE_BACKWARD_FORM(64, 2, 512),
-    TIDE_BACKWARD_FORM(256, 1, 512), TIDE_BACKWARD_FORM(512, 1, 256),  TIDE_BACKWARD_FORM(1024, 1, 256),
-    TIDE_BACKWARD_FORM(1024, 2, 256), TIDE_BACKWARD_FORM(512, 5, 256), TIDE_BACKWARD_FORM(512, 6, 256),
-    TIDE_BACKWARD_FORM(512, 7, 256), TIDE_BACKWARD_FORM(512, 8, 256)};
+    TIDE_BACKWARD_FORM(16, 1),   TIDE_BACKWARD_FORM(64, 1),  TIDE_BACKWARD_FORM(64, 2),
+    TIDE_BACKWARD_FORM(1024, 1), TIDE_BACKWARD_FORM(1024, 2), TIDE_BACKWARD_FORM(512, 5),
+    TIDE_BACKWARD_FORM(512, 6),  TIDE_BACKWARD_FORM(512, 7), TIDE_BACKWARD_FORM(512, 8)};
 
 template <typename Form, size_t N>
 const Form& form_of(const Form (&forms)[N], int64_t cols) {
@@ -591,7 +657,22 @@ const Form& form_of(const Form (&forms)[N], int64_t cols) {
     return forms[N - 1];
 }
 
-int threads_of(const RowShape& s) { return s.lanes > kThreads ? s.lanes : kThreads; }
+// Threads of a workgroup: of wide rows, whole waves that hold one.  (Lanes that
+// hold nothing work all the same, and layer norm is bound by its arithmetic, 87% of
+// the cycles: 8192 rows of 5120 took 84 us with 1024 lanes, 76 with 640.)
+int threads_of(const RowShape& s, int64_t cols) {
+    return s.lanes <= 64 ? kThreads : (int)round_up(ceil_div(act8_pitch(cols) / 8, s.units), 64);
+}
+
+// Rows of a workgroup at a time.
+int64_t rows_of(const RowShape& s) { return s.lanes <= 64 ? kThreads / s.lanes : 1; }
+
+// Workgroups of the backward pass at most.  Each writes a row of sums that another
+// launch reads, so wide rows take no more than the compute units: us at 256 and
+// 512 workgroups for 2300 x 28672 with rms 112 and 125, 8192 x 8192 87 and 89, 512 x
+// 4096 11.2 and 12.1.  Narrower ones take twice as many: 8192 x 2048 39.9 and 29.5
+// (1024: 29.3), 65536 x 128 23.3 and 19.2 (1024: 17.9).
+int64_t most_groups(int threads) { return threads >= 512 ? 256 : 512; }
 
 tide_status check_norm(int64_t rows, int64_t cols, int32_t kind, float eps) {
     if (rows < 0 || cols < 0 || (kind != TIDE_NORM_RMS && kind != TIDE_NORM_LAYER)) return TIDE_EINVAL;
@@ -635,15 +716,16 @@ extern "C" tide_status tide_norm_forward(const tide_norm_forward_args* args, tid
     p.x_kept = static_cast<uint8_t*>(a.x_kept);
     p.y_kept = static_cast<uint8_t*>(a.y_kept);
     const ForwardForm& f = form_of(kForwardForms, C);
-    const int threads = threads_of(f.shape);
-    return launch(a.kind == TIDE_NORM_LAYER ? f.layer : f.rms,
-                  ceil_div(T, threads / f.shape.lanes), threads, stream, p);
+    const int threads = threads_of(f.shape, C);
+    return launch(a.kind == TIDE_NORM_LAYER ? f.layer : f.rms, ceil_div(T, rows_of(f.shape)), threads,
+                  stream, p);
 }
 
 namespace {
 
 struct NormBackwardPlan {
     const BackwardForm* form;
+    int threads;
     int64_t groups, pitch;  // workgroups; columns of their sums
     float *dw = nullptr, *db = nullptr;
     int64_t bytes;
@@ -675,9 +757,8 @@ NormBackwardPlan plan_backward(const tide_norm_backward_args& a, void* ws) {
     NormBackwardPlan b;
     Carver c{static_cast<char*>(ws)};
     b.form = &form_of(kBackwardForms, a.cols);
-    const int threads = threads_of(b.form->shape);
-    const int64_t at_once = threads / b.form->shape.lanes;
-    const int64_t most = b.form->shape.groups;
+    b.threads = threads_of(b.form->shape, a.cols);
+    const int64_t at_once = rows_of(b.form->shape), most = most_groups(b.threads);
     const int64_t each = std::max<int64_t>(1, ceil_div(a.rows, most * at_once));
     b.groups = ceil_div(a.rows, each * at_once);
     b.pitch = round_up(a.cols, 8);
@@ -752,9 +833,9 @@ extern "C" tide_status tide_norm_backward(const tide_norm_backward_args* args, v
     auto k = layer ? a.dbias ? f.layer_db : f.layer : a.dbias ? f.rms_db : f.rms;
     // without rows one workgroup writes the empty sums
     const int64_t grid = T ? b.groups : a.dweight || a.dbias ? 1 : 0;
-    TIDE_TRY(launch(k, grid, threads_of(f.shape), stream, p));
+    TIDE_TRY(launch(k, grid, b.threads, stream, p));
     if (b.groups <= 1 || !(b.dw || b.db)) return TIDE_OK;
-    return launch(norm_sums_kernel, ceil_div(C, 64) * ((b.dw ? 1 : 0) + (b.db ? 1 : 0)),
-                  64 * kSumWaves, stream, (const float*)b.dw, (const float*)b.db, b.groups, b.pitch, C,
+    return launch(norm_sums_kernel, ceil_div(C, kSumCols) * ((b.dw ? 1 : 0) + (b.db ? 1 : 0)),
+                  16 * kSumSets, stream, (const float*)b.dw, (const float*)b.db, b.groups, b.pitch, C,
                   static_cast<uint16_t*>(a.dweight), static_cast<uint16_t*>(a.dbias));
 }
