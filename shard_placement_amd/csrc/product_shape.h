@@ -322,4 +322,17 @@ inline Gradients choose_gated_gradients(int64_t T, int64_t turn, int64_t K, bool
     return choose_gradients(T, 2 * turn, K, dx, dw, 16);
 }
 
+// Whether the gated block's forward product goes by the weights' rows, as
+// forward_by_rows says for one weight; rings leave less for it (us by rows / in
+// rings, N x K of each weight):
+//   2 tokens  128 x 512 5.4 / 6.6, 768 x 2048 6.8 / 10.5, 1024 x 8192 11.5 / 15.1,
+//             13824 x 5120 48.1 / 45.2, 14336 x 1024 24.8 / 13.5
+//   3         13824 x 5120 59.6 / 45.1, 28672 x 4096 94.5 / 78.7, 28672 x 8192 144.4 /
+//             146.3, and 1024 x 8192 in rings 14.3
+inline bool gated_by_rows(int64_t T, int64_t N, int64_t K, bool keep, bool direct) {
+    if (T > 4 || K < 8 || keep) return false;
+    if (T == 1 || !direct) return true;
+    return T == 2 && (K > 1024 || N <= 2048);
+}
+
 }  // namespace tide

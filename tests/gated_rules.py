@@ -6,13 +6,16 @@ import os
 import subprocess
 import tempfile
 
-from tests.shape_rules import HDR, Shape, lib as linear_lib, round8
+from tests.shape_rules import HDR, Shape, round8
 
 SRC = r"""
 #include "product_shape.h"
 static void put(const tide::Shape& s, long long* o) {
     const long long v[] = {s.bi, s.bj, s.bk, s.halves, s.tiles_i, s.tiles_j, s.splits, s.split_depth};
     for (int k = 0; k < 8; ++k) o[k] = v[k];
+}
+extern "C" int by_rows(long long T, long long N, long long K, int keep, int direct) {
+    return tide::gated_by_rows(T, N, K, keep != 0, direct != 0);
 }
 extern "C" int past(long long rows, long long depth) { return tide::past_the_cache(rows, depth); }
 extern "C" int gradients_of(long long T, long long turn, long long K, int dx, int dw, long long* in,
@@ -44,6 +47,7 @@ def lib():
         _lib.choose_gated_of.argtypes = [ll, ll, ll, ctypes.POINTER(ll)]
         _lib.choose_gated_of.restype = None
         _lib.past.argtypes = [ll, ll]
+        _lib.by_rows.argtypes = [ll, ll, ll, ctypes.c_int, ctypes.c_int]
         _lib.gradients_of.argtypes = [ll, ll, ll, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ll),
                                       ctypes.POINTER(ll), ctypes.POINTER(ctypes.c_int)]
     return _lib
@@ -75,7 +79,7 @@ def gradients(T, N, K, dx=True, dw=True):
 
 def forward(T, N, K, keep=False):
     """The forward product's Shape, or None where it goes by the weights' rows."""
-    if linear_lib().by_rows(T, 2 * N, K, keep, K % 8 == 0):
+    if lib().by_rows(T, N, K, keep, K % 8 == 0):
         return None
     return choose(rows(N), T, round8(K))
 

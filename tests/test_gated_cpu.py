@@ -220,6 +220,16 @@ def test_every_choice_is_a_form_and_covers_the_product():
                             (128, 128, 64, 2)}
 
 
+def test_few_tokens_go_by_the_weights_rows():
+    by_rows = lambda *a, **kw: rules.forward(*a, **kw) is None  # noqa: E731
+    assert all(by_rows(1, N, K) for N in (1, 64, 28672) for K in (8, 512, 28672))
+    assert all(by_rows(T, 64, 1001) for T in (1, 2, 3, 4))  # weights that rings would copy
+    assert by_rows(2, 1024, 8192) and by_rows(2, 128, 512) and not by_rows(2, 14336, 1024)
+    for case in ((3, 28672, 8192), (4, 64, 1024), (5, 64, 1001), (1, 8, 7)):
+        assert not by_rows(*case), case
+    assert not by_rows(1, 28672, 8192, keep=True)
+
+
 def test_splits_of_few_tokens():
     for T, N, K, splits in ((16, 4096, 4096, 2), (5, 1001, 8192, 8), (64, 1001, 8192, 8), (24, 768, 2048, 4),
                             (24, 13824, 5120, 1), (40, 768, 1000, 1), (30, 28672, 8192, 1)):
