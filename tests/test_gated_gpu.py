@@ -522,3 +522,53 @@ def test_feed_forward_half_between_placement_and_reduce_scatter():
             want, b = sums[p][r * s:r * s + n], bounds[p][r * s:r * s + n]
             within(got[:n], want, b + R * lref.F32 * (want.abs() + b), "shard %d of %d" % (r, p))
             assert (got[n:] == 0).all()
+
+
+# ---- far offsets -------------------------------------------------------------------------------
+
+@pytest.mark.big
+@pytest.mark.parametrize("T,N,K", [(140000, 40, 16400), (41000, 53000, 72)])
+def test_offsets_past_32_bits(T, N, K):
+    """Operands, results and checkpoints whose byte offsets pass 2^32."""
+    g = gen(8)
+    x = torch.empty(T, K, dtype=BF, device=DEV)
+    for t in range(0, T, 20000):
+        x[t:t + 20000] = torch.randn(min(20000, T - t), K, generator=g, device=DEV)
+    x8, g8, u8, h8 = Act8(T, K, device=DEV).pack(x), *(Act8(T, N, device=DEV) for _ in range(3))
+    wg, wu = normal(g, N, K, scale=1 / math.sqrt(K)), normal(g, N, K, scale=1 / math.sqrt(K))
+    block = Gated(wg, wu, gate_grad=torch.empty_like(wg), up_grad=torch.empty_like(wu))
+    h = block.forward(x, g=g8, u=u8, h=h8)
+    rows = torch.tensor([0, 1, T // 3, T // 2, T - 40001 % T, T - 2, T - 1], device=DEV)
+    raw = lambda k: (k.data.view(torch.uint8)[rows], k.scales.view(torch.uint8)[rows])  # noqa: E731
+    want = ref.forward_ref(x[rows], wg, wu, None, None, "silu")
+    within(h[rows], want["h"][0], ref.rounded(*want["h"]), "h")
+    val = {}
+    for name, k, c in (("x", x8, K), ("g", g8, N), ("u", u8, N), ("h", h8, N)):
+        val[name] = lref.unpack_ref(*raw(k), c)
+        if name != "x":
+            v, err = want[name]
+            step = torch.exp2(raw(k)[1].double() - 127).repeat_interleave(32, 1)[:, :c]
+            within(val[name], v, torch.maximum(lref.E4M3 * (v.abs() + err), lref.E4M3_SUB * step) + err, name)
+    dh = h
+    dh.zero_()
+    dh[rows] = normal(g, len(rows), N)
+    dx = block.backward(dh, x=x8, g=g8, u=u8, dx=x)
+    want = ref.backward_ref(dh[rows], wg, wu, val["x"], val["g"], val["u"], "silu")
+    within(dx[rows], *want["dx"], "dx")
+    within(block.gate_grad, *want["dwg"], "dwg")
+    within(block.up_grad, *want["dwu"], "dwu")
+    assert (dx[T // 4:T // 4 + 5] == 0).all()
+
+
+@pytest.mark.big
+def test_most_tokens():
+    """2^30 tokens of one feature: h = (2 x) (4 x) with act none, every element."""
+    T = 1 << 30
+    x = torch.zeros(T, 1, dtype=BF, device=DEV)
+    at = torch.tensor([0, 1, (1 << 29) + 5, T - 1], device=DEV)
+    x[at] = torch.tensor([[1.0], [-2.0], [0.5], [3.0]], dtype=BF, device=DEV)
+    w2, w4 = (torch.full((1, 1), v, dtype=BF, device=DEV) for v in (2.0, 4.0))
+    h = Gated(w2, w4, act="none").forward(x)
+    want = torch.zeros(T, 1, dtype=BF, device=DEV)
+    want[at] = torch.tensor([[8.0], [32.0], [2.0], [72.0]], dtype=BF, device=DEV)
+    assert torch.equal(h, want)

@@ -221,10 +221,9 @@ def test_rows_that_are_not_finite_stay_alone():
 
 @pytest.mark.parametrize("kind", list(api.NORMS))
 def test_gradients_against_differences(kind):
-    """The sum of y dy changes by the gradients along random directions.  In
-    float64 from the outputs of the reference alone the difference would be
-    exact; from the kernel's bf16 y it is off by y's rounding, so the step is
-    large and the function's own curvature is taken off by both sides."""
+    """The sum of y dy along each gradient's own direction, by central differences
+    of the kernel's y.  y is rounded to bf16, so the step is large: what the
+    difference keeps of the third order is allowed for, and y's roundings."""
     g = gen(31)
     T, C, h = 64, 520, 2.0 ** -4
     x, w, b = normal(g, T, C), normal(g, C), normal(g, C)
@@ -373,3 +372,30 @@ def test_refusals_on_the_gpu():
         Norm(wide).forward(wide.view(1, -1).clone())
     with pytest.raises(TideError, match="rows that share memory"):
         Norm(w).backward(x[:1].expand(4, 64), x)
+
+
+@pytest.mark.big
+@pytest.mark.parametrize("T,C", [(1 << 27, 2), (299593, 28672)])
+def test_most_rows(T, C):
+    """The most rows there may be, and the most elements: rows everywhere against
+    the reference, the weight's gradient from a few rows that are not zero."""
+    g = gen(17)
+    w = normal(g, C)
+    x = torch.zeros(T, C, dtype=BF, device=DEV)
+    rows = torch.tensor([0, 1, T // 3, T // 2 + 1, T - 2, T - 1], device=DEV)
+    x[rows] = normal(g, len(rows), C)
+    layer = Norm(w, kind="layer", eps=EPS, weight_grad=torch.empty_like(w))
+    x8 = Act8(T, C, device=DEV)
+    y = layer.forward(x, x8=x8)
+    want, err = ref.forward_ref(x[rows], w, None, "layer", EPS)
+    within(y[rows], want, ref.rounded(want, err), "y")
+    assert (y[T // 4:T // 4 + 9] == 0).all()
+    val = lref.unpack_ref(x8.data.view(torch.uint8)[rows], x8.scales.view(torch.uint8)[rows], C)
+    y.zero_()
+    dy = y
+    dy[rows] = normal(g, len(rows), C)
+    dx = layer.backward(dy, x8, dx=x)
+    want = ref.backward_ref(dy[rows], w, val, None, "layer", EPS)
+    within(dx[rows], *want["dx"], "dx")
+    within(layer.weight_grad, *want["dw"], "dw")
+    assert (dx[T // 4:T // 4 + 9] == 0).all()
