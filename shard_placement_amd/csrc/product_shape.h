@@ -213,7 +213,8 @@ inline Shape choose_gated(int64_t I, int64_t J, int64_t depth) {
 // most: splits of dx's contraction that are looked at.  The layer product takes
 // none (its sums keep their order); the gated block's dx has twice the terms, few
 // tiles of which are long: its splits fill the chip together with dW's tiles, and
-// the join is cheap beside them.
+// the join is cheap beside them (1003 x 13824 x 5120: 563 us with 3 splits, 574 in
+// two launches).
 inline bool choose_pair(int64_t T, int64_t N, int64_t K, double best, Shape* in, Shape* weight,
                         bool* in_first, int64_t most = 1) {
     constexpr int kWide = 2;  // 256 x 256 and 256 x 192
@@ -285,8 +286,9 @@ struct Gradients {
     bool in_first;  // of 256-wide tiles in one launch: dx's are the longer ones
 };
 
+// whole: a contraction of dx of up to this many terms is not split in such a pair.
 inline Gradients choose_gradients(int64_t T, int64_t N, int64_t K, bool dx, bool dw,
-                                  int64_t pair_splits = 1) {
+                                  int64_t pair_splits = 1, int64_t whole = 1024) {
     const int64_t width = round_up(N, 8);
     Gradients g = {};
     double in_us = 0.0, w_us = 0.0;
@@ -306,7 +308,7 @@ inline Gradients choose_gradients(int64_t T, int64_t N, int64_t K, bool dx, bool
         };
         fit(2 * kCus);
         g.pair = grid_of(in) + grid_of(g.weight) <= 2 * kCus;
-        if (width <= 1024) set_split(&in, K, T, width, 1);
+        if (width <= whole) set_split(&in, K, T, width, 1);
         fit(kCus);
         if (g.pair) g.in = in;
     }
@@ -317,9 +319,12 @@ inline Gradients choose_gradients(int64_t T, int64_t N, int64_t K, bool dx, bool
 }
 
 // The gated block's gradients' products: of both matrices' dz side by side, `turn`
-// columns each.
+// columns each.  Of 513 to 1024 terms dx is whole up to 64 tokens, whose tiles' steps
+// are short, and from 257 on, whose tiles are many (us whole / in four splits: 16 x 512
+// x 2048 10.2 / 11.1, 77 x 512 x 512 14.7 / 11.3, 200 x 512 x 512 15.0 / 12.5, 512 x 512
+// x 512 15.8 / 17.0); fewer terms always are (77 x 192 x 2048 10.3 / 11.4).
 inline Gradients choose_gated_gradients(int64_t T, int64_t turn, int64_t K, bool dx, bool dw) {
-    return choose_gradients(T, 2 * turn, K, dx, dw, 16);
+    return choose_gradients(T, 2 * turn, K, dx, dw, 16, T <= 64 || T > 256 ? 1024 : 512);
 }
 
 // Whether the gated block's forward product goes by the weights' rows, as
