@@ -426,7 +426,7 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
             float s[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                    float v[8], d[8], f[8];
+                float v[8], d[8], f[8];
                 widen(now.x[u], v);
                 widen(now.dy[u], d);
                 widen(w[u], f);
