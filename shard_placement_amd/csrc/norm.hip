@@ -659,7 +659,8 @@ const Form& form_of(const Form (&forms)[N], int64_t cols) {
 
 // Threads of a workgroup: of wide rows, whole waves that hold one.  (Lanes that
 // hold nothing work all the same, and layer norm is bound by its arithmetic, 87% of
-// the cycles: 8192 rows of 5120 took 84 us with 1024 lanes, 76 with 640.)
+// the cycles: 8192 rows of 5120 took 84 us with 1024 lanes, 76 with 640, 63 as the
+// loop is now.)
 int threads_of(const RowShape& s, int64_t cols) {
     return s.lanes <= 64 ? kThreads : (int)round_up(ceil_div(act8_pitch(cols) / 8, s.units), 64);
 }
