@@ -182,9 +182,28 @@ __device__ __forceinline__ void centre(float (&v)[8], float mu, uint32_t c, uint
     }
 }
 
-// A mean worked out in binary32 is off by a few steps of the mean, which a row of
-// nearly equal values would see: what is left of the mean after it was taken
-// off (`off`, a sum of small numbers) is taken off as well.
+// Layer norm takes off the mean's first 8 bits, and what is left of the mean (`off`,
+// the mean of the differences) in a step of its own.  An element, of 8 bits, less a
+// number of 8 bits is few bits long, so the differences are exact, and so, nearly, is
+// their sum, be the mean large next to them or small.  (Differences from the mean in
+// binary32 are rounded, equal ones alike, and what their sum shows is those roundings:
+// n of elements near the mean was off by up to 4%, and 449 of 210 million y of 4096 x
+// 5120 fell to the other side of a border in 8 bits, now 139, in the plain form 128.)
+// Rounded to nearest, the mean of a row of one value is that value.
+__device__ __forceinline__ float first_bits(float mean) {
+    return __uint_as_float((uint32_t)to_bf16(mean) << 16);
+}
+// The sum of a lane's differences, from its sum of elements: one operation in the
+// place of one for each.
+template <int L, int U>
+__device__ __forceinline__ float less_first_bits(float sum, float mu, uint32_t thread, uint32_t cols) {
+    int n = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) n += min(max((int)cols - (int)column<L>(u, thread), 0), 8);
+    return __builtin_fmaf(-(float)n, mu, sum);
+}
+
+// The mean square of the differences, less that of what is left of the mean.
 __device__ __forceinline__ float variance(float mean_square, float off) {
     return fmaxf(__builtin_fmaf(-off, off, mean_square), 0.0f * mean_square);
 }
@@ -232,7 +251,7 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_forward_kern
         for (int u = 0; u < U; ++u) b[u] = load_unit(p.b, column<L>(u, threadIdx.x), p.cols);
     }
     settle<L>(raw, threadIdx.x, p.cols);
-    float mu = 0.0f;
+    float mu = 0.0f, left = 0.0f;
     if constexpr (LAYER) {
         float s[1] = {0.0f};
 #pragma unroll
@@ -242,8 +261,10 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_forward_kern
 #pragma unroll
             for (int k = 0; k < 8; ++k) s[0] += v[k];
         }
+        left = s[0];
         row_sums<L>(s, (lds_float*)box);
-        mu = s[0] * p.inv_cols;
+        mu = first_bits(s[0] * p.inv_cols);
+        left = less_first_bits<L, U>(left, mu, threadIdx.x, p.cols);
         forget(raw);
     }
     float s[LAYER ? 2 : 1] = {};
@@ -253,11 +274,9 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_forward_kern
         widen(raw[u], v);
         if constexpr (LAYER) centre<U>(v, mu, column<L>(u, threadIdx.x), p.cols);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            s[0] = __builtin_fmaf(v[k], v[k], s[0]);
-            if constexpr (LAYER) s[1] += v[k];
-        }
+        for (int k = 0; k < 8; ++k) s[0] = __builtin_fmaf(v[k], v[k], s[0]);
     }
+    if constexpr (LAYER) s[1] = left;
     row_sums<L>(s, (lds_float*)box + (L > 64 ? L / 64 : 0));
     forget(raw);
     const float off = LAYER ? s[LAYER] * p.inv_cols : 0.0f;
@@ -396,6 +415,10 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
     int slot = 0;
 #pragma unroll 1
     for (; row < p.rows; row += stride) {
+        // Fetching a loop of 11 KB for waves in step costs more at some places in
+        // memory than at others: 8192 rows of 5120 with layer norm and a bias took 62 to
+        // 77 us with the loop's start moved by a few instructions, 59.5 on 64 bytes.
+        if constexpr (LAYER && L > 64 && U == 1) asm volatile(".p2align 6" ::: "memory");
         RowParts<U> now;
         if constexpr (kAhead)
             now = next;
@@ -421,7 +444,7 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
         // a slot is written again two rows later, with a barrier in between
         lds_float* mine = box + (L > 64 ? slot * 6 * (L / 64) : 0);
         slot ^= 1;
-        float mu = 0.0f, mean_c = 0.0f;
+        float mu = 0.0f, left = 0.0f, mean_c = 0.0f;
         if constexpr (LAYER) {
             float s[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -436,11 +459,13 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
                     s[1] = __builtin_fmaf(d[k], f[k], s[1]);
                 }
             }
+            left = s[0];
             row_sums<L>(s, mine);
             forget(now.x);
             forget(now.dy);
             forget(w);
-            mu = s[0] * p.inv_cols;
+            mu = first_bits(s[0] * p.inv_cols);
+            left = less_first_bits<L, U>(left, mu, this_thread(), p.cols);
             mean_c = s[1] * p.inv_cols;
             mine += L > 64 ? 2 * (L / 64) : 0;
         }
@@ -458,10 +483,10 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
             for (int k = 0; k < 8; ++k) {
                 s[0] = __builtin_fmaf(v[k], v[k], s[0]);
                 s[1] = __builtin_fmaf(d[k] * f[k], v[k], s[1]);
-                if constexpr (LAYER) s[2] += v[k];
                 if constexpr (U == 1) held[k] = v[k];
             }
         }
+        if constexpr (LAYER) s[2] = left;
         row_sums<L>(s, mine);
         forget(now.x);
         forget(now.dy);
@@ -670,10 +695,19 @@ int64_t rows_of(const RowShape& s) { return s.lanes <= 64 ? kThreads / s.lanes :
 
 // Workgroups of the backward pass at most.  Each writes a row of sums that another
 // launch reads, so wide rows take no more than the compute units: us at 256 and
-// 512 workgroups for 2300 x 28672 with rms 112 and 125, 8192 x 8192 87 and 89, 512 x
+// 512 workgroups for 2300 x 28672 with rms 112 and 125, 8192 x 8192 73 and 78, 512 x
 // 4096 11.2 and 12.1.  Narrower ones take twice as many: 8192 x 2048 39.9 and 29.5
-// (1024: 29.3), 65536 x 128 23.3 and 19.2 (1024: 17.9).
-int64_t most_groups(int threads) { return threads >= 512 ? 256 : 512; }
+// (1024: 29.3), 65536 x 128 23.3 and 19.2 (1024: 17.9; one number for all narrow rows).
+// So does layer norm, whose arithmetic leaves memory waiting, where two of its
+// workgroups fit a compute unit's registers: 8192 rows of 4096 with a bias 54 and 47,
+// without 53 and 44, of 5120 without 71 and 57, of 6144 without 75 and 64; of 5120 with
+// a bias, whose 10 waves of 85 registers do not fit twice, 59.5 and 65, of 7168 without
+// 88 and 93.  (From 2048 rows on, four for each: 777 of 4096 with a bias 14 and 15; of
+// lanes with one unit: 2300 x 28672 148 and 172.)
+int64_t most_groups(const RowShape& s, int threads, int64_t rows, bool layer, bool db) {
+    const bool two = layer && s.units == 1 && threads <= (db ? 512 : 768);
+    return threads < 512 || (two && rows >= 2048) ? 512 : 256;
+}
 
 tide_status check_norm(int64_t rows, int64_t cols, int32_t kind, float eps) {
     if (rows < 0 || cols < 0 || (kind != TIDE_NORM_RMS && kind != TIDE_NORM_LAYER)) return TIDE_EINVAL;
@@ -759,7 +793,9 @@ NormBackwardPlan plan_backward(const tide_norm_backward_args& a, void* ws) {
     Carver c{static_cast<char*>(ws)};
     b.form = &form_of(kBackwardForms, a.cols);
     b.threads = threads_of(b.form->shape, a.cols);
-    const int64_t at_once = rows_of(b.form->shape), most = most_groups(b.threads);
+    const int64_t at_once = rows_of(b.form->shape);
+    const int64_t most = most_groups(b.form->shape, b.threads, a.rows, a.kind == TIDE_NORM_LAYER,
+                                     a.dbias != nullptr);
     const int64_t each = std::max<int64_t>(1, ceil_div(a.rows, most * at_once));
     b.groups = ceil_div(a.rows, each * at_once);
     b.pitch = round_up(a.cols, 8);

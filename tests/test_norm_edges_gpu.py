@@ -1,0 +1,95 @@
+"""GPU tests of the norms where binary32 ends: elements that lie near their
+row's mean, and rows whose squares pass binary32."""
+import pytest
+import torch
+
+from shard_placement_amd import api
+from shard_placement_amd.linear import Act8
+from shard_placement_amd.norm import Norm
+from tests.test_linear_gpu import BF, DEV, gen, normal, within
+
+pytestmark = pytest.mark.gpu
+F24 = 2.0 ** -24  # half a binary32 step, relative
+
+
+def near_the_mean(C, surplus):
+    """(row, columns that are 0, their n in 64 bits): +1 and -1 in turn, `surplus`
+    more of +1, and 128 columns of 0, whose n is -mean / sigma.
+
+    Every sum of x is exact, and so are those of x less the mean's first 8 bits
+    (16 elements a lane, whole multiples of 2^-20).  So n is off by the rounding
+    of x - mean, of 1 / sigma and of their product, and sigma by what its sum is:
+    32 additions of half a step, which the root halves, a step of the root, and
+    the roundings around it: below 40 halves of a step altogether."""
+    x = torch.zeros(C, dtype=torch.float64)
+    body = C - 128 - surplus
+    x[:body // 2 * 2:2], x[1:body // 2 * 2:2] = 1, -1
+    x[C - 128 - surplus:C - 128] = 1
+    d = x - x.mean()
+    n = d / (d * d).mean().sqrt()
+    return x.to(BF).to(DEV), slice(C - 128, C), n[C - 1].item()
+
+
+WEIGHTS = (torch.arange(128) + 128).double() / 128  # every mantissa of bf16
+
+
+@pytest.mark.parametrize("C", [1001, 2040, 5120, 8192, 12000])
+@pytest.mark.parametrize("surplus", [1, 2, 3, 7, 37, 200])
+def test_elements_near_the_mean(C, surplus):
+    """The bias takes off what bf16 holds of n w: what is left shows n to 24 bits."""
+    x, zeros, n = near_the_mean(C, surplus)
+    w, b = torch.ones(C, dtype=BF, device=DEV), torch.zeros(C, dtype=BF, device=DEV)
+    want = n * WEIGHTS.to(DEV)
+    w[zeros], b[zeros] = WEIGHTS.to(BF).to(DEV), -want.to(BF)
+    y = Norm(w, bias=b, kind="layer", eps=1e-30).forward(x[None])[0, zeros]
+    left = want + b[zeros].double()
+    within(y, left, 40 * F24 * want.abs() + 2.0 ** -8 * (left.abs() + 40 * F24 * want.abs()), "y")
+
+
+@pytest.mark.parametrize("C", [1001, 2040, 5120, 8192])
+@pytest.mark.parametrize("surplus", [1, 2, 7, 200])
+@pytest.mark.parametrize("kept", [False, True])
+def test_elements_near_the_mean_backward(C, surplus, kept):
+    """The same in dw, where a row of +-1 (n = +-1 to two steps) takes it off."""
+    x, zeros, n = near_the_mean(C, surplus)
+    x = torch.stack([x, torch.ones_like(x)])
+    x[1, 1::2] = -1
+    if C % 2:
+        x[1, 0] = 0  # as many of +1 as of -1
+    sign = x[1, zeros].double()
+    scale = ((C - C % 2) / C) ** -0.5  # of the second row's n
+    dy = torch.zeros_like(x)
+    want = n * WEIGHTS.to(DEV)
+    dy[0, zeros], dy[1, zeros] = WEIGHTS.to(BF).to(DEV), (-want / scale * sign).to(BF)
+    dw = torch.empty(C, dtype=BF, device=DEV)
+    given = dict(x_kept=Act8(2, C, device=DEV).pack(x).buffer) if kept else dict(x=x)
+    api.tide_norm_backward(dy, kind="layer", eps=1e-30, dweight=dw, **given)
+    other = dy[1, zeros].double() * sign * scale
+    off = 40 * F24 * (want.abs() + other.abs())
+    within(dw[zeros], want + other, off + 2.0 ** -8 * ((want + other).abs() + off), "dw")
+
+
+@pytest.mark.parametrize("C", [64, 200, 1001, 5120, 28672])
+@pytest.mark.parametrize("kind", list(api.NORMS))
+@pytest.mark.parametrize("size", [1e20, 1e27, 1e30, 1e33])
+def test_rows_whose_squares_pass_binary32(kind, C, size):
+    """Such a row is divided by infinity, forward and backward; the others are as
+    they are without it."""
+    g = gen(C)
+    x, w, b = normal(g, 5, C), normal(g, C), normal(g, C)
+    dy, add = normal(g, 5, C), normal(g, 5, C)
+    # |x| from `size` to 4 `size`, of unequal signs: their sum stays below 2^17 * 10^33
+    x[3] = ((1 + 3 * torch.rand(C, generator=g, device=DEV)) * size * torch.sign(x[3].float() + 0.5)).to(BF)
+    rest = [0, 1, 2, 4]
+    layer = Norm(w, bias=b, kind=kind, weight_grad=torch.empty_like(w), bias_grad=torch.empty_like(w))
+    y = layer.forward(x)
+    assert torch.equal(y[3], b)
+    assert torch.equal(y[rest], layer.forward(x[rest]))
+    for from_x in (x, Act8(5, C, device=DEV).pack(x)):
+        dx = layer.backward(dy, from_x, add=add)
+        assert torch.equal(dx[3], add[3])
+        dw = layer.weight_grad.clone()
+        small = x[rest] if from_x is x else from_x.unpack()[rest]
+        assert torch.equal(dx[rest], layer.backward(dy[rest], small, add=add[rest]))
+        # the same terms, added in another order: binary32, then a step of bf16 at most
+        torch.testing.assert_close(dw, layer.weight_grad, rtol=2.0 ** -7, atol=1e-5)
