@@ -157,8 +157,10 @@ __device__ __forceinline__ void dgu_lane(const DguArgs& p, int64_t c, int64_t t0
         for (int k = 0; k < 8; ++k) {
             float slope;
             const float value = act_both<ACT>(g[k], &slope);
-            u[k] = d[k] * u[k] * slope;  // dg
-            g[k] = d[k] * value;         // du
+            // dg; a slope passes 1 by little, so u slope stays within binary32, which
+            // dh u may leave where dg does not (a slope of 0 would be NaN)
+            u[k] = d[k] * (u[k] * slope);
+            g[k] = d[k] * value;  // du
         }
         if constexpr (!WHOLE) {
 #pragma unroll
