@@ -300,8 +300,7 @@ ForwardPlan plan_forward(const tide_gated_forward_args& a, void* ws) {
     const int64_t T = a.tokens, N = a.out_features, K = a.in_features;
     const bool keep = a.g_kept || a.u_kept || a.h_kept;
     f.rows = 2 * round_up(N, 16);
-    f.gemv = gated_by_rows(T, N, K, keep,
-                           direct(a.x, a.ldx, T, K) && direct(a.gate, K, N, K) && direct(a.up, K, N, K));
+    f.gemv = gated_by_rows(T, N, K, keep, direct(a.gate, K, N, K) && direct(a.up, K, N, K));
     f.bytes = 0;
     if (f.gemv) return f;
     f.x = {a.x, a.ldx, T, K};

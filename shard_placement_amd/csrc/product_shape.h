@@ -334,6 +334,9 @@ inline Gradients choose_gated_gradients(int64_t T, int64_t turn, int64_t K, bool
 //             13824 x 5120 48.1 / 45.2, 14336 x 1024 24.8 / 13.5
 //   3         13824 x 5120 59.6 / 45.1, 28672 x 4096 94.5 / 78.7, 28672 x 8192 144.4 /
 //             146.3, and 1024 x 8192 in rings 14.3
+// direct: both weights can be read where they lie.  x, where it cannot, is a few rows
+// to copy (4 tokens 512 x 512 10.0 / 7.6, 768 x 2048 10.8 / 12.5, 8192 x 1024 24.4 /
+// 11.6, 4096 x 4096 20.5 / 23.3, 13824 x 5120 58.6 / 46.5).
 inline bool gated_by_rows(int64_t T, int64_t N, int64_t K, bool keep, bool direct) {
     if (T > 4 || K < 8 || keep) return false;
     if (T == 1 || !direct) return true;

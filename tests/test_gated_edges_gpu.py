@@ -1,10 +1,12 @@
-"""GPU tests of the gated block where binary32 ends."""
+"""GPU tests of the gated block where binary32 ends, and of few tokens on any
+element."""
 import pytest
 import torch
 
 from shard_placement_amd.gated import Gated
+from tests import gated_ref as ref
 from tests import linear_ref as lref
-from tests.test_linear_gpu import BF, DEV, kept_of, within
+from tests.test_linear_gpu import BF, DEV, gen, kept_of, normal, strided, within
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +36,15 @@ def test_a_small_slope_of_large_factors(act, gate, sign):
     off = 2.0 ** -7 + 2 * lref.BF16
     within(dg, want, off * want.abs(), "dg")
     within(dbg, want.sum(0), off * want.sum(0).abs(), "dbg")
+
+
+@pytest.mark.parametrize("T,N,K", [(2, 2305, 264), (3, 4096, 512), (3, 40, 64), (4, 300, 2056), (4, 1001, 8)])
+@pytest.mark.parametrize("shift,more", [(1, 0), (0, 3), (5, 8)])
+def test_few_tokens_on_any_element(T, N, K, shift, more):
+    """x on any element before weights that can be read where they lie."""
+    g = gen(T * N + K)
+    x, wg, wu = normal(g, T, K), normal(g, N, K, scale=K ** -0.5), normal(g, N, K, scale=K ** -0.5)
+    bg, bu = normal(g, N), normal(g, N)
+    xs, _ = strided(x, K + more, shift)
+    want = ref.forward_ref(x, wg, wu, bg, bu, "silu")["h"]
+    within(Gated(wg, wu, gate_bias=bg, up_bias=bu).forward(xs), want[0], ref.rounded(*want), "h")
