@@ -618,10 +618,9 @@ __device__ __forceinline__ void ring_loop(const OA& A, const Operand& B, int64_t
     using SA = typename StagerOf<BI, K, kWaves, CA, false>::type;
     using SB = typename StagerOf<BJ, K, kWaves, CB, false>::type;
     constexpr int kTile = SA::kBytes + SB::kBytes;
-    // B's loads may be fewer than the waves; A's are not
-    constexpr int kMost = SA::kMine + SB::kMine;
-    constexpr bool kUneven = SB::kBytes / 1024 < kWaves;
-    static_assert(SA::kBytes / 1024 % kWaves == 0 && (kUneven || SB::kBytes / 1024 % kWaves == 0), "");
+    // every wave's loads of a step are as many, which is what it waits by
+    constexpr int kLoads = SA::kMine + SB::kMine;
+    static_assert(SA::kBytes / 1024 % kWaves == 0 && SB::kBytes / 1024 % kWaves == 0, "");
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int set = wave / kSet, of = wave - set * kSet;
@@ -646,10 +645,7 @@ __device__ __forceinline__ void ring_loop(const OA& A, const Operand& B, int64_t
     int now = 0, next = (R - 1) * kTile;
 #pragma unroll 1
     for (int s = 0; s < steps; ++s) {
-        if (kUneven && wave >= SB::kBytes / 1024)
-            wait_loads<(R - 2) * (kMost - 1)>(lds + now);
-        else
-            wait_loads<(R - 2) * kMost>(lds + now);
+        wait_loads<(R - 2) * kLoads>(lds + now);
         ring_barrier(lds + now, lds + next);
         ring_step<BI, BJ, K, TI, TJ, CA, CB>(lds + next, lds + now, sa, sb, valid, wi, wj, lane, set, acc);
         valid -= K;
