@@ -599,9 +599,12 @@ __device__ __forceinline__ void ring_step(TIDE_LDS char* __restrict__ next,
 
 // The same loop with R tiles in LDS, R - 1 of them under way: a step waits for the
 // oldest only, so the loads never run dry.  Two sets of WI * WJ waves share the
-// tiles, each with half of a tile's contraction.  Past the contraction's end
-// loads are issued all the same, outside the operands' descriptors (they read
-// as 0), so that every step has as many to wait for.
+// tiles, each with half of a tile's contraction.  Loads are issued to the last step,
+// so that every step has as many to wait for: behind the contraction's end they lie
+// outside the operands' descriptors (they read as 0), behind the end of another
+// split they are the next one's first R - 1 tiles, which it reads too (a third more
+// bytes for 16 x 1001 x 8192 in 8 splits, a tenth for 16 x 4096 x 4096 in 2).  The
+// barrier behind the loop waits for them before LDS is used again.
 //
 // For rows of two matrices (the gated block's forward product, where the plain
 // step's pair of tiles leaves a compute unit waiting for memory): us with the
