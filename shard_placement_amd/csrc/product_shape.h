@@ -172,11 +172,18 @@ inline bool past_the_cache(int64_t rows, int64_t depth) { return rows * depth > 
 // The same for a product with the rows of two matrices in turn (I: both), whose
 // 128-wide tiles are rings (tile_product.h; halves = 2).
 //
-// Up to 64 tokens: the contraction is split to about 128 workgroups and not below
-// 512 elements each.  Half of the compute units with rings read as fast as all of
+// Up to 64 tokens: the contraction is split to about 128 workgroups and into no more
+// splits than it has 512 elements.  (A split takes whole units of 256, so the last one
+// may be shorter, 8 elements of 1544 in three: us in 1, 2, 3 and 6 splits for 16 x 1001 x
+// 1544 10.1, 13.3, 12.7, 12.1; 264 of 4104 in six: 5 x 512 x 4104 in 2, 3, 6 16.6, 14.3,
+// 12.7.  Fewer splits for the sake of a longer last one are slower; 16 x 1001 x 1536 and
+// 30 x 600 x 1288 whole, 9.7 and 9.6, are faster than the two splits taken, 10.9 and
+// 10.7.)  Half of the compute units with rings read as fast as all of
 // them and leave fewer sums to join: us at 1, 2, 4 splits for 16 x 4096 x 4096 (64
 // tiles) 17.9, 17.4, 19.9; 5 x 1001 x 8192 (16 tiles) at 2, 4, 8 splits 20.8, 15.2,
-// 14.6; 5 x 768 x 2048 (12) at 1, 2, 4, 8 10.4, 10.3, 10.0, 10.6.  Of weights past the
+// 14.6; 5 x 768 x 2048 (12) at 1, 2, 4, 8 10.4, 10.3, 10.0, 10.6.  (The target was set
+// with weights that the cache holds.  Past it 32 to 127 tiles read too slowly whole: 4 x
+// 5120 x 13824, 80 tiles, 77 us where the weights' rows take 54.)  Of weights past the
 // cache with more tiles than compute units, up to 32 tokens read 512 bytes of a row
 // at a time instead (24 x 28672 x 8192 147.5 us, with rings 155; 24 x 13824 x 5120, 216
 // tiles, 45.4 with rings, 50.3 so).
