@@ -338,9 +338,13 @@ inline Gradients choose_gated_gradients(int64_t T, int64_t turn, int64_t K, bool
 // forward_by_rows says for one weight; rings leave less for it (us by rows / in
 // rings, N x K of each weight):
 //   2 tokens  128 x 512 5.4 / 6.6, 768 x 2048 6.8 / 10.5, 1024 x 8192 11.5 / 15.1,
-//             13824 x 5120 48.1 / 45.2, 14336 x 1024 24.8 / 13.5
+//             14336 x 1024 24.8 / 13.5; of weights past the cache 13824 x 5120 48 / 45,
+//             16384 x 4608 51 / 47, 15000 x 5000 51 / 61, 11008 x 6144 44 / 57, 16000 x
+//             8192 81 / 98, 5120 x 13824 49 / 77: rows, which lose up to 9% where the
+//             rings' tiles fill the compute units once and win up to a third elsewhere
 //   3         13824 x 5120 59.6 / 45.1, 28672 x 4096 94.5 / 78.7, 28672 x 8192 144.4 /
-//             146.3, and 1024 x 8192 in rings 14.3
+//             146.3, 1024 x 8192 16.0 / 14.3; 5120 x 13824 53 / 77, 8192 x 28672 145 / 183:
+//             rings, though long rows of few outputs are faster read by rows
 // direct: both weights can be read where they lie.  x, where it cannot, is a few rows
 // to copy (4 tokens 512 x 512 10.0 / 7.6, 768 x 2048 10.8 / 12.5, 8192 x 1024 24.4 /
 // 11.6, 4096 x 4096 20.5 / 23.3, 13824 x 5120 58.6 / 46.5).
