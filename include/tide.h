@@ -601,7 +601,8 @@ tide_status tide_linear_backward(const tide_linear_backward_args *args, void *wo
  *           may what only they need (weight for dx; x for dx and dweight).
  *
  * Squares and their sums have to stay within binary32: a row whose sum of
- * squares does not (|x| of 10^17 and more) is divided by infinity.  A row with a
+ * squares does not (|x| of 10^17 and more) is divided by infinity, and is NaN if
+ * the sum of x (TIDE_NORM_LAYER) or of dy weight x (backward) leaves it too.  A row with a
  * NaN or, but for the finite elements of TIDE_NORM_RMS (0), an infinity is NaN.
  * eps is finite and at least 1e-30 (TIDE_EINVAL otherwise).
  *
@@ -674,7 +675,8 @@ tide_status tide_norm_backward(const tide_norm_backward_args *args, void *worksp
  * act as for the layer products, and so are the limits, with 2 N in the place
  * of N, the checks of overlap, empty sizes, workspaces and streams.  act of a g
  * that is minus infinity is NaN forward, but for relu (0); a finite g that
- * reads back as infinity has the value and slope of its limit. */
+ * reads back as infinity has the value and slope of its limit, a finite u is then
+ * infinity (times a slope of 0: NaN). */
 typedef struct tide_gated_forward_args {
     int64_t tokens, out_features, in_features; /* T, N, K */
     int32_t act;                               /* TIDE_ACT_* */

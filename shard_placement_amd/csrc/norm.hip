@@ -188,7 +188,7 @@ __device__ __forceinline__ void centre(float (&v)[8], float mu, uint32_t c, uint
 // their sum, be the mean large next to them or small.  (Differences from the mean in
 // binary32 are rounded, equal ones alike, and what their sum shows is those roundings:
 // n of elements near the mean was off by up to 4%, and 449 of 210 million y of 4096 x
-// 5120 fell to the other side of a border in 8 bits, now 139, in the plain form 128.)
+// 5120 fell to the other side of a border in 8 bits, now 136, in the plain form 128.)
 // Rounded to nearest, the mean of a row of one value is that value.
 __device__ __forceinline__ float first_bits(float mean) {
     return __uint_as_float((uint32_t)to_bf16(mean) << 16);
@@ -208,7 +208,10 @@ __device__ __forceinline__ float variance(float mean_square, float off) {
     return fmaxf(__builtin_fmaf(-off, off, mean_square), 0.0f * mean_square);
 }
 
-// Within one step of 1 / sqrt(v).
+// Within 0.87 of a step of 1 / sqrt(v), one in nine not the nearest number.  Rounded
+// correctly, by one more step of Newton's, it is no nearer in what comes of it: of ten
+// times 4096 x 8192 y in 8 bits 255 are on another side of a border than in 64 bits, 236
+// so, 240 in the plain form.
 __device__ __forceinline__ float inv_sqrt(float v) { return __builtin_amdgcn_rsqf(v); }
 
 // ---- forward -------------------------------------------------------------------
@@ -415,9 +418,9 @@ __global__ __launch_bounds__(L > kThreads ? L : kThreads) void norm_backward_ker
     int slot = 0;
 #pragma unroll 1
     for (; row < p.rows; row += stride) {
-        // Fetching a loop of 11 KB for waves in step costs more at some places in
-        // memory than at others: 8192 rows of 5120 with layer norm and a bias took 62 to
-        // 77 us with the loop's start moved by a few instructions, 59.5 on 64 bytes.
+        // A loop of 11 KB for waves in step takes longer at some places in memory than at
+        // others: 8192 rows of 5120 with layer norm and a bias took 62 to 77 us with the
+        // loop's start moved by a few instructions, 59.5 on 64 bytes.
         if constexpr (LAYER && L > 64 && U == 1) asm volatile(".p2align 6" ::: "memory");
         RowParts<U> now;
         if constexpr (kAhead)
@@ -667,8 +670,12 @@ const ForwardForm kForwardForms[] = {
 // One unit a lane as far as 1024 lanes go, which keeps what the lane holds of the
 // weight, the sums and the next row in few registers: us for 8192 rows of 5120 with
 // rms and 640 lanes 56 (295 MB, 5.3 TB/s), with 256 lanes of 3 units 76.  Past 16384
-// columns 512 lanes have the registers that 1024 have not: 2300 rows of 28672 118
-// with 7 units, with 1024 lanes of 4 178.
+// columns 512 lanes have the registers that 1024 have not (us with 512 lanes / with
+// 1024 of 3 and 4 units, 2300 x 24576, 2300 x 28672 and 2000 x 32768): layer norm 82 / 94,
+// 129 / 146, 132 / 162; with a bias 120 / 135, 151 / 243, 178 / 247, though with 7 units 9
+// registers and with 8 units 57 of 256 are spilled to memory there (of 1024 lanes 34 and
+// 96 of 128); rms 76 / 85, 110 / 103, 113 / 102, whose widest rows would be 7 to 10% faster
+// the other way: one list serves all four.
 const BackwardForm kBackwardForms[] = {
     TIDE_BACKWARD_FORM(16, 1),   TIDE_BACKWARD_FORM(64, 1),  TIDE_BACKWARD_FORM(64, 2),
     TIDE_BACKWARD_FORM(1024, 1), TIDE_BACKWARD_FORM(1024, 2), TIDE_BACKWARD_FORM(512, 5),
@@ -683,9 +690,9 @@ const Form& form_of(const Form (&forms)[N], int64_t cols) {
 }
 
 // Threads of a workgroup: of wide rows, whole waves that hold one.  (Lanes that
-// hold nothing work all the same, and layer norm is bound by its arithmetic, 87% of
-// the cycles: 8192 rows of 5120 took 84 us with 1024 lanes, 76 with 640, 63 as the
-// loop is now.)
+// hold nothing work all the same: 8192 rows of 5120 with layer norm took 84 us with
+// 1024 lanes, 76 with 640, 60 as the loop is now.  Its vector pipes are busy 56% of the
+// time, 30% for 777 rows; the rest the waves of a row wait for each other, twice a row.)
 int threads_of(const RowShape& s, int64_t cols) {
     return s.lanes <= 64 ? kThreads : (int)round_up(ceil_div(act8_pitch(cols) / 8, s.units), 64);
 }
@@ -697,8 +704,9 @@ int64_t rows_of(const RowShape& s) { return s.lanes <= 64 ? kThreads / s.lanes :
 // launch reads, so wide rows take no more than the compute units: us at 256 and
 // 512 workgroups for 2300 x 28672 with rms 112 and 125, 8192 x 8192 73 and 78, 512 x
 // 4096 11.2 and 12.1.  Narrower ones take twice as many: 8192 x 2048 39.9 and 29.5
-// (1024: 29.3), 65536 x 128 23.3 and 19.2 (1024: 17.9; one number for all narrow rows).
-// So does layer norm, whose arithmetic leaves memory waiting, where two of its
+// (1024: 29.3), 65536 x 128 23.3 and 19.2 (1024: 17.9, which is not taken: one number
+// serves all narrow rows).
+// So does layer norm, whose waves wait for each other twice a row, where two of its
 // workgroups fit a compute unit's registers: 8192 rows of 4096 with a bias 54 and 47,
 // without 53 and 44, of 5120 without 71 and 57, of 6144 without 75 and 64; of 5120 with
 // a bias, whose 10 waves of 85 registers do not fit twice, 59.5 and 65, of 7168 without
