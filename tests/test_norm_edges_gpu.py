@@ -1,11 +1,12 @@
 """GPU tests of the norms where binary32 ends: elements that lie near their
-row's mean, and rows whose squares pass binary32."""
+row's mean, rows whose squares pass binary32, and many wide rows."""
 import pytest
 import torch
 
 from shard_placement_amd import api
 from shard_placement_amd.linear import Act8
 from shard_placement_amd.norm import Norm
+from tests import norm_ref as ref
 from tests.test_linear_gpu import BF, DEV, gen, normal, within
 
 pytestmark = pytest.mark.gpu
@@ -93,3 +94,19 @@ def test_rows_whose_squares_pass_binary32(kind, C, size):
         assert torch.equal(dx[rest], layer.backward(dy[rest], small, add=add[rest]))
         # the same terms, added in another order: binary32, then a step of bf16 at most
         torch.testing.assert_close(dw, layer.weight_grad, rtol=2.0 ** -7, atol=1e-5)
+
+
+@pytest.mark.parametrize("T,C", [(2047, 4096), (2048, 4096), (2100, 2056), (2500, 5120), (2049, 6144), (2049, 6152)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_many_wide_rows(T, C, bias):
+    """Both sides of the number of workgroups that layer norm's gradients take."""
+    g = gen(T + C)
+    x, w, dy, add = normal(g, T, C), normal(g, C), normal(g, T, C, scale=1e-2), normal(g, T, C)
+    layer = Norm(w, bias=w if bias else None, kind="layer", eps=1e-5, weight_grad=torch.empty_like(w),
+                 bias_grad=torch.empty_like(w) if bias else None)
+    dx = layer.backward(dy, x, add=add)
+    want = ref.backward_ref(dy, w, x, add, "layer", 1e-5)
+    within(dx, *want["dx"], "dx")
+    within(layer.weight_grad, *want["dw"], "dw")
+    if bias:
+        within(layer.bias_grad, *want["db"], "db")
