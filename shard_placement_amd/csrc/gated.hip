@@ -140,6 +140,7 @@ struct DguArgs {
 template <int ACT, bool WHOLE>
 __device__ __forceinline__ void dgu_lane(const DguArgs& p, int64_t c, int64_t t0, int64_t t1,
                                          float (&sum_g)[8], float (&sum_u)[8]) {
+    constexpr float kHalf = ACT == TIDE_ACT_NONE || ACT == TIDE_ACT_RELU ? 1.0f : 0.5f;
     const int64_t pitch = act8_pitch(p.N), scales = p.T * pitch;
 #pragma unroll 1
     for (int64_t t = t0; t < t1; ++t) {
@@ -160,9 +161,9 @@ __device__ __forceinline__ void dgu_lane(const DguArgs& p, int64_t c, int64_t t0
         for (int k = 0; k < 8; ++k) {
             float slope;
             const float value = act_both<ACT>(g[k], &slope);
-            // dg; a slope passes 1 by little, so u slope stays within binary32, which
-            // dh u may leave where dg does not (a slope of 0 would be NaN)
-            u[k] = d[k] * (u[k] * slope);
+            // dg.  dh u may leave binary32 where dg does not (a slope of 0 would be NaN);
+            // u times half the slope, which stays below 1, never does
+            u[k] = d[k] * (u[k] * (kHalf * slope)) * (1.0f / kHalf);
             g[k] = d[k] * value;  // du
         }
         if constexpr (!WHOLE) {

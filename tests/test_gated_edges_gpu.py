@@ -38,6 +38,22 @@ def test_a_small_slope_of_large_factors(act, gate, sign):
     within(dbg, want.sum(0), off * want.sum(0).abs(), "dbg")
 
 
+@pytest.mark.parametrize("act,gate", [("silu", 2.5), ("gelu", 1.375), ("gelu_tanh", 1.375), ("relu", 1.0), ("none", 1.0)])
+def test_the_largest_factor(act, gate):
+    """u near binary32's end and a slope past 1: dg is finite where a small dh makes
+    it so."""
+    T, N = 3, 33
+    fill = lambda v, dt=torch.float64: torch.full((T, N), v, dtype=dt, device=DEV)  # noqa: E731
+    g8, gv = kept_of(fill(gate))
+    u8, uv = kept_of(fill(240 * 2.0 ** 120))
+    assert act in ("relu", "none") or (lref.slope_ref(gv, act) * uv > 2.0 ** 128).all()
+    dh = fill(2.0 ** -20, BF)
+    eye = torch.eye(N, dtype=BF, device=DEV)
+    dg = Gated(eye, torch.zeros_like(eye), act=act).backward(dh, g=g8, u=u8)
+    want = dh.double() * uv * lref.slope_ref(gv, act)
+    within(dg, want, (2.0 ** -16 + 2 * lref.BF16) * want.abs(), "dg")
+
+
 @pytest.mark.parametrize("T,N,K", [(2, 2305, 264), (3, 4096, 512), (3, 40, 64), (4, 300, 2056), (4, 1001, 8)])
 @pytest.mark.parametrize("shift,more", [(1, 0), (0, 3), (5, 8)])
 def test_few_tokens_on_any_element(T, N, K, shift, more):

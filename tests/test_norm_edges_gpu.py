@@ -96,6 +96,29 @@ def test_rows_whose_squares_pass_binary32(kind, C, size):
         torch.testing.assert_close(dw, layer.weight_grad, rtol=2.0 ** -7, atol=1e-5)
 
 
+@pytest.mark.parametrize("C", [40, 513, 1001, 5120, 12296, 28672])
+def test_rows_of_two_neighbouring_values(C):
+    """Spreads of a step of bf16 around means of any size, in all proportions: what
+    the mean's first bits leave of it is as large as the spread."""
+    g = gen(C)
+    low = torch.tensor([1.0, 255.0, -256.0, 1000.0, 3.296875, -2.0 ** -20, 2.0 ** 30, 1.9921875], device=DEV).to(BF)
+    high = (low.view(torch.int16) + 1).view(BF)
+    share = torch.tensor([1 / C, 0.25, 0.5, 0.75, 1 - 1 / C], device=DEV)
+    pick = torch.rand(len(low), len(share), C, generator=g, device=DEV) < share[:, None]
+    pick[:, 0], pick[:, 4] = False, True
+    pick[:, 0, 7], pick[:, 4, C - 1] = True, False
+    x = torch.where(pick, high[:, None, None], low[:, None, None]).reshape(-1, C)
+    T = x.shape[0]
+    w, b, dy, add = normal(g, C), normal(g, C), normal(g, T, C), normal(g, T, C)
+    layer = Norm(w, bias=b, kind="layer", eps=1e-12, weight_grad=torch.empty_like(w))
+    want, err = ref.forward_ref(x, w, b, "layer", 1e-12)
+    within(layer.forward(x), want, ref.rounded(want, err), "y")
+    dx = layer.backward(dy, x, add=add)
+    want = ref.backward_ref(dy, w, x, add, "layer", 1e-12)
+    within(dx, *want["dx"], "dx")
+    within(layer.weight_grad, *want["dw"], "dw")
+
+
 @pytest.mark.parametrize("T,C", [(2047, 4096), (2048, 4096), (2100, 2056), (2500, 5120), (2049, 6144), (2049, 6152)])
 @pytest.mark.parametrize("bias", [False, True])
 def test_many_wide_rows(T, C, bias):
